@@ -15,6 +15,9 @@ _BINDING_NAMES = (
     "ep_get_layout_static_scratch", "ep_dispatch_expanded", "ep_combine_expanded",
     "ep_expanded_capacity_bound", "ep_combine_topk_weights", "ep_accumulate_expert_stats",
     "ep_bounds_checked", "EP_BF16", "EP_FP8_E4M3",
+    "ep_expert_gemm", "ep_expert_gemm_backward", "ep_expert_gemm_backward_workspace_bytes",
+    "ep_moe_few_tokens", "ep_moe_few_tokens_workspace_bytes", "EP_ACT_NONE", "EP_ACT_RELU", "EP_ACT_GELU",
+    "EP_ACT_SILU", "EP_ACT_SWIGLU",
 )
 
 

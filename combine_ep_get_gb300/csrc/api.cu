@@ -13,6 +13,7 @@
 #include <string>
 
 #include "ep_internal.cuh"
+#include "experts.cuh"
 
 namespace epg {
 
@@ -723,6 +724,172 @@ ep_status_t ep_accumulate_expert_stats(const ep_layout_t* layout, int E, int64_t
                                                static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
                ? EP_OK
                : EP_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks shared by ep_expert_gemm and its backward call.
+ep_status_t check_experts(int64_t num_rows, int K, int N, int E, int act, const int32_t* offset,
+                          const int32_t* counts, const int32_t* d_status) {
+    if (!d_status || num_rows < 0 || K < 1 || N < 1 || E < 1) return EP_RET(EP_ERR_INVALID_ARG);
+    if (act < EP_ACT_NONE || act > EP_ACT_SWIGLU) return EP_RET(EP_ERR_INVALID_ARG);
+    if (E > EP_MAX_EXPERTS || num_rows > INT32_MAX || K > epg::kMaxExpertDim || N > epg::kMaxExpertDim)
+        return EP_RET(EP_ERR_UNSUPPORTED);
+    if (K % 8 != 0 || N % 8 != 0 || !ok_ptr(offset) || !ok_ptr(counts)) return EP_RET(EP_ERR_INVALID_ARG);
+    return EP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ep_status_t ep_expert_gemm(const void* x, const float* x_sf, int sf_col_major, const void* w, const float* w_sf,
+                           int in_dtype, const float* bias, int activation, const float* row_weight,
+                           const void* residual, int64_t num_rows, int K, int N, int E,
+                           const int32_t* expert_offset, const int32_t* num_tokens_per_expert, void* y, void* z,
+                           int32_t* d_status, void* cuda_stream) {
+    EP_DEBUG("ep_expert_gemm: rows=%lld K=%d N=%d E=%d %s act=%d%s%s%s%s", static_cast<long long>(num_rows), K, N, E,
+             in_dtype == EP_FP8_E4M3 ? "fp8" : "bf16", activation, bias ? " bias" : "",
+             row_weight ? " row_weight" : "", residual ? " residual" : "", z ? " z" : "");
+    ep_status_t s = check_experts(num_rows, K, N, E, activation, expert_offset, num_tokens_per_expert, d_status);
+    if (s != EP_OK) return s;
+    const bool fp8 = in_dtype == EP_FP8_E4M3;
+    if (in_dtype != EP_BF16 && !fp8) return EP_RET(EP_ERR_INVALID_ARG);
+    if (fp8 && (K % 128 != 0 || N % 128 != 0)) return EP_RET(EP_ERR_INVALID_ARG);
+    if (!aligned16(bias) || !aligned16(row_weight) || !aligned16(residual) || !aligned16(z))
+        return EP_RET(EP_ERR_INVALID_ARG);
+    if (!ok_ptr(w) || (fp8 && !ok_ptr(w_sf))) return EP_RET(EP_ERR_INVALID_ARG);
+    if (num_rows > 0 && (!ok_ptr(x) || !ok_ptr(y) || (fp8 && !ok_ptr(x_sf)))) return EP_RET(EP_ERR_INVALID_ARG);
+    if (num_rows == 0) return EP_OK;
+
+    epg::ExpertGemmParams p{};
+    p.x = static_cast<const uint8_t*>(x);
+    p.x_sf = x_sf;
+    p.sf_row = sf_col_major ? 1 : K / 128;
+    p.sf_block = sf_col_major ? (num_rows + 3) / 4 * 4 : 1;
+    p.w = static_cast<const uint8_t*>(w);
+    p.w_sf = w_sf;
+    p.bias = bias;
+    p.row_weight = row_weight;
+    p.residual = static_cast<const __nv_bfloat16*>(residual);
+    p.rows = num_rows;
+    p.K = K;
+    p.N = N;
+    p.Nw = activation == EP_ACT_SWIGLU ? 2 * N : N;
+    p.E = E;
+    p.act = activation;
+    p.expert_offset = expert_offset;
+    p.counts = num_tokens_per_expert;
+    p.y = static_cast<__nv_bfloat16*>(y);
+    p.z = static_cast<__nv_bfloat16*>(z);
+    p.status = d_status;
+    return epg::launch_expert_gemm(p, fp8, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
+               ? EP_OK
+               : EP_RET(EP_ERR_CUDA);
+}
+
+size_t ep_expert_gemm_backward_workspace_bytes(int64_t num_rows, int n_dim, int num_experts, int activation) {
+    if (num_rows < 0 || n_dim < 1 || num_experts < 1) return 16;
+    return epg::backward_workspace(num_rows, activation == EP_ACT_SWIGLU ? 2 * n_dim : n_dim, num_experts).total;
+}
+
+ep_status_t ep_expert_gemm_backward(const void* dy, const void* x, const void* w, const void* z, int activation,
+                                    const float* row_weight, int64_t num_rows, int K, int N, int E,
+                                    const int32_t* expert_offset, const int32_t* num_tokens_per_expert, void* dx,
+                                    void* dw, float* dbias, float* d_row_weight, void* workspace, size_t ws_bytes,
+                                    int32_t* d_status, void* cuda_stream) {
+    EP_DEBUG("ep_expert_gemm_backward: rows=%lld K=%d N=%d E=%d act=%d%s%s%s%s%s", static_cast<long long>(num_rows),
+             K, N, E, activation, row_weight ? " row_weight" : "", dx ? " dx" : "", dw ? " dw" : "",
+             dbias ? " dbias" : "", d_row_weight ? " d_row_weight" : "");
+    ep_status_t s = check_experts(num_rows, K, N, E, activation, expert_offset, num_tokens_per_expert, d_status);
+    if (s != EP_OK) return s;
+    if (!aligned16(row_weight) || !aligned16(dx) || !aligned16(dw) || !aligned16(dbias) || !aligned16(d_row_weight) ||
+        !aligned16(x) || !aligned16(w) || !aligned16(z) || !aligned16(dy))
+        return EP_RET(EP_ERR_INVALID_ARG);
+    const int Nw = activation == EP_ACT_SWIGLU ? 2 * N : N;
+    if (num_rows > 0 && (!dy || (dx && !w) || (dw && !x))) return EP_RET(EP_ERR_INVALID_ARG);
+    if (num_rows > 0 && !z && (activation != EP_ACT_NONE || d_row_weight)) return EP_RET(EP_ERR_INVALID_ARG);
+    const epg::BackwardWorkspace b = epg::backward_workspace(num_rows, Nw, E);
+    if (!ok_ptr(workspace) || ws_bytes < b.total) return EP_RET(EP_ERR_INVALID_ARG);
+
+    epg::ExpertBackwardParams p{};
+    p.dy = static_cast<const __nv_bfloat16*>(dy);
+    p.x = static_cast<const __nv_bfloat16*>(x);
+    p.w = static_cast<const __nv_bfloat16*>(w);
+    p.z = static_cast<const __nv_bfloat16*>(z);
+    p.row_weight = row_weight;
+    p.rows = num_rows;
+    p.K = K;
+    p.N = N;
+    p.Nw = Nw;
+    p.E = E;
+    p.act = activation;
+    p.expert_offset = expert_offset;
+    p.counts = num_tokens_per_expert;
+    p.dx = num_rows > 0 ? static_cast<__nv_bfloat16*>(dx) : nullptr;
+    p.dw = static_cast<__nv_bfloat16*>(dw);
+    p.dbias = dbias;
+    p.d_row_weight = num_rows > 0 ? d_row_weight : nullptr;
+    char* ws = static_cast<char*>(workspace);
+    p.dz = reinterpret_cast<__nv_bfloat16*>(ws + b.off_dz);
+    p.bias_part = reinterpret_cast<float*>(ws + b.off_part);
+    p.status = d_status;
+    return epg::launch_expert_backward(p, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
+               ? EP_OK
+               : EP_RET(EP_ERR_CUDA);
+}
+
+size_t ep_moe_few_tokens_workspace_bytes(int num_tokens, int num_topk, int hidden, int inner, int num_experts) {
+    (void)num_experts;
+    if (num_tokens < 0 || num_topk < 1 || hidden < 1 || inner < 1) return 16;
+    return epg::few_workspace(num_tokens, num_topk, hidden, inner).total;
+}
+
+ep_status_t ep_moe_few_tokens(const void* x, const int64_t* topk_idx, const float* topk_weights, const void* w_up,
+                              const float* bias_up, int activation, const void* w_down, const float* bias_down,
+                              const void* residual, int T, int H, int I, int K, int E, void* workspace,
+                              size_t ws_bytes, void* out, int32_t* d_status, void* cuda_stream) {
+    EP_DEBUG("ep_moe_few_tokens: T=%d H=%d I=%d K=%d E=%d act=%d%s%s%s", T, H, I, K, E, activation,
+             bias_up ? " bias_up" : "", bias_down ? " bias_down" : "", residual ? " residual" : "");
+    if (!d_status || T < 0 || H < 1 || I < 1 || K < 1 || E < 1) return EP_RET(EP_ERR_INVALID_ARG);
+    if (activation < EP_ACT_NONE || activation > EP_ACT_SWIGLU) return EP_RET(EP_ERR_INVALID_ARG);
+    if (T > EP_FEW_MAX_TOKENS || K > EP_FEW_MAX_TOPK || E > EP_MAX_EXPERTS || H > epg::kMaxExpertDim ||
+        I > epg::kMaxExpertDim)
+        return EP_RET(EP_ERR_UNSUPPORTED);
+    if (H % 8 != 0 || I % 8 != 0) return EP_RET(EP_ERR_INVALID_ARG);
+    if (!ok_ptr(w_up) || !ok_ptr(w_down) || !aligned16(bias_up) || !aligned16(bias_down) || !aligned16(residual))
+        return EP_RET(EP_ERR_INVALID_ARG);
+    if (T > 0 && (!ok_ptr(x) || !ok_ptr(topk_idx) || !ok_ptr(topk_weights) || !ok_ptr(out)))
+        return EP_RET(EP_ERR_INVALID_ARG);
+    const epg::FewWorkspace f = epg::few_workspace(T, K, H, I);
+    if (!ok_ptr(workspace) || ws_bytes < f.total) return EP_RET(EP_ERR_INVALID_ARG);
+    if (T == 0) return EP_OK;
+
+    epg::FewTokensParams p{};
+    p.x = static_cast<const __nv_bfloat16*>(x);
+    p.topk_idx = topk_idx;
+    p.topk_weights = topk_weights;
+    p.w_up = static_cast<const __nv_bfloat16*>(w_up);
+    p.bias_up = bias_up;
+    p.w_down = static_cast<const __nv_bfloat16*>(w_down);
+    p.bias_down = bias_down;
+    p.residual = static_cast<const __nv_bfloat16*>(residual);
+    p.T = T;
+    p.H = H;
+    p.I = I;
+    p.Nw = activation == EP_ACT_SWIGLU ? 2 * I : I;
+    p.K = K;
+    p.E = E;
+    p.act = activation;
+    char* ws = static_cast<char*>(workspace);
+    p.h = reinterpret_cast<__nv_bfloat16*>(ws + f.off_h);
+    p.part = reinterpret_cast<float*>(ws + f.off_part);
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.status = d_status;
+    return epg::launch_few_tokens(p, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? EP_OK
+                                                                                           : EP_RET(EP_ERR_CUDA);
 }
 
 const char* ep_status_string(int32_t status) {

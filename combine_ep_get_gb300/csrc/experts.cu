@@ -1,0 +1,269 @@
+// The experts between dispatch and combine: matrix product with its epilogue,
+// its gradients, and the whole layer for a few tokens (the contract is in
+// include/ep_get.h).  Plain tiled kernels: 64 x 64 outputs a block, 16 terms
+// at a time through shared memory, fp32 multiply-adds.
+#include <cuda_fp8.h>
+
+#include "experts.cuh"
+
+namespace epg {
+namespace {
+
+constexpr int kT = 64, kD = 16;
+
+// acc[i][j] += sum over k < depth of a(m, k) * b(n, k), m = 4 * ty + i, n = 4 * tx + j
+template <class A, class B>
+__device__ __forceinline__ void tile_product(float (&acc)[4][4], int64_t depth, A a, B b) {
+    __shared__ float sa[kD][kT + 1], sb[kD][kT + 1];
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    for (int64_t k0 = 0; k0 < depth; k0 += kD) {
+        for (int i = tid; i < kT * kD; i += 256) {
+            const int r = i / kD, k = i % kD;
+            sa[k][r] = k0 + k < depth ? a(r, k0 + k) : 0.0f;
+            sb[k][r] = k0 + k < depth ? b(r, k0 + k) : 0.0f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kD; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][4 * ty + i], sb[k][4 * tx + j], acc[i][j]);
+        __syncthreads();
+    }
+}
+
+__device__ __forceinline__ float bf(const __nv_bfloat16* p, int64_t i) { return __bfloat162float(p[i]); }
+
+template <bool kFp8>
+__device__ __forceinline__ float load(const uint8_t* p, int64_t i) {
+    if (kFp8) {
+        __nv_fp8_e4m3 v;
+        v.__x = p[i];
+        return static_cast<float>(v);
+    }
+    return bf(reinterpret_cast<const __nv_bfloat16*>(p), i);
+}
+
+// grid (column tiles, E): every block walks its expert's row tiles
+template <bool kFp8>
+__global__ void __launch_bounds__(256) product_kernel(const __grid_constant__ ExpertGemmParams p) {
+    const int e = blockIdx.y, n0 = blockIdx.x * kT, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    int64_t first;
+    const int cnt = expert_rows(p.expert_offset, p.counts, e, p.rows, &first, p.status);
+    const bool gated = p.act == EP_ACT_SWIGLU;
+    for (int m0 = 0; m0 < cnt; m0 += kT) {
+        float acc[2][4][4] = {};
+        const auto a = [&](int r, int64_t k) {
+            if (m0 + r >= cnt) return 0.0f;
+            const int64_t d = first + m0 + r;
+            const float v = load<kFp8>(p.x, d * p.K + k);
+            return kFp8 ? v * p.x_sf[d * p.sf_row + k / 128 * p.sf_block] : v;
+        };
+        for (int half = 0; half < (gated ? 2 : 1); ++half)
+            tile_product(acc[half], p.K, a, [&](int c, int64_t k) {
+                if (n0 + c >= p.N) return 0.0f;
+                const int64_t n = half * p.N + n0 + c;
+                const float v = load<kFp8>(p.w, (static_cast<int64_t>(e) * p.Nw + n) * p.K + k);
+                return kFp8 ? v * p.w_sf[(e * (p.Nw / 128) + n / 128) * (p.K / 128) + k / 128] : v;
+            });
+        for (int i = 0; i < 4; ++i)
+            for (int j = 0; j < 4; ++j) {
+                const int r = m0 + 4 * ty + i, n = n0 + 4 * tx + j;
+                if (r >= cnt || n >= p.N) continue;
+                const int64_t d = first + r;
+                float z[2] = {acc[0][i][j], acc[1][i][j]};
+                for (int half = 0; half < (gated ? 2 : 1); ++half) {
+                    if (p.bias) z[half] += p.bias[static_cast<int64_t>(e) * p.Nw + half * p.N + n];
+                    if (p.z) p.z[d * p.Nw + half * p.N + n] = __float2bfloat16(z[half]);
+                }
+                float v = gated ? silu(z[0]) * z[1] : activate(z[0], p.act);
+                if (p.row_weight) v *= p.row_weight[d];
+                if (p.residual) v += bf(p.residual, d * p.N + n);
+                p.y[d * p.N + n] = __float2bfloat16(v);
+            }
+    }
+}
+
+// grid (column tiles, E): dz, its column sums, and the row weights' gradient
+// (by the blocks of the first column tile, which walk all columns)
+__global__ void __launch_bounds__(256) activation_backward_kernel(const __grid_constant__ ExpertBackwardParams p) {
+    const int e = blockIdx.y;
+    int64_t first;
+    const int cnt = expert_rows(p.expert_offset, p.counts, e, p.rows, &first, p.status);
+    const bool gated = p.act == EP_ACT_SWIGLU;
+    const int n = blockIdx.x * 256 + threadIdx.x;
+    if (n < p.N) {
+        float sum[2] = {0.0f, 0.0f};
+        for (int r = 0; r < cnt; ++r) {
+            const int64_t d = first + r;
+            const float da = bf(p.dy, d * p.N + n) * (p.row_weight ? p.row_weight[d] : 1.0f);
+            const float z0 = p.act != EP_ACT_NONE ? bf(p.z, d * p.Nw + n) : 0.0f;
+            if (gated) {
+                const float up = bf(p.z, d * p.Nw + p.N + n);
+                const float g = da * up * silu_slope(z0), u = da * silu(z0);
+                sum[0] += g;
+                sum[1] += u;
+                p.dz[d * p.Nw + n] = __float2bfloat16(g);
+                p.dz[d * p.Nw + p.N + n] = __float2bfloat16(u);
+            } else {
+                const float g = da * activate_slope(z0, p.act);
+                sum[0] += g;
+                p.dz[d * p.Nw + n] = __float2bfloat16(g);
+            }
+        }
+        if (p.dbias) {
+            p.dbias[static_cast<int64_t>(e) * p.Nw + n] = sum[0];
+            if (gated) p.dbias[static_cast<int64_t>(e) * p.Nw + p.N + n] = sum[1];
+        }
+    }
+    if (p.d_row_weight && blockIdx.x == 0)
+        for (int r = threadIdx.x / 32; r < cnt; r += 8) {
+            const int64_t d = first + r;
+            float s = 0.0f;
+            for (int c = threadIdx.x & 31; c < p.N; c += 32) {
+                const float z0 = bf(p.z, d * p.Nw + c);
+                s += bf(p.dy, d * p.N + c) *
+                     (gated ? silu(z0) * bf(p.z, d * p.Nw + p.N + c) : activate(z0, p.act));
+            }
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if ((threadIdx.x & 31) == 0) p.d_row_weight[d] = s;
+        }
+}
+
+// grid (column tiles of K, E)
+__global__ void __launch_bounds__(256) dx_kernel(const __grid_constant__ ExpertBackwardParams p) {
+    const int e = blockIdx.y, n0 = blockIdx.x * kT, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    int64_t first;
+    const int cnt = expert_rows(p.expert_offset, p.counts, e, p.rows, &first, p.status);
+    for (int m0 = 0; m0 < cnt; m0 += kT) {
+        float acc[4][4] = {};
+        tile_product(
+            acc, p.Nw, [&](int r, int64_t k) { return m0 + r < cnt ? bf(p.dz, (first + m0 + r) * p.Nw + k) : 0.0f; },
+            [&](int c, int64_t k) {
+                return n0 + c < p.K ? bf(p.w, (static_cast<int64_t>(e) * p.Nw + k) * p.K + n0 + c) : 0.0f;
+            });
+        for (int i = 0; i < 4; ++i)
+            for (int j = 0; j < 4; ++j) {
+                const int r = m0 + 4 * ty + i, n = n0 + 4 * tx + j;
+                if (r < cnt && n < p.K) p.dx[(first + r) * p.K + n] = __float2bfloat16(acc[i][j]);
+            }
+    }
+}
+
+// grid (column tiles of K, E, row tiles of Nw)
+__global__ void __launch_bounds__(256) dw_kernel(const __grid_constant__ ExpertBackwardParams p) {
+    const int e = blockIdx.y, n0 = blockIdx.x * kT, m0 = blockIdx.z * kT;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    int64_t first;
+    const int cnt = expert_rows(p.expert_offset, p.counts, e, p.rows, &first, p.status);
+    float acc[4][4] = {};
+    tile_product(
+        acc, cnt, [&](int r, int64_t k) { return m0 + r < p.Nw ? bf(p.dz, (first + k) * p.Nw + m0 + r) : 0.0f; },
+        [&](int c, int64_t k) { return n0 + c < p.K ? bf(p.x, (first + k) * p.K + n0 + c) : 0.0f; });
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 4; ++j) {
+            const int m = m0 + 4 * ty + i, n = n0 + 4 * tx + j;
+            if (m < p.Nw && n < p.K)
+                p.dw[(static_cast<int64_t>(e) * p.Nw + m) * p.K + n] = __float2bfloat16(acc[i][j]);
+        }
+}
+
+// The block's entries (t, k) that name expert e, ascending; returns how many.
+__device__ int entries_of(const FewTokensParams& p, int e, int16_t* list) {
+    __shared__ int n;
+    if (threadIdx.x < 32) {
+        int found = 0;
+        for (int i0 = 0; i0 < p.T * p.K; i0 += 32) {
+            const int i = i0 + threadIdx.x;
+            const int64_t v = i < p.T * p.K ? p.topk_idx[i] : -1;
+            if ((v < -1 || v >= p.E) && blockIdx.x == 0 && e == 0) atomicOr(p.status, EP_ERR_INVALID_INDEX);
+            const unsigned m = __ballot_sync(0xffffffffu, v == e);
+            if (v == e) list[found + __popc(m & ((1u << threadIdx.x) - 1))] = static_cast<int16_t>(i);
+            found += __popc(m);
+        }
+        if (threadIdx.x == 0) n = found;
+    }
+    __syncthreads();
+    return n;
+}
+
+// grid (column tiles, E)
+template <bool kUp>
+__global__ void __launch_bounds__(256) few_kernel(const __grid_constant__ FewTokensParams p) {
+    __shared__ int16_t list[EP_FEW_MAX_TOKENS * EP_FEW_MAX_TOPK];
+    const int e = blockIdx.y, n0 = blockIdx.x * kT, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int cnt = entries_of(p, e, list);
+    const bool gated = kUp && p.act == EP_ACT_SWIGLU;
+    const int N = kUp ? p.I : p.H, Nw = kUp ? p.Nw : p.H, depth = kUp ? p.H : p.I;
+    const __nv_bfloat16* w = kUp ? p.w_up : p.w_down;
+    const float* bias = kUp ? p.bias_up : p.bias_down;
+    for (int m0 = 0; m0 < cnt; m0 += kT) {
+        float acc[2][4][4] = {};
+        for (int half = 0; half < (gated ? 2 : 1); ++half)
+            tile_product(
+                acc[half], depth,
+                [&](int r, int64_t k) {
+                    if (m0 + r >= cnt) return 0.0f;
+                    const int i = list[m0 + r];
+                    return kUp ? bf(p.x, static_cast<int64_t>(i / p.K) * p.H + k)
+                               : bf(p.h, static_cast<int64_t>(i) * p.I + k);
+                },
+                [&](int c, int64_t k) {
+                    return n0 + c < N ? bf(w, (static_cast<int64_t>(e) * Nw + half * N + n0 + c) * depth + k) : 0.0f;
+                });
+        for (int i = 0; i < 4; ++i)
+            for (int j = 0; j < 4; ++j) {
+                const int r = m0 + 4 * ty + i, n = n0 + 4 * tx + j;
+                if (r >= cnt || n >= N) continue;
+                float z[2] = {acc[0][i][j], acc[1][i][j]};
+                for (int half = 0; half < (gated ? 2 : 1); ++half)
+                    if (bias) z[half] += bias[static_cast<int64_t>(e) * Nw + half * N + n];
+                const int64_t at = static_cast<int64_t>(list[r]) * N + n;
+                if (kUp)
+                    p.h[at] = __float2bfloat16(gated ? silu(z[0]) * z[1] : activate(z[0], p.act));
+                else
+                    p.part[at] = z[0];
+            }
+    }
+}
+
+// grid (column blocks, T)
+__global__ void __launch_bounds__(256) few_sum_kernel(const __grid_constant__ FewTokensParams p) {
+    const int t = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x;
+    if (n >= p.H) return;
+    float v = p.residual ? bf(p.residual, static_cast<int64_t>(t) * p.H + n) : 0.0f;
+    for (int k = 0; k < p.K; ++k) {
+        const int i = t * p.K + k;
+        const int64_t e = p.topk_idx[i];
+        if (e >= 0 && e < p.E) v = fmaf(p.topk_weights[i], p.part[static_cast<int64_t>(i) * p.H + n], v);
+    }
+    p.out[static_cast<int64_t>(t) * p.H + n] = __float2bfloat16(v);
+}
+
+}  // namespace
+
+cudaError_t launch_expert_gemm(const ExpertGemmParams& p, bool fp8, cudaStream_t stream) {
+    const dim3 grid((p.N + kT - 1) / kT, p.E);
+    if (fp8)
+        product_kernel<true><<<grid, 256, 0, stream>>>(p);
+    else
+        product_kernel<false><<<grid, 256, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_expert_backward(const ExpertBackwardParams& p, cudaStream_t stream) {
+    activation_backward_kernel<<<dim3((p.N + 255) / 256, p.E), 256, 0, stream>>>(p);
+    if (p.dx) dx_kernel<<<dim3((p.K + kT - 1) / kT, p.E), 256, 0, stream>>>(p);
+    if (p.dw) dw_kernel<<<dim3((p.K + kT - 1) / kT, p.E, (p.Nw + kT - 1) / kT), 256, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_few_tokens(const FewTokensParams& p, cudaStream_t stream) {
+    few_kernel<true><<<dim3((p.I + kT - 1) / kT, p.E), 256, 0, stream>>>(p);
+    few_kernel<false><<<dim3((p.H + kT - 1) / kT, p.E), 256, 0, stream>>>(p);
+    few_sum_kernel<<<dim3((p.H + 255) / 256, p.T), 256, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace epg

@@ -1,0 +1,137 @@
+// Parameter blocks and launchers of the experts' operators (experts*.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "ep_internal.cuh"
+
+namespace epg {
+
+constexpr int kMaxExpertDim = 1 << 20;
+
+struct ExpertGemmParams {
+    const uint8_t* x;            // [rows][K] bf16 or E4M3 codes
+    const float* x_sf;           // FP8: element (d, b) at d * sf_row + b * sf_block
+    int64_t sf_row, sf_block;
+    const uint8_t* w;            // [E][Nw][K]
+    const float* w_sf;           // FP8: [E][Nw / 128][K / 128]
+    const float* bias;           // [E][Nw] or null
+    const float* row_weight;     // [rows] or null
+    const __nv_bfloat16* residual;   // [rows][N] or null
+    int64_t rows;
+    int K, N, Nw, E, act;
+    const int32_t* expert_offset;    // [E]
+    const int32_t* counts;           // [E]
+    __nv_bfloat16* y;            // [rows][N]
+    __nv_bfloat16* z;            // [rows][Nw] or null
+    int32_t* status;
+};
+
+struct ExpertBackwardParams {
+    const __nv_bfloat16* dy;     // [rows][N]
+    const __nv_bfloat16* x;      // [rows][K]
+    const __nv_bfloat16* w;      // [E][Nw][K]
+    const __nv_bfloat16* z;      // [rows][Nw]
+    const float* row_weight;     // [rows] or null
+    int64_t rows;
+    int K, N, Nw, E, act;
+    const int32_t* expert_offset;
+    const int32_t* counts;
+    __nv_bfloat16* dx;           // [rows][K] or null
+    __nv_bfloat16* dw;           // [E][Nw][K] or null
+    float* dbias;                // [E][Nw] or null
+    float* d_row_weight;         // [rows] or null
+    __nv_bfloat16* dz;           // workspace [rows][Nw]
+    float* bias_part;            // workspace [row tiles][Nw]
+    int32_t* status;
+};
+
+struct FewTokensParams {
+    const __nv_bfloat16* x;      // [T][H]
+    const int64_t* topk_idx;     // [T][K]
+    const float* topk_weights;   // [T][K]
+    const __nv_bfloat16* w_up;   // [E][Nw][H]
+    const float* bias_up;        // [E][Nw] or null
+    const __nv_bfloat16* w_down; // [E][H][I]
+    const float* bias_down;      // [E][H] or null
+    const __nv_bfloat16* residual;   // [T][H] or null
+    int T, H, I, Nw, K, E, act;
+    __nv_bfloat16* h;            // workspace [T * K][I]
+    float* part;                 // workspace [T * K][H]
+    __nv_bfloat16* out;          // [T][H]
+    int32_t* status;
+};
+
+cudaError_t launch_expert_gemm(const ExpertGemmParams& p, bool fp8, cudaStream_t stream);
+cudaError_t launch_expert_backward(const ExpertBackwardParams& p, cudaStream_t stream);
+cudaError_t launch_few_tokens(const FewTokensParams& p, cudaStream_t stream);
+
+// Workspace carve-ups shared by the size queries and the calls.
+constexpr int kBackwardTileRows = 64;   // rows of one partial column sum of dz
+struct BackwardWorkspace {
+    size_t off_dz, off_part, total;
+};
+inline BackwardWorkspace backward_workspace(int64_t rows, int Nw, int E) {
+    const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+    const size_t tiles = static_cast<size_t>(rows) / kBackwardTileRows + E;
+    BackwardWorkspace b;
+    b.off_dz = 0;
+    b.off_part = up(static_cast<size_t>(rows) * Nw * 2);
+    b.total = b.off_part + up(tiles * Nw * 4) + 256;
+    return b;
+}
+struct FewWorkspace {
+    size_t off_h, off_part, total;
+};
+inline FewWorkspace few_workspace(int T, int K, int H, int I) {
+    const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+    FewWorkspace f;
+    f.off_h = 0;
+    f.off_part = up(static_cast<size_t>(T) * K * I * 2);
+    f.total = f.off_part + up(static_cast<size_t>(T) * K * H * 4) + 256;
+    return f;
+}
+
+// The activation of a pre-activation z (the gated one takes gate and up).
+__device__ __forceinline__ float silu(float z) { return z / (1.0f + expf(-z)); }
+__device__ __forceinline__ float activate(float z, int act) {
+    switch (act) {
+        case EP_ACT_RELU: return fmaxf(z, 0.0f);
+        case EP_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+        case EP_ACT_SILU: return silu(z);
+        default: return z;
+    }
+}
+// Its derivative.
+__device__ __forceinline__ float silu_slope(float z) {
+    const float s = 1.0f / (1.0f + expf(-z));
+    return s * (1.0f + z * (1.0f - s));
+}
+__device__ __forceinline__ float activate_slope(float z, int act) {
+    switch (act) {
+        case EP_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
+        case EP_ACT_GELU:
+            return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
+        case EP_ACT_SILU: return silu_slope(z);
+        default: return 1.0f;
+    }
+}
+
+// Rows of expert e that lie inside the arrays; the rest is skipped and flagged.
+__device__ __forceinline__ int expert_rows(const int32_t* offset, const int32_t* counts, int e, int64_t rows,
+                                           int64_t* first, int32_t* status) {
+    const int64_t o = offset[e], c = counts[e];
+    *first = o;
+    if (c <= 0) return 0;
+    if (o < 0 || o >= rows) {
+        atomicOr(status, EP_ERR_CAPACITY);
+        return 0;
+    }
+    if (o + c > rows) {
+        atomicOr(status, EP_ERR_CAPACITY);
+        return static_cast<int>(rows - o);
+    }
+    return static_cast<int>(c);
+}
+
+}  // namespace epg

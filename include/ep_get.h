@@ -345,6 +345,144 @@ ep_status_t ep_combine_expanded(const void* y, int64_t num_y_rows, const float* 
                                 int32_t* d_status, void* cuda_stream);
 
 /*
+ * The experts between dispatch and combine.  The pages leave the experts to
+ * the user; these calls compute them on the expanded receive rows, whose
+ * per-expert blocks are "the input of a grouped GEMM" above.
+ *
+ * Activations.  z is the product with its bias, act(z) what the call returns:
+ * NONE z; RELU max(z, 0); GELU z * Phi(z) (Phi the normal distribution
+ * function, by erf); SILU z / (1 + exp(-z)); SWIGLU silu(z[0 .. n)) * z[n .. 2n):
+ * the weights then have 2 * n_dim rows per expert, the gate's first.
+ */
+#define EP_ACT_NONE   0
+#define EP_ACT_RELU   1
+#define EP_ACT_GELU   2
+#define EP_ACT_SILU   3
+#define EP_ACT_SWIGLU 4
+
+/*
+ * Experts' matrix product, bias, activation, row weight and residual in its
+ * epilogue.  For every expert e and row d of its block,
+ * expert_offset[e] <= d < expert_offset[e] + num_tokens_per_expert[e]:
+ *   z[d]  = x[d] W[e]^T + bias[e]
+ *   y[d]  = bf16_rne( row_weight[d] * act(z[d]) + residual[d] )
+ * accumulated in fp32.  Rows in no block (padding) are neither read into a
+ * result nor written.
+ *
+ * x             [num_rows, k_dim]: bf16, or E4M3 codes with x_sf (as
+ *               ep_dispatch_expanded leaves them).
+ * w             [num_experts, n_w, k_dim] of x's type, n_w = n_dim, or 2 n_dim
+ *               for EP_ACT_SWIGLU.
+ * in_dtype      EP_BF16 (k_dim % 8 == 0, n_dim % 8 == 0) or EP_FP8_E4M3
+ *               (k_dim % 128 == 0, n_dim % 128 == 0).
+ * x_sf          FP8 only: the scale of row d's 128-channel block b at
+ *               d * (k_dim/128) + b, or, with sf_col_major, at
+ *               b * sf_stride + d, sf_stride = num_rows rounded up to 4.
+ * w_sf          FP8 only: fp32 [num_experts, n_w/128, k_dim/128], the scale of
+ *               each 128 x 128 block of w.
+ * bias          fp32 [num_experts, n_w] or NULL.
+ * row_weight    fp32 [num_rows] or NULL (= 1): ep_dispatch_expanded's
+ *               recv_weight here and an unweighted ep_combine_expanded give
+ *               the weighted combine.
+ * residual      bf16 [num_rows, n_dim] or NULL; may be y itself.
+ * expert_offset, num_tokens_per_expert
+ *               int32 [num_experts + 1] and [num_experts], as ep_get_layout
+ *               writes them (any offsets of disjoint blocks will do: one
+ *               expert of num_rows rows is a dense product).  Rows at or
+ *               beyond num_rows are skipped and set EP_ERR_CAPACITY.
+ * y             bf16 [num_rows, n_dim].
+ * z             bf16 [num_rows, n_w] or NULL: z[d] rounded, for
+ *               ep_expert_gemm_backward.
+ * Limits: num_experts <= EP_MAX_EXPERTS, num_rows <= 2^31 - 1, k_dim and
+ * n_dim <= 2^20 (beyond: EP_ERR_UNSUPPORTED).
+ */
+ep_status_t ep_expert_gemm(const void* x, const float* x_sf, int sf_col_major, const void* w,
+                           const float* w_sf, int in_dtype, const float* bias, int activation,
+                           const float* row_weight, const void* residual, int64_t num_rows, int k_dim,
+                           int n_dim, int num_experts, const int32_t* expert_offset,
+                           const int32_t* num_tokens_per_expert, void* y, void* z, int32_t* d_status,
+                           void* cuda_stream);
+
+/* Bytes of device workspace ep_expert_gemm_backward needs (>= 16). */
+size_t ep_expert_gemm_backward_workspace_bytes(int64_t num_rows, int n_dim, int num_experts,
+                                               int activation);
+
+/*
+ * Gradients of ep_expert_gemm (bf16).  With dy the gradient of y (which is
+ * also the residual's), for every row d of expert e's block:
+ *   dz[d]            = row_weight[d] * dy[d] * act'(z[d])   (rounded to bf16 for the two products)
+ *   dx[d]            = bf16_rne( dz[d] W[e] )
+ *   dw[e]            = bf16_rne( sum over e's rows of dz[d]^T x[d] )
+ *   dbias[e]         = sum over e's rows of dz[d]           (fp32, from dz before its rounding)
+ *   d_row_weight[d]  = sum over columns of dy[d] * act(z[d])
+ * dw and dbias are written whole: zero for an expert without rows.  Padding
+ * rows of dx and d_row_weight are not written.  The sums run in a fixed
+ * order: results depend only on the inputs.
+ *
+ * dy            bf16 [num_rows, n_dim].
+ * x, w          as in the forward call, bf16 (x may be NULL without dw, w
+ *               without dx).
+ * z             bf16 [num_rows, n_w], the forward call's; may be NULL for
+ *               EP_ACT_NONE without d_row_weight.
+ * dx            bf16 [num_rows, k_dim] or NULL (not wanted).
+ * dw            bf16 [num_experts, n_w, k_dim] or NULL.
+ * dbias         fp32 [num_experts, n_w] or NULL.
+ * d_row_weight  fp32 [num_rows] or NULL.
+ * workspace     device scratch of ws_bytes >=
+ *               ep_expert_gemm_backward_workspace_bytes(...); no
+ *               initialisation, garbage after.
+ * Other arguments and limits as ep_expert_gemm.
+ */
+ep_status_t ep_expert_gemm_backward(const void* dy, const void* x, const void* w, const void* z,
+                                    int activation, const float* row_weight, int64_t num_rows, int k_dim,
+                                    int n_dim, int num_experts, const int32_t* expert_offset,
+                                    const int32_t* num_tokens_per_expert, void* dx, void* dw, float* dbias,
+                                    float* d_row_weight, void* workspace, size_t ws_bytes,
+                                    int32_t* d_status, void* cuda_stream);
+
+/* Limits of ep_moe_few_tokens. */
+#define EP_FEW_MAX_TOKENS 256
+#define EP_FEW_MAX_TOPK   16
+
+/* Bytes of device workspace ep_moe_few_tokens needs (>= 16). */
+size_t ep_moe_few_tokens_workspace_bytes(int num_tokens, int num_topk, int hidden, int inner,
+                                         int num_experts);
+
+/*
+ * A whole mixture-of-experts layer for a few tokens, in two kernels: routing
+ * by topk_idx, up product, activation, down product, the weighted sum over a
+ * token's experts and the residual, without receive rows in between.  For
+ * every token t:
+ *   h      = bf16_rne( act( w_up[e] x[t] + bias_up[e] ) ),  e = topk_idx[t,k] >= 0
+ *   out[t] = bf16_rne( residual[t] + sum over those k of
+ *                      topk_weights[t,k] * ( w_down[e] h + bias_down[e] ) )
+ * accumulated in fp32, k ascending.  A token without valid entries gets its
+ * residual, or zeros.  Only the weights of experts that some token names are
+ * read.
+ *
+ * x             bf16 [T, H]; topk_idx int64 [T, K] (entries outside [-1, E)
+ *               set EP_ERR_INVALID_INDEX and are skipped); topk_weights fp32
+ *               [T, K].
+ * w_up          bf16 [E, n_w, H], n_w = inner, or 2 inner for EP_ACT_SWIGLU.
+ * w_down        bf16 [E, H, inner].
+ * bias_up       fp32 [E, n_w] or NULL; bias_down fp32 [E, H] or NULL.
+ * residual      bf16 [T, H] or NULL; may be out itself.
+ * out           bf16 [T, H].
+ * workspace     device scratch of ws_bytes >=
+ *               ep_moe_few_tokens_workspace_bytes(...); no initialisation,
+ *               garbage after.
+ * Limits: T <= EP_FEW_MAX_TOKENS, K <= EP_FEW_MAX_TOPK, E <= EP_MAX_EXPERTS,
+ * H and inner multiples of 8 and <= 2^20 (beyond: EP_ERR_UNSUPPORTED).
+ * More tokens take ep_dispatch_expanded, ep_expert_gemm twice and
+ * ep_combine_expanded.
+ */
+ep_status_t ep_moe_few_tokens(const void* x, const int64_t* topk_idx, const float* topk_weights,
+                              const void* w_up, const float* bias_up, int activation, const void* w_down,
+                              const float* bias_down, const void* residual, int num_tokens, int hidden,
+                              int inner, int num_topk, int num_experts, void* workspace, size_t ws_bytes,
+                              void* out, int32_t* d_status, void* cuda_stream);
+
+/*
  * Combined top-k weights ("DeepEP Symmetric Memory" section 9.2: combine
  * returns combined_topk_weights).  For every token t and slot k:
  *   combined_topk_weights[t,k] = sum over ranks r holding t (ascending, fp32)
