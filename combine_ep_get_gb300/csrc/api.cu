@@ -886,6 +886,7 @@ ep_status_t ep_moe_few_tokens(const void* x, const int64_t* topk_idx, const floa
     char* ws = static_cast<char*>(workspace);
     p.h = reinterpret_cast<__nv_bfloat16*>(ws + f.off_h);
     p.part = reinterpret_cast<float*>(ws + f.off_part);
+    p.done = reinterpret_cast<uint32_t*>(ws + f.off_done);
     p.out = static_cast<__nv_bfloat16*>(out);
     p.status = d_status;
     return epg::launch_few_tokens(p, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? EP_OK

@@ -131,26 +131,6 @@ __global__ void __launch_bounds__(256) activation_backward_kernel(const __grid_c
         }
 }
 
-// grid (column tiles of K, E)
-__global__ void __launch_bounds__(256) dx_kernel(const __grid_constant__ ExpertBackwardParams p) {
-    const int e = blockIdx.y, n0 = blockIdx.x * kT, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    int64_t first;
-    const int cnt = expert_rows(p.expert_offset, p.counts, e, p.rows, &first, p.status);
-    for (int m0 = 0; m0 < cnt; m0 += kT) {
-        float acc[4][4] = {};
-        tile_product(
-            acc, p.Nw, [&](int r, int64_t k) { return m0 + r < cnt ? bf(p.dz, (first + m0 + r) * p.Nw + k) : 0.0f; },
-            [&](int c, int64_t k) {
-                return n0 + c < p.K ? bf(p.w, (static_cast<int64_t>(e) * p.Nw + k) * p.K + n0 + c) : 0.0f;
-            });
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) {
-                const int r = m0 + 4 * ty + i, n = n0 + 4 * tx + j;
-                if (r < cnt && n < p.K) p.dx[(first + r) * p.K + n] = __float2bfloat16(acc[i][j]);
-            }
-    }
-}
-
 // grid (column tiles of K, E, row tiles of Nw)
 __global__ void __launch_bounds__(256) dw_kernel(const __grid_constant__ ExpertBackwardParams p) {
     const int e = blockIdx.y, n0 = blockIdx.x * kT, m0 = blockIdx.z * kT;
@@ -169,100 +149,22 @@ __global__ void __launch_bounds__(256) dw_kernel(const __grid_constant__ ExpertB
         }
 }
 
-// The block's entries (t, k) that name expert e, ascending; returns how many.
-__device__ int entries_of(const FewTokensParams& p, int e, int16_t* list) {
-    __shared__ int n;
-    if (threadIdx.x < 32) {
-        int found = 0;
-        for (int i0 = 0; i0 < p.T * p.K; i0 += 32) {
-            const int i = i0 + threadIdx.x;
-            const int64_t v = i < p.T * p.K ? p.topk_idx[i] : -1;
-            if ((v < -1 || v >= p.E) && blockIdx.x == 0 && e == 0) atomicOr(p.status, EP_ERR_INVALID_INDEX);
-            const unsigned m = __ballot_sync(0xffffffffu, v == e);
-            if (v == e) list[found + __popc(m & ((1u << threadIdx.x) - 1))] = static_cast<int16_t>(i);
-            found += __popc(m);
-        }
-        if (threadIdx.x == 0) n = found;
-    }
-    __syncthreads();
-    return n;
-}
-
-// grid (column tiles, E)
-template <bool kUp>
-__global__ void __launch_bounds__(256) few_kernel(const __grid_constant__ FewTokensParams p) {
-    __shared__ int16_t list[EP_FEW_MAX_TOKENS * EP_FEW_MAX_TOPK];
-    const int e = blockIdx.y, n0 = blockIdx.x * kT, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int cnt = entries_of(p, e, list);
-    const bool gated = kUp && p.act == EP_ACT_SWIGLU;
-    const int N = kUp ? p.I : p.H, Nw = kUp ? p.Nw : p.H, depth = kUp ? p.H : p.I;
-    const __nv_bfloat16* w = kUp ? p.w_up : p.w_down;
-    const float* bias = kUp ? p.bias_up : p.bias_down;
-    for (int m0 = 0; m0 < cnt; m0 += kT) {
-        float acc[2][4][4] = {};
-        for (int half = 0; half < (gated ? 2 : 1); ++half)
-            tile_product(
-                acc[half], depth,
-                [&](int r, int64_t k) {
-                    if (m0 + r >= cnt) return 0.0f;
-                    const int i = list[m0 + r];
-                    return kUp ? bf(p.x, static_cast<int64_t>(i / p.K) * p.H + k)
-                               : bf(p.h, static_cast<int64_t>(i) * p.I + k);
-                },
-                [&](int c, int64_t k) {
-                    return n0 + c < N ? bf(w, (static_cast<int64_t>(e) * Nw + half * N + n0 + c) * depth + k) : 0.0f;
-                });
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) {
-                const int r = m0 + 4 * ty + i, n = n0 + 4 * tx + j;
-                if (r >= cnt || n >= N) continue;
-                float z[2] = {acc[0][i][j], acc[1][i][j]};
-                for (int half = 0; half < (gated ? 2 : 1); ++half)
-                    if (bias) z[half] += bias[static_cast<int64_t>(e) * Nw + half * N + n];
-                const int64_t at = static_cast<int64_t>(list[r]) * N + n;
-                if (kUp)
-                    p.h[at] = __float2bfloat16(gated ? silu(z[0]) * z[1] : activate(z[0], p.act));
-                else
-                    p.part[at] = z[0];
-            }
-    }
-}
-
-// grid (column blocks, T)
-__global__ void __launch_bounds__(256) few_sum_kernel(const __grid_constant__ FewTokensParams p) {
-    const int t = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x;
-    if (n >= p.H) return;
-    float v = p.residual ? bf(p.residual, static_cast<int64_t>(t) * p.H + n) : 0.0f;
-    for (int k = 0; k < p.K; ++k) {
-        const int i = t * p.K + k;
-        const int64_t e = p.topk_idx[i];
-        if (e >= 0 && e < p.E) v = fmaf(p.topk_weights[i], p.part[static_cast<int64_t>(i) * p.H + n], v);
-    }
-    p.out[static_cast<int64_t>(t) * p.H + n] = __float2bfloat16(v);
-}
-
 }  // namespace
 
 cudaError_t launch_expert_gemm(const ExpertGemmParams& p, bool fp8, cudaStream_t stream) {
+    if (!fp8) return launch_expert_gemm_bf16(p, stream);
     const dim3 grid((p.N + kT - 1) / kT, p.E);
-    if (fp8)
-        product_kernel<true><<<grid, 256, 0, stream>>>(p);
-    else
-        product_kernel<false><<<grid, 256, 0, stream>>>(p);
+    product_kernel<true><<<grid, 256, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
 cudaError_t launch_expert_backward(const ExpertBackwardParams& p, cudaStream_t stream) {
     activation_backward_kernel<<<dim3((p.N + 255) / 256, p.E), 256, 0, stream>>>(p);
-    if (p.dx) dx_kernel<<<dim3((p.K + kT - 1) / kT, p.E), 256, 0, stream>>>(p);
+    if (p.dx) {
+        const cudaError_t e = launch_input_grad(p, p.dz, stream);
+        if (e != cudaSuccess) return e;
+    }
     if (p.dw) dw_kernel<<<dim3((p.K + kT - 1) / kT, p.E, (p.Nw + kT - 1) / kT), 256, 0, stream>>>(p);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_few_tokens(const FewTokensParams& p, cudaStream_t stream) {
-    few_kernel<true><<<dim3((p.I + kT - 1) / kT, p.E), 256, 0, stream>>>(p);
-    few_kernel<false><<<dim3((p.H + kT - 1) / kT, p.E), 256, 0, stream>>>(p);
-    few_sum_kernel<<<dim3((p.H + 255) / 256, p.T), 256, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -58,6 +58,7 @@ struct FewTokensParams {
     int T, H, I, Nw, K, E, act;
     __nv_bfloat16* h;            // workspace [T * K][I]
     float* part;                 // workspace [T * K][H]
+    uint32_t* done;              // workspace [H / 128, rounded up][T]
     __nv_bfloat16* out;          // [T][H]
     int32_t* status;
 };
@@ -65,6 +66,9 @@ struct FewTokensParams {
 cudaError_t launch_expert_gemm(const ExpertGemmParams& p, bool fp8, cudaStream_t stream);
 cudaError_t launch_expert_backward(const ExpertBackwardParams& p, cudaStream_t stream);
 cudaError_t launch_few_tokens(const FewTokensParams& p, cudaStream_t stream);
+// The parts of these on the tensor cores.
+cudaError_t launch_expert_gemm_bf16(const ExpertGemmParams& p, cudaStream_t stream);
+cudaError_t launch_input_grad(const ExpertBackwardParams& p, const __nv_bfloat16* dz, cudaStream_t stream);
 
 // Workspace carve-ups shared by the size queries and the calls.
 constexpr int kBackwardTileRows = 64;   // rows of one partial column sum of dz
@@ -81,14 +85,15 @@ inline BackwardWorkspace backward_workspace(int64_t rows, int Nw, int E) {
     return b;
 }
 struct FewWorkspace {
-    size_t off_h, off_part, total;
+    size_t off_h, off_part, off_done, total;
 };
 inline FewWorkspace few_workspace(int T, int K, int H, int I) {
     const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     FewWorkspace f;
     f.off_h = 0;
     f.off_part = up(static_cast<size_t>(T) * K * I * 2);
-    f.total = f.off_part + up(static_cast<size_t>(T) * K * H * 4) + 256;
+    f.off_done = f.off_part + up(static_cast<size_t>(T) * K * H * 4);
+    f.total = f.off_done + up((static_cast<size_t>(H) + 127) / 128 * T * 4) + 256;
     return f;
 }
 

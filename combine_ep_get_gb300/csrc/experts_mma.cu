@@ -1,0 +1,637 @@
+// The experts' products on the tensor cores (tcgen05): rows of the expanded
+// receive layout times each expert's weights, the input gradient, and the two
+// products of the few-token layer.
+//
+// D[feature, row] = sum over k of W[feature, k] * rows[row, k].  The weights'
+// features are the M side (128 a tile, always full) and an expert's rows the
+// N side, whose width an MMA may choose in steps of 16: a tile takes the rows
+// an expert has instead of padding them to 128, and the weights, which are
+// what a call with few rows per expert has to read, stream through the wide
+// side.  Accumulators: fp32 in tensor memory, two of them, so that the
+// epilogue of one tile runs under the MMAs of the next.
+//
+// One CTA per SM walks the tiles (expert, rows, features): warp 0 issues the
+// tensor-map loads of 128-byte-swizzled operand tiles, 64 terms of the sum a
+// stage; warp 1 issues the MMAs; warps 4-7 read the accumulators, lane =
+// feature, and apply the epilogue.
+//
+// SWIGLU: the 128 features of a tile are, for every 32 lanes, 16 gate rows
+// and the 16 up rows that belong to them, so one exchange across half a warp
+// brings each pair together.
+#include <algorithm>
+
+#include "experts.cuh"
+#include "tcgen05.cuh"
+
+namespace epg {
+
+namespace {
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static const EncodeFn fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            f = nullptr;
+        }
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+}  // namespace
+
+bool encode_map(CUtensorMap* map, bool fp8, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                const uint32_t* box) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t d[5], s[5];
+    cuuint32_t b[5], one[5] = {1, 1, 1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i + 1 < rank) s[i] = strides[i];
+    }
+    return fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+              const_cast<void*>(base), d, s, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kM = 128;          // features of a tile
+constexpr int kDepth = 64;       // terms of the sum in a stage (128 bytes of bf16)
+constexpr int kABytes = kM * kDepth * 2;
+constexpr int kGroupTiles = 16;  // row tiles whose features are walked together, for the L2
+
+enum Mode { kProduct, kInputGrad, kFewUp, kFewDown };
+
+struct MmaArgs {
+    CUtensorMap a, b;
+    int depth;                    // terms of the sum
+    int F;                        // output features of an expert
+    int gate_half;                // SWIGLU: rows of W from a gate row to its up row (0: not gated)
+    int E, act;
+    int64_t rows;
+    const int32_t* expert_offset;
+    const int32_t* counts;
+    const float* bias;            // [E][F or 2 F]
+    const float* row_weight;
+    const __nv_bfloat16* residual;
+    __nv_bfloat16* y;             // rows of F
+    __nv_bfloat16* z;             // rows of F or 2 F
+    // few tokens
+    const int64_t* topk_idx;
+    const float* topk_weights;
+    int T, K;
+    float* part;                  // [T * K][F]
+    uint32_t* done;               // [feature tiles][T]: experts of a token that are done
+    int done_words;
+    __nv_bfloat16* out;           // [T][F]
+    int32_t* status;
+};
+
+template <int NT>
+struct Shape {
+    static constexpr int kStageBytes = kABytes + NT * kDepth * 2;
+    static constexpr int kStages = (192 * 1024) / kStageBytes < 10 ? (192 * 1024) / kStageBytes : 10;
+    static constexpr int kBoxRows = NT < 64 ? NT : 64;
+    static constexpr int kColumns = 2 * NT < 32 ? 32 : 2 * NT;   // of tensor memory
+};
+
+struct Barriers {
+    uint64_t full[12], empty[12], acc_full[2], acc_empty[2], drain;
+    uint32_t tmem;
+    int total_tiles;
+    int warp_sum[8];
+    int gave_up;                  // a wait of the epilogue ran out
+    int completed;                // few tokens, down: tokens whose last expert this tile was
+};
+
+// Experts' row tiles: tile_end[e] = row tiles of experts 0 .. e.
+struct Table {
+    int* tile_end;    // [E]
+    int* first;       // [E] first row, or first entry of the list
+    int* count;       // [E]
+    int16_t* list;    // few tokens: entries t * K + k, expert by expert
+    int16_t* expert;  // few tokens: expert of each entry, -1 for none; behind them, tokens just completed
+};
+
+// Inclusive scan of f(e) over the experts into out[e], by all threads.
+template <class F>
+__device__ void scan_experts(int E, int* out, Barriers* s, F f) {
+    const int each = (E + kThreads - 1) / kThreads, e0 = threadIdx.x * each;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    int sum = 0;
+    for (int i = 0; i < each; ++i)
+        if (e0 + i < E) sum += f(e0 + i);
+    const int incl = warp_inclusive_scan(sum);
+    if (lane == 31) s->warp_sum[warp] = incl;
+    __syncthreads();
+    int run = incl - sum;
+    for (int w = 0; w < warp; ++w) run += s->warp_sum[w];
+    for (int i = 0; i < each; ++i)
+        if (e0 + i < E) {
+            run += f(e0 + i);
+            out[e0 + i] = run;
+        }
+    __syncthreads();
+}
+
+// A tile: expert, its rows [row0, row0 + rows) within the expert, features from f0.
+struct Tile {
+    int e, row0, rows, width, f0;
+};
+
+template <int NT>
+__device__ __forceinline__ Tile tile_at(int g, const Table& t, int E, int feature_tiles, int tile_features) {
+    int lo = 0, hi = E - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (static_cast<int64_t>(t.tile_end[mid]) * feature_tiles > g)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    Tile r;
+    r.e = lo;
+    const int before = lo > 0 ? t.tile_end[lo - 1] : 0;
+    const int n = t.tile_end[lo] - before, cnt = t.count[lo];
+    int local = g - before * feature_tiles;
+    const int group = local / (kGroupTiles * feature_tiles);
+    local -= group * kGroupTiles * feature_tiles;
+    const int in_group = min(kGroupTiles, n - group * kGroupTiles);
+    const int f = local / in_group, row_tile = group * kGroupTiles + local % in_group;
+    // few tiles share an expert's rows evenly (each with its weights from L2)
+    const int per = n <= 4 ? ((cnt + n - 1) / n + 15) / 16 * 16 : NT;
+    r.row0 = row_tile * per;
+    r.rows = min(per, cnt - r.row0);
+    r.width = (r.rows + 15) / 16 * 16;
+    r.f0 = f * tile_features;
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+
+// Four-byte stores of two neighbouring features: the lanes of a pair trade
+// so that the even lane holds both features of token j, the odd one of j + 1.
+__device__ __forceinline__ float2 trade_pair(float first, float second, int lane) {
+    const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? first : second, 1);
+    return lane & 1 ? make_float2(got, second) : make_float2(first, got);
+}
+
+template <int kMode, int NT>
+__global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_constant__ MmaArgs p) {
+    using S = Shape<NT>;
+    constexpr bool kFew = kMode == kFewUp || kMode == kFewDown;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* stages = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
+    Barriers* s = reinterpret_cast<Barriers*>(stages + S::kStages * S::kStageBytes);
+    Table t;
+    t.tile_end = reinterpret_cast<int*>(s + 1);
+    t.first = t.tile_end + p.E;
+    t.count = t.first + p.E;
+    t.list = reinterpret_cast<int16_t*>(t.count + p.E);
+    t.expert = t.list + p.T * p.K;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int tile_features = p.gate_half ? kM / 2 : kM;
+    const int feature_tiles = (p.F + tile_features - 1) / tile_features;
+    const int k_blocks = (p.depth + kDepth - 1) / kDepth;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&s->full[i], 1);
+            mbar_init(&s->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s->acc_full[i], 1);
+            mbar_init(&s->acc_empty[i], 4);
+        }
+        mbar_init(&s->drain, 1);
+        s->gave_up = 0;
+        fence_mbar_init();
+        prefetch_map(&p.a);
+        prefetch_map(&p.b);
+    }
+    if (warp == 2) tmem_alloc<1>(&s->tmem, S::kColumns);
+    // The down product's kernel may start, and route, once every CTA of the
+    // up product's has seen its own inputs complete.
+    if (kMode != kFewDown) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
+
+    if (kFew) {
+        // entries by expert, in the order of (token, slot)
+        for (int i = threadIdx.x; i < p.T * p.K; i += kThreads) {
+            const int64_t e = p.topk_idx[i];
+            const bool ok = e >= 0 && e < p.E;
+            if (!ok && e != -1 && kMode == kFewUp && blockIdx.x == 0) atomicOr(p.status, EP_ERR_INVALID_INDEX);
+            t.expert[i] = ok ? static_cast<int16_t>(e) : static_cast<int16_t>(-1);
+        }
+        for (int e = threadIdx.x; e < p.E; e += kThreads) t.count[e] = 0;
+        if (kMode == kFewUp && blockIdx.x == 0)
+            for (int i = threadIdx.x; i < p.done_words; i += kThreads) p.done[i] = 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < p.T * p.K; i += kThreads)
+            if (t.expert[i] >= 0) atomicAdd(&t.count[t.expert[i]], 1);
+        __syncthreads();
+        scan_experts(p.E, t.first, s, [&](int e) { return t.count[e]; });
+        scan_experts(p.E, t.tile_end, s, [&](int e) { return (t.count[e] + NT - 1) / NT; });
+        // first[e] now ends expert e's entries; filling from the last entry
+        // down turns it into their start
+        if (warp == 0)
+            for (int i0 = (p.T * p.K - 1) / 32 * 32; i0 >= 0; i0 -= 32) {
+                const int i = i0 + lane, e = i < p.T * p.K ? t.expert[i] : -1;
+                const unsigned same = __match_any_sync(0xffffffffu, e);
+                if (e >= 0) {
+                    const int at = t.first[e] - __popc(same >> lane);
+                    t.list[at] = static_cast<int16_t>(i);
+                }
+                __syncwarp();
+                if (e >= 0 && (same >> lane) == 1u) t.first[e] -= __popc(same);
+                __syncwarp();
+            }
+    } else {
+        for (int e = threadIdx.x; e < p.E; e += kThreads) {
+            int64_t first;
+            t.count[e] = expert_rows(p.expert_offset, p.counts, e, p.rows, &first, p.status);
+            t.first[e] = static_cast<int>(first);
+        }
+        __syncthreads();
+        scan_experts(p.E, t.tile_end, s, [&](int e) { return (t.count[e] + NT - 1) / NT; });
+    }
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    const uint32_t tmem = s->tmem;
+    const int tiles = t.tile_end[p.E - 1] * feature_tiles;
+
+    if (kMode == kFewDown) {
+        pdl_wait();
+        pdl_launch_dependents();
+        // tokens of no expert: their residual, or zeros
+        for (int tok = blockIdx.x; tok < p.T; tok += gridDim.x) {
+            bool any = false;
+            for (int k = 0; k < p.K; ++k) any |= t.expert[tok * p.K + k] >= 0;
+            if (!any)
+                for (int f = threadIdx.x; f < p.F; f += kThreads) {
+                    const int64_t at = static_cast<int64_t>(tok) * p.F + f;
+                    p.out[at] = p.residual ? p.residual[at] : __float2bfloat16(0.0f);
+                }
+        }
+    }
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int g = blockIdx.x; g < tiles && ok; g += gridDim.x) {
+                const Tile r = tile_at<NT>(g, t, p.E, feature_tiles, tile_features);
+                const int first = t.first[r.e] + r.row0;
+                const int boxes = kFew ? (r.rows + 3) / 4 : (r.rows + S::kBoxRows - 1) / S::kBoxRows;
+                const uint32_t bytes = kABytes + boxes * (kFew ? 4 : S::kBoxRows) * kDepth * 2;
+                for (int kb = 0; kb < k_blocks; ++kb, ++it) {
+                    const int st = it % S::kStages;
+                    ok = mbar_wait_bounded(&s->empty[st], ((it / S::kStages) & 1) ^ 1);
+                    if (!ok) break;
+                    uint8_t* sa = stages + st * S::kStageBytes;
+                    uint8_t* sb = sa + kABytes;
+                    const uint32_t bar = smem_addr(&s->full[st]);
+                    mbar_arrive_expect_tx(&s->full[st], bytes);
+                    if (kMode == kInputGrad) {
+                        tma_load_3d<1>(sa, &p.a, bar, r.f0, kb * kDepth, r.e);
+                        tma_load_3d<1>(sa + kABytes / 2, &p.a, bar, r.f0 + 64, kb * kDepth, r.e);
+                    } else if (p.gate_half) {
+                        for (int i = 0; i < 4; ++i) {
+                            tma_load_3d<1>(sa + i * 4096, &p.a, bar, kb * kDepth, r.f0 + 16 * i, r.e);
+                            tma_load_3d<1>(sa + i * 4096 + 2048, &p.a, bar, kb * kDepth, p.gate_half + r.f0 + 16 * i,
+                                           r.e);
+                        }
+                    } else {
+                        tma_load_3d<1>(sa, &p.a, bar, kb * kDepth, r.f0, r.e);
+                    }
+                    if (kFew) {
+                        for (int i = 0; i < boxes; ++i) {
+                            int row[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int entry = t.list[first + min(4 * i + j, r.rows - 1)];
+                                row[j] = kMode == kFewUp ? entry / p.K : entry;
+                            }
+                            tma_gather4(sb + i * 4 * kDepth * 2, &p.b, bar, kb * kDepth, row[0], row[1], row[2], row[3]);
+                        }
+                    } else {
+                        for (int i = 0; i < boxes; ++i)
+                            tma_load_2d<1>(sb + i * S::kBoxRows * kDepth * 2, &p.b, bar, kb * kDepth,
+                                           first + i * S::kBoxRows);
+                    }
+                }
+            }
+            if (!ok) atomicOr(p.status, EP_ERR_TIMEOUT);
+            // no copy may still be in flight when the CTA ends
+            for (int i = max(0, it - S::kStages); i < it; ++i)
+                if (!mbar_wait_bounded(&s->full[i % S::kStages], (i / S::kStages) & 1)) break;
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int it = 0, n = 0;
+            bool ok = true;
+            for (int g = blockIdx.x; g < tiles && ok; g += gridDim.x, ++n) {
+                const Tile r = tile_at<NT>(g, t, p.E, feature_tiles, tile_features);
+                const uint32_t idesc = instr_desc(false, kMode == kInputGrad, false, kM, r.width);
+                const uint32_t d = tmem + (n & 1) * NT;
+                ok = mbar_wait_bounded(&s->acc_empty[n & 1], ((n / 2) & 1) ^ 1);
+                tcgen05_after_sync();
+                for (int kb = 0; kb < k_blocks && ok; ++kb, ++it) {
+                    const int st = it % S::kStages;
+                    ok = mbar_wait_bounded(&s->full[st], (it / S::kStages) & 1);
+                    if (!ok) break;
+                    tcgen05_after_sync();
+                    const uint32_t sa = smem_addr(stages + st * S::kStageBytes), sb = sa + kABytes;
+#pragma unroll
+                    for (int k = 0; k < kDepth / 16; ++k) {
+                        const uint64_t a = kMode == kInputGrad ? operand_desc(sa + k * 2048, kABytes / 2)
+                                                               : operand_desc(sa + k * 32, 16);
+                        mma<1, false>(d, a, operand_desc(sb + k * 32, 16), idesc, kb > 0 || k > 0);
+                    }
+                    mma_commit<1>(&s->empty[st]);
+                }
+                if (ok) mma_commit<1>(&s->acc_full[n & 1]);
+            }
+            if (!ok) {
+                atomicOr(p.status, EP_ERR_TIMEOUT);
+                mma_commit<1>(&s->drain);
+                mbar_wait_bounded(&s->drain, 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        const int q = warp - 4;
+        int n = 0;
+        for (int g = blockIdx.x; g < tiles; g += gridDim.x, ++n) {
+            const Tile r = tile_at<NT>(g, t, p.E, feature_tiles, tile_features);
+            const int first = t.first[r.e] + r.row0;
+            const uint32_t acc = tmem + (n & 1) * NT + (static_cast<uint32_t>(q * 32) << 16);
+            const bool ready =
+                __all_sync(0xffffffffu, mbar_wait_bounded(&s->acc_full[n & 1], (n / 2) & 1) ? 1 : 0) != 0;
+            if (!ready) {
+                atomicOr(p.status, EP_ERR_TIMEOUT);
+                s->gave_up = 1;
+            }
+            if (kMode == kFewDown) named_barrier(1, 128);   // its barriers below are for all four warps
+            if (kMode == kFewDown ? *reinterpret_cast<volatile int*>(&s->gave_up) != 0 : !ready) break;
+            tcgen05_after_sync();
+            const bool gated = p.gate_half != 0;
+            // this lane's row of W within the expert, and its feature of y
+            const int f = gated ? r.f0 + q * 16 + (lane & 15) : r.f0 + q * 32 + lane;
+            const int wrow = gated && lane >= 16 ? p.gate_half + f : f;
+            const int Fw = gated ? 2 * p.F : p.F;
+            const bool f_ok = f < p.F;
+            const float bias = p.bias && f_ok ? p.bias[static_cast<int64_t>(r.e) * Fw + wrow] : 0.0f;
+            for (int c0 = 0; c0 < r.width; c0 += 32) {
+                float v[32];
+                __syncwarp();
+                tmem_load32(acc + c0, v);
+                if (c0 + 32 >= r.width) {
+                    tcgen05_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s->acc_empty[n & 1]);
+                }
+                const auto row_of = [&](int j) -> int64_t {
+                    return kFew ? static_cast<int64_t>(t.list[first + j]) : static_cast<int64_t>(first) + j;
+                };
+                if (kMode != kInputGrad)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] += bias;
+                if (kMode == kFewDown) {
+#pragma unroll 8
+                    for (int j = 0; j < 32; ++j)
+                        if (c0 + j < r.rows && f_ok && EP_IN(row_of(c0 + j), p.rows)) p.part[row_of(c0 + j) * p.F + f] = v[j];
+                    continue;
+                }
+                if (kMode == kProduct && p.z) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float2 w = trade_pair(v[j], v[j + 1], lane);
+                        const int c = c0 + j + (lane & 1);
+                        if (c < r.rows && f_ok && EP_IN(row_of(c), p.rows))
+                            *reinterpret_cast<uint32_t*>(p.z + row_of(c) * Fw + (wrow & ~1)) = pack2(w.x, w.y);
+                    }
+                }
+                const auto store = [&](int c, int feature, float2 a) {
+                    if (c >= r.rows || feature >= p.F || !EP_IN(row_of(c), p.rows)) return;
+                    const int64_t d = row_of(c), at = d * p.F + feature;
+                    if (kMode == kProduct) {
+                        if (p.row_weight) {
+                            const float w = p.row_weight[d];
+                            a.x *= w;
+                            a.y *= w;
+                        }
+                        if (p.residual) {
+                            const float2 b = unpack2(*reinterpret_cast<const uint32_t*>(p.residual + at));
+                            a.x += b.x;
+                            a.y += b.y;
+                        }
+                    }
+                    *reinterpret_cast<uint32_t*>(p.y + at) = pack2(a.x, a.y);
+                };
+                if (kMode != kInputGrad && gated) {
+                    const bool up = lane >= 16;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        // lanes 0-15 take token j (then j + 2), lanes 16-31 token j + 1 (j + 3)
+                        const float g0 = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + 1], 16);
+                        const float g1 = __shfl_xor_sync(0xffffffffu, up ? v[j + 2] : v[j + 3], 16);
+                        const float a0 = up ? silu(g0) * v[j + 1] : silu(v[j]) * g0;
+                        const float a1 = up ? silu(g1) * v[j + 3] : silu(v[j + 2]) * g1;
+                        store(c0 + j + (up ? 1 : 0) + 2 * (lane & 1), f & ~1, trade_pair(a0, a1, lane));
+                    }
+                } else {
+                    if (kMode != kInputGrad && p.act != EP_ACT_NONE) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = activate(v[j], p.act);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2)
+                        store(c0 + j + (lane & 1), f & ~1, trade_pair(v[j], v[j + 1], lane));
+                }
+            }
+            if (kMode == kFewDown) {
+                // the tokens whose last expert this was: their sum over the
+                // experts, k ascending, whoever came last
+                const int tid = threadIdx.x - 128;
+                if (tid == 0) s->completed = 0;
+                __threadfence();
+                named_barrier(1, 128);
+                for (int j = tid; j < r.rows; j += 128) {
+                    const int tok = t.list[first + j] / p.K;
+                    int experts = 0;
+                    for (int k = 0; k < p.K; ++k) experts += t.expert[tok * p.K + k] >= 0;
+                    const uint32_t before = atomicAdd(&p.done[(r.f0 / kM) * p.T + tok], 1u);
+                    if (before + 1 == static_cast<uint32_t>(experts)) {
+                        __threadfence();
+                        t.expert[p.T * p.K + atomicAdd(&s->completed, 1)] = static_cast<int16_t>(tok);
+                    }
+                }
+                named_barrier(1, 128);
+                const int m = s->completed;
+                const int feature = r.f0 + tid;
+                for (int i = 0; i < m; ++i) {
+                    const int tok = t.expert[p.T * p.K + i];
+                    if (feature >= p.F || !EP_IN(tok, p.T)) continue;
+                    float sum = 0.0f;
+                    for (int k = 0; k < p.K; ++k) {
+                        const int entry = tok * p.K + k;
+                        if (t.expert[entry] >= 0)
+                            sum = fmaf(p.topk_weights[entry], __ldcg(p.part + static_cast<int64_t>(entry) * p.F + feature),
+                                       sum);
+                    }
+                    const int64_t at = static_cast<int64_t>(tok) * p.F + feature;
+                    if (p.residual) sum += __bfloat162float(p.residual[at]);
+                    p.out[at] = __float2bfloat16(sum);
+                }
+                named_barrier(1, 128);
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 2) tmem_free<1>(tmem, S::kColumns);
+}
+
+template <int NT>
+size_t smem_bytes(int E, int entries) {
+    using S = Shape<NT>;
+    return 1024 + S::kStages * S::kStageBytes + sizeof(Barriers) + static_cast<size_t>(E) * 12 +
+           (entries > 0 ? static_cast<size_t>(entries) * 4 + EP_FEW_MAX_TOKENS * 2 : 0);
+}
+
+template <int kMode, int NT>
+cudaError_t launch(const MmaArgs& a, int tiles_bound, cudaStream_t stream) {
+    const size_t smem = smem_bytes<NT>(a.E, a.T * a.K);
+    const auto kernel = experts_mma_kernel<kMode, NT>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const int grid = std::max(1, std::min(device_info().num_sms, tiles_bound));
+    return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, stream, a);
+}
+
+// Weights [E][rows][cols] bf16 as a map of boxes of 64 columns x `box` rows.
+bool weight_map(CUtensorMap* m, const void* w, int E, int rows, int cols, int box) {
+    const uint64_t dims[3] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows), static_cast<uint64_t>(E)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(cols) * 2, static_cast<uint64_t>(cols) * rows * 2};
+    const uint32_t boxes[3] = {kDepth, static_cast<uint32_t>(box), 1};
+    return encode_map(m, false, 3, w, dims, strides, boxes);
+}
+bool row_map(CUtensorMap* m, const void* x, int64_t rows, int cols, int box) {
+    const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)};
+    const uint64_t strides[1] = {static_cast<uint64_t>(cols) * 2};
+    const uint32_t boxes[2] = {kDepth, static_cast<uint32_t>(box)};
+    return encode_map(m, false, 2, x, dims, strides, boxes);
+}
+
+int bound_tiles(int64_t row_tiles, int feature_tiles) {
+    const int64_t v = row_tiles * feature_tiles;
+    return v > (1 << 20) ? 1 << 20 : static_cast<int>(v);
+}
+
+}  // namespace
+
+cudaError_t launch_expert_gemm_bf16(const ExpertGemmParams& p, cudaStream_t stream) {
+    constexpr int NT = 256;
+    MmaArgs a{};
+    const bool gated = p.act == EP_ACT_SWIGLU;
+    if (!weight_map(&a.a, p.w, p.E, p.Nw, p.K, gated ? 16 : kM) ||
+        !row_map(&a.b, p.x, p.rows, p.K, Shape<NT>::kBoxRows))
+        return cudaErrorInvalidValue;
+    a.depth = p.K;
+    a.F = p.N;
+    a.gate_half = gated ? p.N : 0;
+    a.E = p.E;
+    a.act = p.act;
+    a.rows = p.rows;
+    a.expert_offset = p.expert_offset;
+    a.counts = p.counts;
+    a.bias = p.bias;
+    a.row_weight = p.row_weight;
+    a.residual = p.residual;
+    a.y = p.y;
+    a.z = p.z;
+    a.status = p.status;
+    const int per = gated ? kM / 2 : kM;
+    return launch<kProduct, NT>(a, bound_tiles(p.rows / NT + p.E, (p.N + per - 1) / per), stream);
+}
+
+cudaError_t launch_input_grad(const ExpertBackwardParams& p, const __nv_bfloat16* dz, cudaStream_t stream) {
+    constexpr int NT = 256;
+    MmaArgs a{};
+    if (!weight_map(&a.a, p.w, p.E, p.Nw, p.K, kDepth) || !row_map(&a.b, dz, p.rows, p.Nw, Shape<NT>::kBoxRows))
+        return cudaErrorInvalidValue;
+    a.depth = p.Nw;
+    a.F = p.K;
+    a.E = p.E;
+    a.rows = p.rows;
+    a.expert_offset = p.expert_offset;
+    a.counts = p.counts;
+    a.y = p.dx;
+    a.status = p.status;
+    return launch<kInputGrad, NT>(a, bound_tiles(p.rows / NT + p.E, (p.K + kM - 1) / kM), stream);
+}
+
+cudaError_t launch_few_tokens(const FewTokensParams& p, cudaStream_t stream) {
+    constexpr int NT = 64;
+    MmaArgs up{};
+    const bool gated = p.act == EP_ACT_SWIGLU;
+    if (!weight_map(&up.a, p.w_up, p.E, p.Nw, p.H, gated ? 16 : kM) || !row_map(&up.b, p.x, p.T, p.H, 1))
+        return cudaErrorInvalidValue;
+    up.depth = p.H;
+    up.F = p.I;
+    up.gate_half = gated ? p.I : 0;
+    up.E = p.E;
+    up.act = p.act;
+    up.topk_idx = p.topk_idx;
+    up.topk_weights = p.topk_weights;
+    up.T = p.T;
+    up.K = p.K;
+    up.rows = static_cast<int64_t>(p.T) * p.K;
+    up.bias = p.bias_up;
+    up.y = p.h;
+    up.done = p.done;
+    up.done_words = (p.H + kM - 1) / kM * p.T;
+    up.status = p.status;
+    MmaArgs down = up;
+    if (!weight_map(&down.a, p.w_down, p.E, p.H, p.I, kM) ||
+        !row_map(&down.b, p.h, static_cast<int64_t>(p.T) * p.K, p.I, 1))
+        return cudaErrorInvalidValue;
+    down.depth = p.I;
+    down.F = p.H;
+    down.gate_half = 0;
+    down.act = EP_ACT_NONE;
+    down.bias = p.bias_down;
+    down.y = nullptr;
+    down.part = p.part;
+    down.residual = p.residual;
+    down.out = p.out;
+    const int entries = p.T * p.K, active = std::min(p.E, entries);
+    const int per = gated ? kM / 2 : kM;
+    cudaError_t e = launch<kFewUp, NT>(up, bound_tiles(active + entries / NT, (p.I + per - 1) / per), stream);
+    if (e != cudaSuccess) return e;
+    return launch<kFewDown, NT>(down, bound_tiles(active + entries / NT, (p.H + kM - 1) / kM), stream);
+}
+
+}  // namespace epg

@@ -1,0 +1,160 @@
+// Inline PTX of the Blackwell tensor path: tensor-map loads, tensor memory,
+// tcgen05.mma and its commits, as the experts' kernels use them.  kCtas is
+// the CTA group: 1, or 2 for a pair of CTAs on one tile (ranks 0 and 1 of a
+// cluster; rank 0 issues the MMAs and owns the "full" barriers).
+#pragma once
+
+#include <cuda.h>
+
+#include "ep_internal.cuh"
+
+namespace epg {
+
+// Shared-memory address of the same offset in the pair's rank 0: bit 24 of a
+// shared::cluster address of one's own memory is the CTA's parity in a pair.
+__device__ __forceinline__ uint32_t cluster_ctarank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// Arrive on a barrier given by its shared::cluster address.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
+
+// Tensor-map loads; `bar` is a shared::cluster address (rank 0's for pairs).
+template <int kCtas>
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uint32_t bar, int x, int y) {
+    if (kCtas == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::
+                "r"(smem_addr(dst)), "l"(m), "r"(bar), "r"(x), "r"(y) : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::
+                "r"(smem_addr(dst)), "l"(m), "r"(bar), "r"(x), "r"(y) : "memory");
+}
+template <int kCtas>
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
+    if (kCtas == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::
+                "r"(smem_addr(dst)), "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::
+                "r"(smem_addr(dst)), "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+}
+// Four rows of a map whose box is one row high, by their indices.
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* m, uint32_t bar, int x, int r0, int r1,
+                                            int r2, int r3) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::
+            "r"(smem_addr(dst)), "l"(m), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3) : "memory");
+}
+
+template <int kCtas>
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t columns) {
+    if (kCtas == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)),
+                     "r"(columns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)),
+                     "r"(columns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+}
+template <int kCtas>
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
+    if (kCtas == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+}
+__device__ __forceinline__ void tcgen05_before_sync() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tcgen05_after_sync() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+// D[tmem] (+)= A B for 16-bit operands (f16 kind) or 8-bit ones.
+template <int kCtas, bool kFp8>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    const uint32_t acc = accumulate ? 1u : 0u;
+#define EP_MMA(group, kind)                                                                                  \
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                           \
+                 "tcgen05.mma.cta_group::" group ".kind::" kind " [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), \
+                 "l"(b), "r"(idesc), "r"(acc)                                                                  \
+                 : "memory")
+    if (kCtas == 1 && !kFp8) EP_MMA("1", "f16");
+    if (kCtas == 2 && !kFp8) EP_MMA("2", "f16");
+    if (kCtas == 1 && kFp8) EP_MMA("1", "f8f6f4");
+    if (kCtas == 2 && kFp8) EP_MMA("2", "f8f6f4");
+#undef EP_MMA
+}
+// The MMAs issued so far arrive on `bar` (in both CTAs of a pair) when done.
+template <int kCtas>
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    if (kCtas == 1)
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                         smem_addr(bar)) : "memory");
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_addr(bar)), "h"(static_cast<uint16_t>(3)) : "memory");
+}
+
+// Shared-memory operand descriptor, 128-byte swizzle.  K-major: rows of 128
+// bytes, 8-row groups 1024 bytes apart (stride offset; the leading offset is
+// not used).  MN-major: 64 elements of MN a 128-byte row, 8-row groups of K
+// 1024 bytes apart, the next 64 of MN `lead` bytes on.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lead) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (static_cast<uint64_t>(lead >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// Instruction descriptor: fp32 accumulation, bf16 (or E4M3) operands.
+__device__ __forceinline__ uint32_t instr_desc(bool fp8, bool a_mn, bool b_mn, int m, int n) {
+    const uint32_t type = fp8 ? 0u : 1u;
+    return (1u << 4) | (type << 7) | (type << 10) | (static_cast<uint32_t>(a_mn) << 15) |
+           (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// 32 lanes x 32 columns of fp32: lane l of the warp gets its 32 columns.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Host: a tensor map of 16- or 8-bit elements, 128-byte swizzle, zero fill.
+// dims and box from the innermost on; strides in bytes from the second.
+bool encode_map(CUtensorMap* map, bool fp8, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                const uint32_t* box);
+
+}  // namespace epg
