@@ -792,7 +792,7 @@ ep_status_t ep_expert_gemm(const void* x, const float* x_sf, int sf_col_major, c
 
 size_t ep_expert_gemm_backward_workspace_bytes(int64_t num_rows, int n_dim, int num_experts, int activation) {
     if (num_rows < 0 || n_dim < 1 || num_experts < 1) return 16;
-    return epg::backward_workspace(num_rows, activation == EP_ACT_SWIGLU ? 2 * n_dim : n_dim, num_experts).total;
+    return epg::backward_workspace(num_rows, n_dim, activation == EP_ACT_SWIGLU ? 2 * n_dim : n_dim, num_experts).total;
 }
 
 ep_status_t ep_expert_gemm_backward(const void* dy, const void* x, const void* w, const void* z, int activation,
@@ -811,7 +811,7 @@ ep_status_t ep_expert_gemm_backward(const void* dy, const void* x, const void* w
     const int Nw = activation == EP_ACT_SWIGLU ? 2 * N : N;
     if (num_rows > 0 && (!dy || (dx && !w) || (dw && !x))) return EP_RET(EP_ERR_INVALID_ARG);
     if (num_rows > 0 && !z && (activation != EP_ACT_NONE || d_row_weight)) return EP_RET(EP_ERR_INVALID_ARG);
-    const epg::BackwardWorkspace b = epg::backward_workspace(num_rows, Nw, E);
+    const epg::BackwardWorkspace b = epg::backward_workspace(num_rows, N, Nw, E);
     if (!ok_ptr(workspace) || ws_bytes < b.total) return EP_RET(EP_ERR_INVALID_ARG);
 
     epg::ExpertBackwardParams p{};
@@ -835,6 +835,7 @@ ep_status_t ep_expert_gemm_backward(const void* dy, const void* x, const void* w
     char* ws = static_cast<char*>(workspace);
     p.dz = reinterpret_cast<__nv_bfloat16*>(ws + b.off_dz);
     p.bias_part = reinterpret_cast<float*>(ws + b.off_part);
+    p.weight_part = reinterpret_cast<float*>(ws + b.off_weight);
     p.status = d_status;
     return epg::launch_expert_backward(p, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
                ? EP_OK

@@ -85,86 +85,12 @@ __global__ void __launch_bounds__(256) product_kernel(const __grid_constant__ Ex
     }
 }
 
-// grid (column tiles, E): dz, its column sums, and the row weights' gradient
-// (by the blocks of the first column tile, which walk all columns)
-__global__ void __launch_bounds__(256) activation_backward_kernel(const __grid_constant__ ExpertBackwardParams p) {
-    const int e = blockIdx.y;
-    int64_t first;
-    const int cnt = expert_rows(p.expert_offset, p.counts, e, p.rows, &first, p.status);
-    const bool gated = p.act == EP_ACT_SWIGLU;
-    const int n = blockIdx.x * 256 + threadIdx.x;
-    if (n < p.N) {
-        float sum[2] = {0.0f, 0.0f};
-        for (int r = 0; r < cnt; ++r) {
-            const int64_t d = first + r;
-            const float da = bf(p.dy, d * p.N + n) * (p.row_weight ? p.row_weight[d] : 1.0f);
-            const float z0 = p.act != EP_ACT_NONE ? bf(p.z, d * p.Nw + n) : 0.0f;
-            if (gated) {
-                const float up = bf(p.z, d * p.Nw + p.N + n);
-                const float g = da * up * silu_slope(z0), u = da * silu(z0);
-                sum[0] += g;
-                sum[1] += u;
-                p.dz[d * p.Nw + n] = __float2bfloat16(g);
-                p.dz[d * p.Nw + p.N + n] = __float2bfloat16(u);
-            } else {
-                const float g = da * activate_slope(z0, p.act);
-                sum[0] += g;
-                p.dz[d * p.Nw + n] = __float2bfloat16(g);
-            }
-        }
-        if (p.dbias) {
-            p.dbias[static_cast<int64_t>(e) * p.Nw + n] = sum[0];
-            if (gated) p.dbias[static_cast<int64_t>(e) * p.Nw + p.N + n] = sum[1];
-        }
-    }
-    if (p.d_row_weight && blockIdx.x == 0)
-        for (int r = threadIdx.x / 32; r < cnt; r += 8) {
-            const int64_t d = first + r;
-            float s = 0.0f;
-            for (int c = threadIdx.x & 31; c < p.N; c += 32) {
-                const float z0 = bf(p.z, d * p.Nw + c);
-                s += bf(p.dy, d * p.N + c) *
-                     (gated ? silu(z0) * bf(p.z, d * p.Nw + p.N + c) : activate(z0, p.act));
-            }
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if ((threadIdx.x & 31) == 0) p.d_row_weight[d] = s;
-        }
-}
-
-// grid (column tiles of K, E, row tiles of Nw)
-__global__ void __launch_bounds__(256) dw_kernel(const __grid_constant__ ExpertBackwardParams p) {
-    const int e = blockIdx.y, n0 = blockIdx.x * kT, m0 = blockIdx.z * kT;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    int64_t first;
-    const int cnt = expert_rows(p.expert_offset, p.counts, e, p.rows, &first, p.status);
-    float acc[4][4] = {};
-    tile_product(
-        acc, cnt, [&](int r, int64_t k) { return m0 + r < p.Nw ? bf(p.dz, (first + k) * p.Nw + m0 + r) : 0.0f; },
-        [&](int c, int64_t k) { return n0 + c < p.K ? bf(p.x, (first + k) * p.K + n0 + c) : 0.0f; });
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int m = m0 + 4 * ty + i, n = n0 + 4 * tx + j;
-            if (m < p.Nw && n < p.K)
-                p.dw[(static_cast<int64_t>(e) * p.Nw + m) * p.K + n] = __float2bfloat16(acc[i][j]);
-        }
-}
-
 }  // namespace
 
 cudaError_t launch_expert_gemm(const ExpertGemmParams& p, bool fp8, cudaStream_t stream) {
     if (!fp8) return launch_expert_gemm_bf16(p, stream);
     const dim3 grid((p.N + kT - 1) / kT, p.E);
     product_kernel<true><<<grid, 256, 0, stream>>>(p);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_expert_backward(const ExpertBackwardParams& p, cudaStream_t stream) {
-    activation_backward_kernel<<<dim3((p.N + 255) / 256, p.E), 256, 0, stream>>>(p);
-    if (p.dx) {
-        const cudaError_t e = launch_input_grad(p, p.dz, stream);
-        if (e != cudaSuccess) return e;
-    }
-    if (p.dw) dw_kernel<<<dim3((p.K + kT - 1) / kT, p.E, (p.Nw + kT - 1) / kT), 256, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -42,7 +42,8 @@ struct ExpertBackwardParams {
     float* dbias;                // [E][Nw] or null
     float* d_row_weight;         // [rows] or null
     __nv_bfloat16* dz;           // workspace [rows][Nw]
-    float* bias_part;            // workspace [row tiles][Nw]
+    float* bias_part;            // workspace [row tiles][Nw]: sums of dz over a tile's rows
+    float* weight_part;          // workspace [strips][rows]: sums of dy * a over a strip's columns
     int32_t* status;
 };
 
@@ -69,19 +70,22 @@ cudaError_t launch_few_tokens(const FewTokensParams& p, cudaStream_t stream);
 // The parts of these on the tensor cores.
 cudaError_t launch_expert_gemm_bf16(const ExpertGemmParams& p, cudaStream_t stream);
 cudaError_t launch_input_grad(const ExpertBackwardParams& p, const __nv_bfloat16* dz, cudaStream_t stream);
+cudaError_t launch_weight_grad(const ExpertBackwardParams& p, const __nv_bfloat16* dz, cudaStream_t stream);
 
 // Workspace carve-ups shared by the size queries and the calls.
 constexpr int kBackwardTileRows = 64;   // rows of one partial column sum of dz
+constexpr int kBackwardStrip = 512;     // columns of one partial row sum
 struct BackwardWorkspace {
-    size_t off_dz, off_part, total;
+    size_t off_dz, off_part, off_weight, total;
 };
-inline BackwardWorkspace backward_workspace(int64_t rows, int Nw, int E) {
+inline BackwardWorkspace backward_workspace(int64_t rows, int N, int Nw, int E) {
     const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     const size_t tiles = static_cast<size_t>(rows) / kBackwardTileRows + E;
     BackwardWorkspace b;
     b.off_dz = 0;
     b.off_part = up(static_cast<size_t>(rows) * Nw * 2);
-    b.total = b.off_part + up(tiles * Nw * 4) + 256;
+    b.off_weight = b.off_part + up(tiles * Nw * 4);
+    b.total = b.off_weight + up((static_cast<size_t>(N) + kBackwardStrip - 1) / kBackwardStrip * rows * 4) + 256;
     return b;
 }
 struct FewWorkspace {
@@ -137,6 +141,28 @@ __device__ __forceinline__ int expert_rows(const int32_t* offset, const int32_t*
         return static_cast<int>(rows - o);
     }
     return static_cast<int>(c);
+}
+
+// Inclusive scan of f(e) over the experts into out[e], by all threads of a
+// block of kThreads; warp_sum has a word for each warp.
+template <int kThreads, class F>
+__device__ __forceinline__ void scan_experts(int E, int* out, int* warp_sum, F f) {
+    const int each = (E + kThreads - 1) / kThreads, e0 = threadIdx.x * each;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    int sum = 0;
+    for (int i = 0; i < each; ++i)
+        if (e0 + i < E) sum += f(e0 + i);
+    const int incl = warp_inclusive_scan(sum);
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int run = incl - sum;
+    for (int w = 0; w < warp; ++w) run += warp_sum[w];
+    for (int i = 0; i < each; ++i)
+        if (e0 + i < E) {
+            run += f(e0 + i);
+            out[e0 + i] = run;
+        }
+    __syncthreads();
 }
 
 }  // namespace epg

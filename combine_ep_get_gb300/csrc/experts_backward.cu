@@ -1,0 +1,230 @@
+// Gradients of the experts' product: the activation's backward pass with the
+// bias' and the row weights' gradients, then the two matrix products
+// (experts_mma.cu).
+//
+// The activation's pass reads dy and z and writes dz, each once: it is bound
+// by memory.  A block takes 64 rows of one expert x 512 columns (a strip),
+// each thread 8 neighbouring columns (16-byte loads and stores) of every
+// fourth row.  The bias' gradient is the sum of dz down the rows: 64 rows in
+// a block's registers, before dz is rounded, the blocks' sums then added in
+// order by a second kernel.  The row weights' gradient is the sum along a row
+// of dy * act(z): a strip's sum by shuffles, the strips' sums added in order
+// by the same second kernel.  No atomics: results do not depend on timing.
+#include "experts.cuh"
+
+namespace epg {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVecs = kBackwardStrip / 8;      // 8-column vectors of a strip
+constexpr int kRowLanes = kThreads / kVecs;    // rows at a time
+
+__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+struct Tables {
+    int* tile_end;   // [E] row tiles of experts 0 .. e
+    int* first;
+    int* count;
+};
+
+__device__ __forceinline__ Tables row_tables(const ExpertBackwardParams& p, int* smem, int* warp_sum) {
+    Tables t;
+    t.tile_end = smem;
+    t.first = smem + p.E;
+    t.count = t.first + p.E;
+    for (int e = threadIdx.x; e < p.E; e += kThreads) {
+        int64_t first;
+        t.count[e] = expert_rows(p.expert_offset, p.counts, e, p.rows, &first, p.status);
+        t.first[e] = static_cast<int>(first);
+    }
+    __syncthreads();
+    scan_experts<kThreads>(p.E, t.tile_end, warp_sum,
+                           [&](int e) { return (t.count[e] + kBackwardTileRows - 1) / kBackwardTileRows; });
+    return t;
+}
+
+template <bool kGated>
+__global__ void __launch_bounds__(kThreads) activation_backward_kernel(const __grid_constant__ ExpertBackwardParams p) {
+    extern __shared__ int tables[];
+    __shared__ int warp_sum[kThreads / 32];
+    __shared__ float sums[kRowLanes][kBackwardStrip];
+    __shared__ float row_sum[kBackwardTileRows][kVecs / 32];
+    pdl_wait();
+    pdl_launch_dependents();
+    const Tables t = row_tables(p, tables, warp_sum);
+    const int strips = (p.N + kBackwardStrip - 1) / kBackwardStrip;
+    const int row_tiles = t.tile_end[p.E - 1];
+    const int vec = threadIdx.x % kVecs, row_lane = threadIdx.x / kVecs;
+    const bool need_z = p.act != EP_ACT_NONE || p.d_row_weight;
+    for (int64_t g = blockIdx.x; g < static_cast<int64_t>(row_tiles) * strips; g += gridDim.x) {
+        const int tile = static_cast<int>(g / strips), strip = static_cast<int>(g % strips);
+        int lo = 0, hi = p.E - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (t.tile_end[mid] > tile)
+                hi = mid;
+            else
+                lo = mid + 1;
+        }
+        const int row0 = (tile - (lo > 0 ? t.tile_end[lo - 1] : 0)) * kBackwardTileRows;
+        const int rows = min(kBackwardTileRows, t.count[lo] - row0);
+        const int64_t first = static_cast<int64_t>(t.first[lo]) + row0;
+        const int n = strip * kBackwardStrip + vec * 8;
+        float sum[kGated ? 2 : 1][8] = {};
+        for (int r = row_lane; r < kBackwardTileRows; r += kRowLanes) {
+            const int64_t d = first + r;
+            float dot = 0.0f;
+            if (r < rows && n < p.N && EP_IN(d, p.rows)) {
+                float dy[8], z[8], u[8], dz[8], du[8];
+                unpack8(ld_stream_v4(p.dy + d * p.N + n), dy);
+                if (need_z) unpack8(ld_stream_v4(p.z + d * p.Nw + n), z);
+                if (kGated) unpack8(ld_stream_v4(p.z + d * p.Nw + p.N + n), u);
+                const float w = p.row_weight ? p.row_weight[d] : 1.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float da = dy[i] * w;
+                    if (kGated) {
+                        const float s = 1.0f / (1.0f + expf(-z[i])), a = z[i] * s;
+                        dz[i] = da * u[i] * (s * (1.0f + z[i] * (1.0f - s)));
+                        du[i] = da * a;
+                        sum[kGated ? 1 : 0][i] += du[i];
+                        dot = fmaf(dy[i], a * u[i], dot);
+                    } else {
+                        dz[i] = p.act == EP_ACT_NONE ? da : da * activate_slope(z[i], p.act);
+                        if (p.d_row_weight) dot = fmaf(dy[i], activate(z[i], p.act), dot);
+                    }
+                    sum[0][i] += dz[i];
+                }
+                if (p.dz) {
+                    st_v4(p.dz + d * p.Nw + n, pack8(dz));
+                    if (kGated) st_v4(p.dz + d * p.Nw + p.N + n, pack8(du));
+                }
+            }
+            if (p.d_row_weight) {
+                for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                if ((threadIdx.x & 31) == 0) row_sum[r][vec / 32] = dot;
+            }
+        }
+        if (p.d_row_weight) {
+            __syncthreads();
+            if (threadIdx.x < rows && EP_IN(first + threadIdx.x, p.rows))
+                p.weight_part[strip * p.rows + first + threadIdx.x] = row_sum[threadIdx.x][0] + row_sum[threadIdx.x][1];
+        }
+        if (p.dbias)
+            for (int half = 0; half < (kGated ? 2 : 1); ++half) {
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sums[row_lane][vec * 8 + i] = sum[half][i];
+                __syncthreads();
+                for (int c = threadIdx.x; c < kBackwardStrip; c += kThreads)
+                    if (strip * kBackwardStrip + c < p.N) {
+                        float v = 0.0f;
+                        for (int i = 0; i < kRowLanes; ++i) v += sums[i][c];
+                        p.bias_part[static_cast<int64_t>(tile) * p.Nw + half * p.N + strip * kBackwardStrip + c] = v;
+                    }
+            }
+        __syncthreads();
+    }
+}
+
+// The partial sums, in order: blocks of 32 columns of every expert's dbias,
+// then row_blocks blocks for every expert's rows of d_row_weight.
+constexpr int kSumColumns = 32;
+__global__ void __launch_bounds__(kThreads) backward_sums_kernel(const __grid_constant__ ExpertBackwardParams p,
+                                                                 int bias_blocks, int row_blocks) {
+    __shared__ int warp_sum[kThreads / 32];
+    __shared__ float sums[kThreads / kSumColumns][kSumColumns];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int column_blocks = (p.Nw + kSumColumns - 1) / kSumColumns;
+    int64_t first;
+    if (static_cast<int>(blockIdx.x) >= bias_blocks) {
+        const int block = blockIdx.x - bias_blocks, e = block / row_blocks;
+        const int cnt = expert_rows(p.expert_offset, p.counts, e, p.rows, &first, p.status);
+        const int strips = (p.N + kBackwardStrip - 1) / kBackwardStrip;
+        for (int r = block % row_blocks * kThreads + threadIdx.x; r < cnt; r += row_blocks * kThreads) {
+            float v = 0.0f;
+            for (int i = 0; i < strips; ++i) v += p.weight_part[i * p.rows + first + r];
+            if (EP_IN(first + r, p.rows)) p.d_row_weight[first + r] = v;
+        }
+        return;
+    }
+    const int e = blockIdx.x / column_blocks, c = threadIdx.x % kSumColumns, part = threadIdx.x / kSumColumns;
+    const int n = blockIdx.x % column_blocks * kSumColumns + c;
+    // row tiles of the experts before this one
+    int before = 0;
+    for (int i = threadIdx.x; i < e; i += kThreads)
+        before += (expert_rows(p.expert_offset, p.counts, i, p.rows, &first, p.status) + kBackwardTileRows - 1) /
+                  kBackwardTileRows;
+    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x / 32] = before;
+    __syncthreads();
+    before = 0;
+    for (int w = 0; w < kThreads / 32; ++w) before += warp_sum[w];
+    const int tiles = (expert_rows(p.expert_offset, p.counts, e, p.rows, &first, p.status) + kBackwardTileRows - 1) /
+                      kBackwardTileRows;
+    float v = 0.0f;
+    if (n < p.Nw)
+#pragma unroll 8
+        for (int i = part; i < tiles; i += kThreads / kSumColumns)
+            v += p.bias_part[static_cast<int64_t>(before + i) * p.Nw + n];
+    sums[part][c] = v;
+    __syncthreads();
+    if (part == 0 && n < p.Nw) {
+        v = 0.0f;
+        for (int i = 0; i < kThreads / kSumColumns; ++i) v += sums[i][c];
+        p.dbias[static_cast<int64_t>(e) * p.Nw + n] = v;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_expert_backward(const ExpertBackwardParams& given, cudaStream_t stream) {
+    ExpertBackwardParams p = given;
+    // without activation and row weight dz is dy
+    const bool plain = p.act == EP_ACT_NONE && !p.row_weight;
+    const __nv_bfloat16* dz = plain ? p.dy : p.dz;
+    if (plain || (!p.dx && !p.dw)) p.dz = nullptr;
+    if (p.rows > 0 && (p.dz || p.dbias || p.d_row_weight)) {
+        const auto kernel =
+            p.act == EP_ACT_SWIGLU ? activation_backward_kernel<true> : activation_backward_kernel<false>;
+        const int64_t tiles =
+            (p.rows / kBackwardTileRows + p.E) * static_cast<int64_t>((p.N + kBackwardStrip - 1) / kBackwardStrip);
+        const int grid = static_cast<int>(tiles < device_info().num_sms * 4 ? tiles : device_info().num_sms * 4);
+        const cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(kThreads), static_cast<size_t>(p.E) * 12, stream, p);
+        if (e != cudaSuccess) return e;
+    }
+    if (p.dbias || p.d_row_weight) {
+        const int64_t bias_blocks =
+            p.dbias ? static_cast<int64_t>(p.E) * ((p.Nw + kSumColumns - 1) / kSumColumns) : 0;
+        const int row_blocks = p.E < 64 ? 16 : p.E < 1024 ? 1024 / p.E : 1;
+        const int64_t blocks = bias_blocks + (p.d_row_weight ? static_cast<int64_t>(row_blocks) * p.E : 0);
+        if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+        const cudaError_t e = launch_pdl(backward_sums_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0,
+                                         stream, p, static_cast<int>(bias_blocks), row_blocks);
+        if (e != cudaSuccess) return e;
+    }
+    if (p.dx) {
+        const cudaError_t e = launch_input_grad(p, dz, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return p.dw ? launch_weight_grad(p, dz, stream) : cudaSuccess;
+}
+
+}  // namespace epg

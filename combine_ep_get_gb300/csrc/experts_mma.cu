@@ -109,6 +109,7 @@ struct Shape {
 
 struct Barriers {
     uint64_t full[12], empty[12], acc_full[2], acc_empty[2], drain;
+    uint64_t tail_full[4], cleared[4];   // weight gradient: an expert's last stage
     uint32_t tmem;
     int total_tiles;
     int warp_sum[8];
@@ -124,27 +125,6 @@ struct Table {
     int16_t* list;    // few tokens: entries t * K + k, expert by expert
     int16_t* expert;  // few tokens: expert of each entry, -1 for none; behind them, tokens just completed
 };
-
-// Inclusive scan of f(e) over the experts into out[e], by all threads.
-template <class F>
-__device__ void scan_experts(int E, int* out, Barriers* s, F f) {
-    const int each = (E + kThreads - 1) / kThreads, e0 = threadIdx.x * each;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    int sum = 0;
-    for (int i = 0; i < each; ++i)
-        if (e0 + i < E) sum += f(e0 + i);
-    const int incl = warp_inclusive_scan(sum);
-    if (lane == 31) s->warp_sum[warp] = incl;
-    __syncthreads();
-    int run = incl - sum;
-    for (int w = 0; w < warp; ++w) run += s->warp_sum[w];
-    for (int i = 0; i < each; ++i)
-        if (e0 + i < E) {
-            run += f(e0 + i);
-            out[e0 + i] = run;
-        }
-    __syncthreads();
-}
 
 // A tile: expert, its rows [row0, row0 + rows) within the expert, features from f0.
 struct Tile {
@@ -250,8 +230,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
         for (int i = threadIdx.x; i < p.T * p.K; i += kThreads)
             if (t.expert[i] >= 0) atomicAdd(&t.count[t.expert[i]], 1);
         __syncthreads();
-        scan_experts(p.E, t.first, s, [&](int e) { return t.count[e]; });
-        scan_experts(p.E, t.tile_end, s, [&](int e) { return (t.count[e] + NT - 1) / NT; });
+        scan_experts<kThreads>(p.E, t.first, s->warp_sum, [&](int e) { return t.count[e]; });
+        scan_experts<kThreads>(p.E, t.tile_end, s->warp_sum, [&](int e) { return (t.count[e] + NT - 1) / NT; });
         // first[e] now ends expert e's entries; filling from the last entry
         // down turns it into their start
         if (warp == 0)
@@ -273,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
             t.first[e] = static_cast<int>(first);
         }
         __syncthreads();
-        scan_experts(p.E, t.tile_end, s, [&](int e) { return (t.count[e] + NT - 1) / NT; });
+        scan_experts<kThreads>(p.E, t.tile_end, s->warp_sum, [&](int e) { return (t.count[e] + NT - 1) / NT; });
     }
     tcgen05_before_sync();
     __syncthreads();
@@ -550,6 +530,211 @@ int bound_tiles(int64_t row_tiles, int feature_tiles) {
     return v > (1 << 20) ? 1 << 20 : static_cast<int>(v);
 }
 
+// ---------------------------------------------------------------------------
+// Weight gradient: dW[e][n, k] = sum over e's rows of dz[row, n] * x[row, k].
+// Both operands are read as they lie, rows of the sum outermost (MN-major
+// descriptors), 128 n x 256 k a tile.  The last stage of an expert may hold
+// rows of the next one, or padding with anything in it: two warps clear those
+// rows of both operands in shared memory before the MMAs read them.
+// ---------------------------------------------------------------------------
+
+constexpr int kGradK = 256;      // columns of a tile
+
+struct GradArgs {
+    CUtensorMap dz, x;           // boxes of 64 columns x 64 rows
+    int Nw, K, E;
+    int64_t rows;
+    const int32_t* expert_offset;
+    const int32_t* counts;
+    __nv_bfloat16* dw;           // [E][Nw][K]
+    int32_t* status;
+};
+
+struct GradShape {
+    static constexpr int kStageBytes = (kM + kGradK) * kDepth * 2;
+    static constexpr int kStages = 4;
+    static constexpr int kColumns = 2 * kGradK;
+};
+
+__global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_constant__ GradArgs p) {
+    using S = GradShape;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* stages = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
+    Barriers* s = reinterpret_cast<Barriers*>(stages + S::kStages * S::kStageBytes);
+    int* s_first = reinterpret_cast<int*>(s + 1);
+    int* s_count = s_first + p.E;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int n_tiles = (p.Nw + kM - 1) / kM, k_tiles = (p.K + kGradK - 1) / kGradK;
+    const int tiles = p.E * n_tiles * k_tiles;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&s->full[i], 1);
+            mbar_init(&s->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s->acc_full[i], 1);
+            mbar_init(&s->acc_empty[i], 4);
+        }
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&s->tail_full[i], 1);
+            mbar_init(&s->cleared[i], 2);
+        }
+        mbar_init(&s->drain, 1);
+        fence_mbar_init();
+        prefetch_map(&p.dz);
+        prefetch_map(&p.x);
+    }
+    if (warp == 2) tmem_alloc<1>(&s->tmem, S::kColumns);
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int e = threadIdx.x; e < p.E; e += kThreads) {
+        int64_t first;
+        s_count[e] = expert_rows(p.expert_offset, p.counts, e, p.rows, &first, p.status);
+        s_first[e] = static_cast<int>(first);
+    }
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    const uint32_t tmem = s->tmem;
+    const auto expert_of = [&](int g) { return g / (n_tiles * k_tiles); };
+    const auto n0_of = [&](int g) { return g % (n_tiles * k_tiles) % n_tiles * kM; };
+    const auto k0_of = [&](int g) { return g % (n_tiles * k_tiles) / n_tiles * kGradK; };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            uint32_t tail_bits = 0, full_bits = 0, last_tail = 0;   // parities of the stages' next loads
+            bool ok = true;
+            for (int g = blockIdx.x; g < tiles && ok; g += gridDim.x) {
+                const int e = expert_of(g), n0 = n0_of(g), k0 = k0_of(g), cnt = s_count[e], first = s_first[e];
+                const int a_boxes = min(2, (p.Nw - n0 + 63) / 64), b_boxes = min(4, (p.K - k0 + 63) / 64);
+                for (int r = 0; r < cnt; r += kDepth, ++it) {
+                    const int st = it % S::kStages;
+                    ok = mbar_wait_bounded(&s->empty[st], ((it / S::kStages) & 1) ^ 1);
+                    if (!ok) break;
+                    uint8_t* sa = stages + st * S::kStageBytes;
+                    const bool tail = r + kDepth > cnt;
+                    uint64_t* const full = tail ? &s->tail_full[st] : &s->full[st];
+                    (tail ? tail_bits : full_bits) ^= 1u << st;
+                    last_tail = (last_tail & ~(1u << st)) | (static_cast<uint32_t>(tail) << st);
+                    const uint32_t bar = smem_addr(full);
+                    mbar_arrive_expect_tx(full, (a_boxes + b_boxes) * 8192);
+                    for (int i = 0; i < a_boxes; ++i) tma_load_2d<1>(sa + i * 8192, &p.dz, bar, n0 + 64 * i, first + r);
+                    for (int i = 0; i < b_boxes; ++i)
+                        tma_load_2d<1>(sa + kABytes + i * 8192, &p.x, bar, k0 + 64 * i, first + r);
+                }
+            }
+            if (!ok) atomicOr(p.status, EP_ERR_TIMEOUT);
+            // no copy may still be in flight when the CTA ends
+            for (int st = 0; st < S::kStages && st < it; ++st) {
+                const bool tail = (last_tail >> st) & 1;
+                if (!mbar_wait_bounded(tail ? &s->tail_full[st] : &s->full[st],
+                                       (((tail ? tail_bits : full_bits) >> st) & 1) ^ 1))
+                    break;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = instr_desc(false, true, true, kM, kGradK);
+            int it = 0, n = 0;
+            uint32_t tail_bits = 0, full_bits = 0;
+            bool ok = true;
+            for (int g = blockIdx.x; g < tiles && ok; g += gridDim.x) {
+                const int cnt = s_count[expert_of(g)];
+                if (cnt == 0) continue;
+                const uint32_t d = tmem + (n & 1) * kGradK;
+                ok = mbar_wait_bounded(&s->acc_empty[n & 1], ((n / 2) & 1) ^ 1);
+                tcgen05_after_sync();
+                for (int r = 0; r < cnt && ok; r += kDepth, ++it) {
+                    const int st = it % S::kStages;
+                    const bool tail = r + kDepth > cnt;
+                    ok = mbar_wait_bounded(tail ? &s->cleared[st] : &s->full[st],
+                                           ((tail ? tail_bits : full_bits) >> st) & 1);
+                    (tail ? tail_bits : full_bits) ^= 1u << st;
+                    if (!ok) break;
+                    tcgen05_after_sync();
+                    const uint32_t sa = smem_addr(stages + st * S::kStageBytes), sb = sa + kABytes;
+#pragma unroll
+                    for (int k = 0; k < kDepth / 16; ++k)
+                        mma<1, false>(d, operand_desc(sa + k * 2048, 8192), operand_desc(sb + k * 2048, 8192), idesc,
+                                      r > 0 || k > 0);
+                    mma_commit<1>(&s->empty[st]);
+                }
+                if (ok) mma_commit<1>(&s->acc_full[n & 1]);
+                ++n;
+            }
+            if (!ok) {
+                atomicOr(p.status, EP_ERR_TIMEOUT);
+                mma_commit<1>(&s->drain);
+                mbar_wait_bounded(&s->drain, 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        int it = 0;
+        uint32_t tail_bits = 0;
+        for (int g = blockIdx.x; g < tiles; g += gridDim.x) {
+            const int cnt = s_count[expert_of(g)], blocks = (cnt + kDepth - 1) / kDepth, valid = cnt % kDepth;
+            it += blocks;
+            if (valid == 0) continue;
+            const int st = (it - 1) % S::kStages;
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&s->tail_full[st], (tail_bits >> st) & 1) ? 1 : 0)) {
+                atomicOr(p.status, EP_ERR_TIMEOUT);
+                break;
+            }
+            tail_bits ^= 1u << st;
+            // whole 128-byte rows of every 64-column box, so the swizzle does not matter
+            const int clear = (kDepth - valid) * 8;
+            uint8_t* base = stages + st * S::kStageBytes + valid * 128;
+            for (int box = 0; box < (kM + kGradK) / 64; ++box)
+                for (int i = (warp - 2) * 32 + lane; i < clear; i += 64)
+                    *reinterpret_cast<uint4*>(base + box * 8192 + i * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s->cleared[st]);
+        }
+    } else {
+        const int q = warp - 4;
+        int n = 0;
+        for (int g = blockIdx.x; g < tiles; g += gridDim.x) {
+            const int e = expert_of(g), n0 = n0_of(g), k0 = k0_of(g), cnt = s_count[e];
+            const int row = n0 + q * 32 + lane;
+            __nv_bfloat16* out = p.dw + (static_cast<int64_t>(e) * p.Nw + row) * p.K + k0;
+            const int columns = row < p.Nw && EP_IN(e, p.E) ? min(kGradK, p.K - k0) : 0;
+            if (cnt == 0) {
+                for (int c = 0; c < columns; c += 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&s->acc_full[n & 1], (n / 2) & 1) ? 1 : 0)) {
+                atomicOr(p.status, EP_ERR_TIMEOUT);
+                break;
+            }
+            tcgen05_after_sync();
+            const uint32_t acc = tmem + (n & 1) * kGradK + (static_cast<uint32_t>(q * 32) << 16);
+            for (int c0 = 0; c0 < kGradK; c0 += 32) {
+                float v[32];
+                __syncwarp();
+                tmem_load32(acc + c0, v);
+                if (c0 + 32 == kGradK) {
+                    tcgen05_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s->acc_empty[n & 1]);
+                }
+#pragma unroll
+                for (int c = 0; c < 32; c += 8)
+                    if (c0 + c < columns)
+                        st_v4(out + c0 + c, make_uint4(pack2(v[c], v[c + 1]), pack2(v[c + 2], v[c + 3]),
+                                                       pack2(v[c + 4], v[c + 5]), pack2(v[c + 6], v[c + 7])));
+            }
+            ++n;
+        }
+    }
+    __syncthreads();
+    if (warp == 2) tmem_free<1>(tmem, S::kColumns);
+}
+
 }  // namespace
 
 cudaError_t launch_expert_gemm_bf16(const ExpertGemmParams& p, cudaStream_t stream) {
@@ -591,6 +776,31 @@ cudaError_t launch_input_grad(const ExpertBackwardParams& p, const __nv_bfloat16
     a.y = p.dx;
     a.status = p.status;
     return launch<kInputGrad, NT>(a, bound_tiles(p.rows / NT + p.E, (p.K + kM - 1) / kM), stream);
+}
+
+cudaError_t launch_weight_grad(const ExpertBackwardParams& p, const __nv_bfloat16* dz, cudaStream_t stream) {
+    GradArgs a{};
+    // no rows: nothing is loaded, but a map needs an extent
+    const int64_t rows = std::max<int64_t>(p.rows, 1);
+    if (!row_map(&a.dz, p.rows > 0 ? dz : p.dw, rows, p.Nw, kDepth) ||
+        !row_map(&a.x, p.rows > 0 ? p.x : p.dw, rows, p.K, kDepth))
+        return cudaErrorInvalidValue;
+    a.Nw = p.Nw;
+    a.K = p.K;
+    a.E = p.E;
+    a.rows = p.rows;
+    a.expert_offset = p.expert_offset;
+    a.counts = p.counts;
+    a.dw = p.dw;
+    a.status = p.status;
+    const size_t smem = 1024 + GradShape::kStages * GradShape::kStageBytes + sizeof(Barriers) + 8 * p.E;
+    cudaError_t e = cudaFuncSetAttribute(weight_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = static_cast<int64_t>(p.E) * ((p.Nw + kM - 1) / kM) * ((p.K + kGradK - 1) / kGradK);
+    if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+    const int grid = static_cast<int>(std::min<int64_t>(device_info().num_sms, tiles));
+    return launch_pdl(weight_grad_kernel, dim3(grid), dim3(kThreads), smem, stream, a);
 }
 
 cudaError_t launch_few_tokens(const FewTokensParams& p, cudaStream_t stream) {
