@@ -15,9 +15,9 @@
 // stage; warp 1 issues the MMAs; warps 4-7 read the accumulators, lane =
 // feature, and apply the epilogue.
 //
-// SWIGLU: the 128 features of a tile are, for every 32 lanes, 16 gate rows
-// and the 16 up rows that belong to them, so one exchange across half a warp
-// brings each pair together.
+// SWIGLU: the 128 features of a tile are, in turns, 8 gate rows and the 8 up
+// rows that belong to them (one box of a five-dimensional map), so one
+// exchange between lanes 8 apart brings each pair together.
 #include <algorithm>
 
 #include "experts.cuh"
@@ -297,11 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
                         tma_load_3d<1>(sa, &p.a, bar, r.f0, kb * kDepth, r.e);
                         tma_load_3d<1>(sa + kABytes / 2, &p.a, bar, r.f0 + 64, kb * kDepth, r.e);
                     } else if (p.gate_half) {
-                        for (int i = 0; i < 4; ++i) {
-                            tma_load_3d<1>(sa + i * 4096, &p.a, bar, kb * kDepth, r.f0 + 16 * i, r.e);
-                            tma_load_3d<1>(sa + i * 4096 + 2048, &p.a, bar, kb * kDepth, p.gate_half + r.f0 + 16 * i,
-                                           r.e);
-                        }
+                        tma_load_5d<1>(sa, &p.a, bar, kb * kDepth, 0, 0, r.f0 / 8, r.e);
                     } else {
                         tma_load_3d<1>(sa, &p.a, bar, kb * kDepth, r.f0, r.e);
                     }
@@ -379,8 +375,9 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
             tcgen05_after_sync();
             const bool gated = p.gate_half != 0;
             // this lane's row of W within the expert, and its feature of y
-            const int f = gated ? r.f0 + q * 16 + (lane & 15) : r.f0 + q * 32 + lane;
-            const int wrow = gated && lane >= 16 ? p.gate_half + f : f;
+            const bool up = gated && (lane & 8);
+            const int f = gated ? r.f0 + q * 16 + (lane / 16) * 8 + (lane & 7) : r.f0 + q * 32 + lane;
+            const int wrow = up ? p.gate_half + f : f;
             const int Fw = gated ? 2 * p.F : p.F;
             const bool f_ok = f < p.F;
             const float bias = p.bias && f_ok ? p.bias[static_cast<int64_t>(r.e) * Fw + wrow] : 0.0f;
@@ -414,33 +411,55 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
                             *reinterpret_cast<uint32_t*>(p.z + row_of(c) * Fw + (wrow & ~1)) = pack2(w.x, w.y);
                     }
                 }
-                const auto store = [&](int c, int feature, float2 a) {
-                    if (c >= r.rows || feature >= p.F || !EP_IN(row_of(c), p.rows)) return;
-                    const int64_t d = row_of(c), at = d * p.F + feature;
-                    if (kMode == kProduct) {
-                        if (p.row_weight) {
-                            const float w = p.row_weight[d];
-                            a.x *= w;
-                            a.y *= w;
-                        }
-                        if (p.residual) {
-                            const float2 b = unpack2(*reinterpret_cast<const uint32_t*>(p.residual + at));
-                            a.x += b.x;
-                            a.y += b.y;
-                        }
+                // What each of the lane's 16 pairs of features adds and is
+                // scaled by, all asked for before the first store: the
+                // residual may be y itself, so a load would have to wait for
+                // the stores before it.
+                const auto column = [&](int i) {   // of pair i
+                    return gated ? c0 + 4 * i + (up ? 1 : 0) + 2 * (lane & 1) : c0 + 2 * i + (lane & 1);
+                };
+                const int pairs = gated ? 8 : 16;
+                uint32_t add[16];
+                float scale[16];
+                if (kMode == kProduct && p.residual) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (i < pairs)
+                            add[i] = column(i) < r.rows && f_ok && EP_IN(row_of(column(i)), p.rows)
+                                         ? *reinterpret_cast<const uint32_t*>(p.residual + row_of(column(i)) * p.F + (f & ~1))
+                                         : 0u;
+                }
+                if (kMode == kProduct && p.row_weight) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (i < pairs)
+                            scale[i] = column(i) < r.rows && EP_IN(row_of(column(i)), p.rows)
+                                           ? p.row_weight[row_of(column(i))]
+                                           : 0.0f;
+                }
+                const auto store = [&](int i, float2 a) {
+                    if (kMode == kProduct && p.row_weight) {
+                        a.x *= scale[i];
+                        a.y *= scale[i];
                     }
-                    *reinterpret_cast<uint32_t*>(p.y + at) = pack2(a.x, a.y);
+                    if (kMode == kProduct && p.residual) {
+                        const float2 b = unpack2(add[i]);
+                        a.x += b.x;
+                        a.y += b.y;
+                    }
+                    const int c = column(i);
+                    if (c < r.rows && f_ok && EP_IN(row_of(c), p.rows))
+                        *reinterpret_cast<uint32_t*>(p.y + row_of(c) * p.F + (f & ~1)) = pack2(a.x, a.y);
                 };
                 if (kMode != kInputGrad && gated) {
-                    const bool up = lane >= 16;
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
-                        // lanes 0-15 take token j (then j + 2), lanes 16-31 token j + 1 (j + 3)
-                        const float g0 = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + 1], 16);
-                        const float g1 = __shfl_xor_sync(0xffffffffu, up ? v[j + 2] : v[j + 3], 16);
+                        // gate lanes take token j (then j + 2), up lanes token j + 1 (j + 3)
+                        const float g0 = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + 1], 8);
+                        const float g1 = __shfl_xor_sync(0xffffffffu, up ? v[j + 2] : v[j + 3], 8);
                         const float a0 = up ? silu(g0) * v[j + 1] : silu(v[j]) * g0;
                         const float a1 = up ? silu(g1) * v[j + 3] : silu(v[j + 2]) * g1;
-                        store(c0 + j + (up ? 1 : 0) + 2 * (lane & 1), f & ~1, trade_pair(a0, a1, lane));
+                        store(j / 4, trade_pair(a0, a1, lane));
                     }
                 } else {
                     if (kMode != kInputGrad && p.act != EP_ACT_NONE) {
@@ -448,8 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
                         for (int j = 0; j < 32; ++j) v[j] = activate(v[j], p.act);
                     }
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2)
-                        store(c0 + j + (lane & 1), f & ~1, trade_pair(v[j], v[j + 1], lane));
+                    for (int j = 0; j < 32; j += 2) store(j / 2, trade_pair(v[j], v[j + 1], lane));
                 }
             }
             if (kMode == kFewDown) {
@@ -517,6 +535,15 @@ bool weight_map(CUtensorMap* m, const void* w, int E, int rows, int cols, int bo
     const uint64_t strides[2] = {static_cast<uint64_t>(cols) * 2, static_cast<uint64_t>(cols) * rows * 2};
     const uint32_t boxes[3] = {kDepth, static_cast<uint32_t>(box), 1};
     return encode_map(m, false, 3, w, dims, strides, boxes);
+}
+// Gate and up rows in turns of 8, for tiles of 64 + 64 rows (see above).
+bool gated_map(CUtensorMap* m, const void* w, int E, int n, int cols) {
+    const uint64_t pitch = static_cast<uint64_t>(cols) * 2, half = pitch * n;
+    const uint64_t dims[5] = {static_cast<uint64_t>(cols), 8, 2, static_cast<uint64_t>(n / 8),
+                              static_cast<uint64_t>(E)};
+    const uint64_t strides[4] = {pitch, half, 8 * pitch, 2 * half};
+    const uint32_t boxes[5] = {kDepth, 8, 2, kM / 16, 1};
+    return encode_map(m, false, 5, w, dims, strides, boxes);
 }
 bool row_map(CUtensorMap* m, const void* x, int64_t rows, int cols, int box) {
     const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)};
@@ -741,7 +768,7 @@ cudaError_t launch_expert_gemm_bf16(const ExpertGemmParams& p, cudaStream_t stre
     constexpr int NT = 256;
     MmaArgs a{};
     const bool gated = p.act == EP_ACT_SWIGLU;
-    if (!weight_map(&a.a, p.w, p.E, p.Nw, p.K, gated ? 16 : kM) ||
+    if (!(gated ? gated_map(&a.a, p.w, p.E, p.N, p.K) : weight_map(&a.a, p.w, p.E, p.Nw, p.K, kM)) ||
         !row_map(&a.b, p.x, p.rows, p.K, Shape<NT>::kBoxRows))
         return cudaErrorInvalidValue;
     a.depth = p.K;
@@ -807,7 +834,8 @@ cudaError_t launch_few_tokens(const FewTokensParams& p, cudaStream_t stream) {
     constexpr int NT = 64;
     MmaArgs up{};
     const bool gated = p.act == EP_ACT_SWIGLU;
-    if (!weight_map(&up.a, p.w_up, p.E, p.Nw, p.H, gated ? 16 : kM) || !row_map(&up.b, p.x, p.T, p.H, 1))
+    if (!(gated ? gated_map(&up.a, p.w_up, p.E, p.I, p.H) : weight_map(&up.a, p.w_up, p.E, p.Nw, p.H, kM)) ||
+        !row_map(&up.b, p.x, p.T, p.H, 1))
         return cudaErrorInvalidValue;
     up.depth = p.H;
     up.F = p.I;

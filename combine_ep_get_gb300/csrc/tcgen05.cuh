@@ -59,6 +59,18 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uin
             "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::
                 "r"(smem_addr(dst)), "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
 }
+template <int kCtas>
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z, int u,
+                                            int v) {
+    if (kCtas == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::
+                "r"(smem_addr(dst)), "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v) : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::
+                "r"(smem_addr(dst)), "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v) : "memory");
+}
 // Four rows of a map whose box is one row high, by their indices.
 __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* m, uint32_t bar, int x, int r0, int r1,
                                             int r2, int r3) {
