@@ -785,9 +785,9 @@ ep_status_t ep_expert_gemm(const void* x, const float* x_sf, int sf_col_major, c
     p.y = static_cast<__nv_bfloat16*>(y);
     p.z = static_cast<__nv_bfloat16*>(z);
     p.status = d_status;
-    return epg::launch_expert_gemm(p, fp8, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
-               ? EP_OK
-               : EP_RET(EP_ERR_CUDA);
+    const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+    const cudaError_t e = fp8 ? epg::launch_expert_gemm_fp8(p, stream) : epg::launch_expert_gemm_bf16(p, stream);
+    return e == cudaSuccess ? EP_OK : EP_RET(EP_ERR_CUDA);
 }
 
 size_t ep_expert_gemm_backward_workspace_bytes(int64_t num_rows, int n_dim, int num_experts, int activation) {

@@ -64,10 +64,10 @@ struct FewTokensParams {
     int32_t* status;
 };
 
-cudaError_t launch_expert_gemm(const ExpertGemmParams& p, bool fp8, cudaStream_t stream);
 cudaError_t launch_expert_backward(const ExpertBackwardParams& p, cudaStream_t stream);
 cudaError_t launch_few_tokens(const FewTokensParams& p, cudaStream_t stream);
 // The parts of these on the tensor cores.
+cudaError_t launch_expert_gemm_fp8(const ExpertGemmParams& p, cudaStream_t stream);
 cudaError_t launch_expert_gemm_bf16(const ExpertGemmParams& p, cudaStream_t stream);
 cudaError_t launch_input_grad(const ExpertBackwardParams& p, const __nv_bfloat16* dz, cudaStream_t stream);
 cudaError_t launch_weight_grad(const ExpertBackwardParams& p, const __nv_bfloat16* dz, cudaStream_t stream);

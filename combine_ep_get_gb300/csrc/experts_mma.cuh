@@ -1,0 +1,281 @@
+// What the experts' tensor-core kernels share: tiles, tables, tensor maps and
+// the epilogue of a tile.
+#pragma once
+
+#include <algorithm>
+
+#include "experts.cuh"
+#include "tcgen05.cuh"
+
+namespace epg {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kM = 128;          // features of a tile
+constexpr int kDepth = 64;       // terms of the sum in a stage (128 bytes of bf16)
+constexpr int kABytes = kM * kDepth * 2;
+constexpr int kGroupTiles = 16;  // row tiles whose features are walked together, for the L2
+
+enum Mode { kProduct, kInputGrad, kFewUp, kFewDown };
+
+struct MmaArgs {
+    CUtensorMap a, b;
+    int depth;                    // terms of the sum
+    int F;                        // output features of an expert
+    int gate_half;                // SWIGLU: rows of W from a gate row to its up row (0: not gated)
+    int E, act;
+    int64_t rows;
+    const int32_t* expert_offset;
+    const int32_t* counts;
+    const float* bias;            // [E][F or 2 F]
+    const float* row_weight;
+    const __nv_bfloat16* residual;
+    __nv_bfloat16* y;             // rows of F
+    __nv_bfloat16* z;             // rows of F or 2 F
+    // few tokens
+    const int64_t* topk_idx;
+    const float* topk_weights;
+    int T, K;
+    float* part;                  // [T * K][F]
+    uint32_t* done;               // [feature tiles][T]: experts of a token that are done
+    int done_words;
+    __nv_bfloat16* out;           // [T][F]
+    int32_t* status;
+};
+
+template <int NT>
+struct Shape {
+    static constexpr int kStageBytes = kABytes + NT * kDepth * 2;
+    static constexpr int kStages = (192 * 1024) / kStageBytes < 10 ? (192 * 1024) / kStageBytes : 10;
+    static constexpr int kBoxRows = NT < 64 ? NT : 64;
+    static constexpr int kColumns = 2 * NT < 32 ? 32 : 2 * NT;   // of tensor memory
+};
+
+struct Barriers {
+    uint64_t full[12], empty[12], acc_full[2], acc_empty[2], drain;
+    uint64_t tail_full[4], cleared[4];   // weight gradient: an expert's last stage
+    uint32_t tmem;
+    int total_tiles;
+    int warp_sum[8];
+    int gave_up;                  // a wait of the epilogue ran out
+    int completed;                // few tokens, down: tokens whose last expert this tile was
+};
+
+// Experts' row tiles: tile_end[e] = row tiles of experts 0 .. e.
+struct Table {
+    int* tile_end;    // [E]
+    int* first;       // [E] first row, or first entry of the list
+    int* count;       // [E]
+    int16_t* list;    // few tokens: entries t * K + k, expert by expert
+    int16_t* expert;  // few tokens: expert of each entry, -1 for none; behind them, tokens just completed
+};
+
+// A tile: expert, its rows [row0, row0 + rows) within the expert, features from f0.
+struct Tile {
+    int e, row0, rows, width, f0;
+};
+
+template <int NT>
+__device__ __forceinline__ Tile tile_at(int g, const Table& t, int E, int feature_tiles, int tile_features) {
+    int lo = 0, hi = E - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (static_cast<int64_t>(t.tile_end[mid]) * feature_tiles > g)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    Tile r;
+    r.e = lo;
+    const int before = lo > 0 ? t.tile_end[lo - 1] : 0;
+    const int n = t.tile_end[lo] - before, cnt = t.count[lo];
+    int local = g - before * feature_tiles;
+    const int group = local / (kGroupTiles * feature_tiles);
+    local -= group * kGroupTiles * feature_tiles;
+    const int in_group = min(kGroupTiles, n - group * kGroupTiles);
+    const int f = local / in_group, row_tile = group * kGroupTiles + local % in_group;
+    // few tiles share an expert's rows evenly (each with its weights from L2)
+    const int per = n <= 4 ? ((cnt + n - 1) / n + 15) / 16 * 16 : NT;
+    r.row0 = row_tile * per;
+    r.rows = min(per, cnt - r.row0);
+    r.width = (r.rows + 15) / 16 * 16;
+    r.f0 = f * tile_features;
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+
+// Four-byte stores of two neighbouring features: the lanes of a pair trade
+// so that the even lane holds both features of token j, the odd one of j + 1.
+__device__ __forceinline__ float2 trade_pair(float first, float second, int lane) {
+    const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? first : second, 1);
+    return lane & 1 ? make_float2(got, second) : make_float2(first, got);
+}
+
+// A lane's feature of y and its row of W within the expert.
+struct Lane {
+    int f, wrow;
+    bool up;
+};
+__device__ __forceinline__ Lane lane_of(const MmaArgs& p, const Tile& r, int q, int lane) {
+    Lane l;
+    const bool gated = p.gate_half != 0;
+    l.up = gated && (lane & 8);
+    l.f = gated ? r.f0 + q * 16 + (lane / 16) * 8 + (lane & 7) : r.f0 + q * 32 + lane;
+    l.wrow = l.up ? p.gate_half + l.f : l.f;
+    return l;
+}
+__device__ __forceinline__ float bias_of(const MmaArgs& p, const Tile& r, int q, int lane) {
+    const Lane l = lane_of(p, r, q, lane);
+    const int Fw = p.gate_half ? 2 * p.F : p.F;
+    return p.bias && l.f < p.F ? p.bias[static_cast<int64_t>(r.e) * Fw + l.wrow] : 0.0f;
+}
+
+// The epilogue of 32 of a tile's columns (its rows row0 + c0 ...), lane =
+// feature, q = the warp's 32 lanes of the accumulator.
+template <int kMode>
+__device__ __forceinline__ void finish_columns(const MmaArgs& p, const Table& t, const Tile& r, int first, int q,
+                                               int lane, float bias, int c0, float (&v)[32]) {
+    constexpr bool kFew = kMode == kFewUp || kMode == kFewDown;
+    const Lane l = lane_of(p, r, q, lane);
+    const bool gated = p.gate_half != 0, up = l.up, f_ok = l.f < p.F;
+    const int f = l.f, wrow = l.wrow, Fw = gated ? 2 * p.F : p.F;
+    const auto row_of = [&](int j) -> int64_t {
+        return kFew ? static_cast<int64_t>(t.list[first + j]) : static_cast<int64_t>(first) + j;
+    };
+    if (kMode != kInputGrad)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += bias;
+    if (kMode == kFewDown) {
+#pragma unroll 8
+        for (int j = 0; j < 32; ++j)
+            if (c0 + j < r.rows && f_ok && EP_IN(row_of(c0 + j), p.rows))
+                p.part[row_of(c0 + j) * p.F + f] = v[j];
+        return;
+    }
+    if (kMode == kProduct && p.z) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            const float2 w = trade_pair(v[j], v[j + 1], lane);
+            const int c = c0 + j + (lane & 1);
+            if (c < r.rows && f_ok && EP_IN(row_of(c), p.rows))
+                *reinterpret_cast<uint32_t*>(p.z + row_of(c) * Fw + (wrow & ~1)) = pack2(w.x, w.y);
+        }
+    }
+    // What each of the lane's 16 pairs of features adds and is
+    // scaled by, all asked for before the first store: the
+    // residual may be y itself, so a load would have to wait for
+    // the stores before it.
+    const auto column = [&](int i) {   // of pair i
+        return gated ? c0 + 4 * i + (up ? 1 : 0) + 2 * (lane & 1) : c0 + 2 * i + (lane & 1);
+    };
+    const int pairs = gated ? 8 : 16;
+    uint32_t add[16];
+    float scale[16];
+    if (kMode == kProduct && p.residual) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (i < pairs)
+                add[i] = column(i) < r.rows && f_ok && EP_IN(row_of(column(i)), p.rows)
+                             ? *reinterpret_cast<const uint32_t*>(p.residual + row_of(column(i)) * p.F + (f & ~1))
+                             : 0u;
+    }
+    if (kMode == kProduct && p.row_weight) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (i < pairs)
+                scale[i] = column(i) < r.rows && EP_IN(row_of(column(i)), p.rows)
+                               ? p.row_weight[row_of(column(i))]
+                               : 0.0f;
+    }
+    const auto store = [&](int i, float2 a) {
+        if (kMode == kProduct && p.row_weight) {
+            a.x *= scale[i];
+            a.y *= scale[i];
+        }
+        if (kMode == kProduct && p.residual) {
+            const float2 b = unpack2(add[i]);
+            a.x += b.x;
+            a.y += b.y;
+        }
+        const int c = column(i);
+        if (c < r.rows && f_ok && EP_IN(row_of(c), p.rows))
+            *reinterpret_cast<uint32_t*>(p.y + row_of(c) * p.F + (f & ~1)) = pack2(a.x, a.y);
+    };
+    if (kMode != kInputGrad && gated) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            // gate lanes take token j (then j + 2), up lanes token j + 1 (j + 3)
+            const float g0 = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + 1], 8);
+            const float g1 = __shfl_xor_sync(0xffffffffu, up ? v[j + 2] : v[j + 3], 8);
+            const float a0 = up ? silu(g0) * v[j + 1] : silu(v[j]) * g0;
+            const float a1 = up ? silu(g1) * v[j + 3] : silu(v[j + 2]) * g1;
+            store(j / 4, trade_pair(a0, a1, lane));
+        }
+    } else {
+        if (kMode != kInputGrad && p.act != EP_ACT_NONE) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = activate(v[j], p.act);
+        }
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) store(j / 2, trade_pair(v[j], v[j + 1], lane));
+    }
+}
+
+// Weights [E][rows][cols] as a map of boxes of 128 bytes of columns x `box` rows.
+inline bool weight_map(CUtensorMap* m, const void* w, int E, int rows, int cols, int box, bool fp8 = false) {
+    const uint64_t dims[3] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows), static_cast<uint64_t>(E)};
+    const uint64_t pitch = static_cast<uint64_t>(cols) * (fp8 ? 1 : 2);
+    const uint64_t strides[2] = {pitch, pitch * rows};
+    const uint32_t boxes[3] = {fp8 ? 128u : 64u, static_cast<uint32_t>(box), 1};
+    return encode_map(m, fp8, 3, w, dims, strides, boxes);
+}
+// Gate and up rows in turns of 8, for tiles of 64 + 64 rows (see above).
+inline bool gated_map(CUtensorMap* m, const void* w, int E, int n, int cols, bool fp8 = false) {
+    const uint64_t pitch = static_cast<uint64_t>(cols) * (fp8 ? 1 : 2), half = pitch * n;
+    const uint64_t dims[5] = {static_cast<uint64_t>(cols), 8, 2, static_cast<uint64_t>(n / 8),
+                              static_cast<uint64_t>(E)};
+    const uint64_t strides[4] = {pitch, half, 8 * pitch, 2 * half};
+    const uint32_t boxes[5] = {fp8 ? 128u : 64u, 8, 2, kM / 16, 1};
+    return encode_map(m, fp8, 5, w, dims, strides, boxes);
+}
+inline bool row_map(CUtensorMap* m, const void* x, int64_t rows, int cols, int box, bool fp8 = false) {
+    const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)};
+    const uint64_t strides[1] = {static_cast<uint64_t>(cols) * (fp8 ? 1 : 2)};
+    const uint32_t boxes[2] = {fp8 ? 128u : 64u, static_cast<uint32_t>(box)};
+    return encode_map(m, fp8, 2, x, dims, strides, boxes);
+}
+
+// The product's arguments; the maps are the caller's.
+inline MmaArgs product_args(const ExpertGemmParams& p) {
+    MmaArgs a{};
+    a.depth = p.K;
+    a.F = p.N;
+    a.gate_half = p.act == EP_ACT_SWIGLU ? p.N : 0;
+    a.E = p.E;
+    a.act = p.act;
+    a.rows = p.rows;
+    a.expert_offset = p.expert_offset;
+    a.counts = p.counts;
+    a.bias = p.bias;
+    a.row_weight = p.row_weight;
+    a.residual = p.residual;
+    a.y = p.y;
+    a.z = p.z;
+    a.status = p.status;
+    return a;
+}
+
+inline int bound_tiles(int64_t row_tiles, int feature_tiles) {
+    const int64_t v = row_tiles * feature_tiles;
+    return v > (1 << 20) ? 1 << 20 : static_cast<int>(v);
+}
+
+}  // namespace
+}  // namespace epg
