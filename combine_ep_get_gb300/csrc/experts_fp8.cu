@@ -4,25 +4,30 @@
 //             x_sf[d, b] * w_sf[n / 128, b] * sum over k in b of x[d, k] * W[n, k]
 //
 // The scales change every 128 terms of the sum, so a block's product goes to
-// tensor memory by itself (four MMAs, the first overwriting) and eight warps
-// scale it and add it to fp32 sums in their registers, while the MMAs of the
-// next blocks fill three more accumulators.  128 features x 128 rows a tile:
-// 64 sums a thread.  The row scales of a block come through shared memory,
-// copied there asynchronously by two warps well ahead of their use.
+// tensor memory by itself (four MMAs, the first overwriting) and sixteen warps
+// scale it and add it to fp32 sums in their registers, 32 a thread, while the
+// MMAs of the next blocks fill three more accumulators.  128 features x 128
+// rows a tile.  Two warps multiply row scales by weight scales ahead of their
+// use, so that a product's element costs one multiply-add (two elements an
+// instruction).
 #include "experts_mma.cuh"
 
 namespace epg {
 namespace {
 
-constexpr int kFp8Threads = 384;
+constexpr int kFp8Threads = 640;
+constexpr int kSumWarps = 16;
 constexpr int kRows = 128;             // rows of a tile
 constexpr int kBlock = 128;            // terms that share their scales: one stage
 constexpr int kFp8Stage = (kM + kRows) * kBlock;
 constexpr int kFp8Stages = 6;
 constexpr int kAccs = 4;
 constexpr int kScaleStages = 8;
-static_assert((kRows + 4) % 4 == 0, "rows of scales are read 16 bytes at a time");
-constexpr int kScaleWords = kRows + 4; // row scales, then the gate's and the up rows' weight scales
+constexpr int kScaleBatch = 8;         // blocks whose scales are asked for at once
+// A block's scales of the tile's rows, times the gate's (or only) weight scale
+// and times the up rows'; the second four words on, so that the two are read
+// from different banks.
+constexpr int kScaleWords = kRows + 4;
 
 struct Fp8Args {
     MmaArgs m;
@@ -34,28 +39,30 @@ struct Fp8Args {
 struct Fp8Shared {
     uint64_t full[kFp8Stages], empty[kFp8Stages], acc_full[kAccs], acc_empty[kAccs];
     uint64_t sc_full[kScaleStages], sc_empty[kScaleStages], drain;
-    alignas(16) float scales[kScaleStages][kScaleWords];
+    alignas(16) float scales[kScaleStages][2][kScaleWords];
     uint32_t tmem;
     int warp_sum[kFp8Threads / 32];
 };
 
-// 4 bytes from global to shared memory, asynchronously; zeros if not wanted.
-__device__ __forceinline__ void copy_word_async(float* dst, const float* src, bool wanted) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(wanted ? 4 : 0)
-                 : "memory");
+// Two fp32 multiply-adds in one instruction, each rounded as the scalar one;
+// pairs stay in 64-bit registers, or their packing would cost what it saves.
+__device__ __forceinline__ void fma2(uint64_t& sum, uint64_t a, uint64_t b) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(sum) : "l"(a), "l"(b));
 }
-// One arrival on `bar` once this thread's copies so far have landed.
-__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
 }
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-        "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
+// sum += v * scale, 32 columns; the scales lie in shared memory.
+__device__ __forceinline__ void add_scaled(uint64_t (&sum)[16], const float (&v)[32], const float* scale) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(scale + 4 * i);
+        fma2(sum[2 * i], pair(v[4 * i], v[4 * i + 1]), x.x);
+        fma2(sum[2 * i + 1], pair(v[4 * i + 2], v[4 * i + 3]), x.y);
+    }
 }
 
 __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __grid_constant__ Fp8Args args) {
@@ -67,7 +74,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
     t.tile_end = reinterpret_cast<int*>(s + 1);
     t.first = t.tile_end + p.E;
     t.count = t.first + p.E;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const bool gated = p.gate_half != 0;
     const int tile_features = gated ? kM / 2 : kM;
     const int feature_tiles = (p.F + tile_features - 1) / tile_features;
@@ -80,11 +87,11 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
         }
         for (int i = 0; i < kAccs; ++i) {
             mbar_init(&s->acc_full[i], 1);
-            mbar_init(&s->acc_empty[i], 8);
+            mbar_init(&s->acc_empty[i], kSumWarps);
         }
         for (int i = 0; i < kScaleStages; ++i) {
-            mbar_init(&s->sc_full[i], 64);
-            mbar_init(&s->sc_empty[i], 8);
+            mbar_init(&s->sc_full[i], 2);
+            mbar_init(&s->sc_empty[i], kSumWarps);
         }
         mbar_init(&s->drain, 1);
         fence_mbar_init();
@@ -108,19 +115,19 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
     const int tiles = t.tile_end[p.E - 1] * feature_tiles;
 
     if (warp == 0) {
-        if (lane == 0) {
-            int it = 0;
-            bool ok = true;
-            for (int g = blockIdx.x; g < tiles && ok; g += gridDim.x) {
-                const Tile r = tile_at<kRows>(g, t, p.E, feature_tiles, tile_features);
-                const int first = t.first[r.e] + r.row0, boxes = (r.rows + 63) / 64;
-                for (int kb = 0; kb < k_blocks; ++kb, ++it) {
-                    const int st = it % kFp8Stages;
-                    ok = mbar_wait_bounded(&s->empty[st], ((it / kFp8Stages) & 1) ^ 1);
-                    if (!ok) break;
-                    uint8_t* sa = stages + st * kFp8Stage;
-                    const uint32_t bar = smem_addr(&s->full[st]);
-                    mbar_arrive_expect_tx(&s->full[st], (kM + boxes * 64) * kBlock);
+        Ring<kFp8Stages> ring;
+        int issued = 0;
+        bool ok = true;
+        for (int g = blockIdx.x; g < tiles && ok; g += gridDim.x) {
+            const Tile r = tile_at<kRows>(g, t, p.E, feature_tiles, tile_features);
+            const int first = t.first[r.e] + r.row0, boxes = (r.rows + 63) / 64;
+            for (int kb = 0; kb < k_blocks; ++kb, ++issued, ring.next()) {
+                ok = warp_wait(&s->empty[ring.stage], ring.parity ^ 1);
+                if (!ok) break;
+                if (elect_one()) {
+                    uint8_t* const sa = stages + ring.stage * kFp8Stage;
+                    const uint32_t bar = smem_addr(&s->full[ring.stage]);
+                    mbar_arrive_expect_tx(&s->full[ring.stage], (kM + boxes * 64) * kBlock);
                     if (gated)
                         tma_load_5d<1>(sa, &p.a, bar, kb * kBlock, 0, 0, r.f0 / 8, r.e);
                     else
@@ -128,42 +135,43 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
                     for (int i = 0; i < boxes; ++i)
                         tma_load_2d<1>(sa + (kM + i * 64) * kBlock, &p.b, bar, kb * kBlock, first + i * 64);
                 }
+                __syncwarp();
             }
-            if (!ok) atomicOr(p.status, EP_ERR_TIMEOUT);
-            // no copy may still be in flight when the CTA ends
-            for (int i = max(0, it - kFp8Stages); i < it; ++i)
-                if (!mbar_wait_bounded(&s->full[i % kFp8Stages], (i / kFp8Stages) & 1)) break;
         }
-        __syncwarp();
+        if (!ok) atomicOr(p.status, EP_ERR_TIMEOUT);
+        // no copy may still be in flight when the CTA ends
+        for (int i = max(0, issued - kFp8Stages); i < issued; ++i)
+            if (!warp_wait(&s->full[i % kFp8Stages], (i / kFp8Stages) & 1)) break;
     } else if (warp == 1) {
-        if (lane == 0) {
-            int it = 0;
-            bool ok = true;
-            for (int g = blockIdx.x; g < tiles && ok; g += gridDim.x) {
-                const Tile r = tile_at<kRows>(g, t, p.E, feature_tiles, tile_features);
-                const uint32_t idesc = instr_desc(true, false, false, kM, r.width);
-                for (int kb = 0; kb < k_blocks; ++kb, ++it) {
-                    const int st = it % kFp8Stages, acc = it % kAccs;
-                    ok = mbar_wait_bounded(&s->acc_empty[acc], ((it / kAccs) & 1) ^ 1) &&
-                         mbar_wait_bounded(&s->full[st], (it / kFp8Stages) & 1);
-                    if (!ok) break;
-                    tcgen05_after_sync();
-                    const uint32_t sa = smem_addr(stages + st * kFp8Stage), sb = sa + kM * kBlock;
+        Ring<kFp8Stages> ring;
+        Ring<kAccs> accs;
+        const uint64_t desc = operand_desc(smem_addr(stages), 16);
+        bool ok = true;
+        for (int g = blockIdx.x; g < tiles && ok; g += gridDim.x) {
+            const Tile r = tile_at<kRows>(g, t, p.E, feature_tiles, tile_features);
+            const uint32_t idesc = instr_desc(true, false, false, kM, r.width);
+            for (int kb = 0; kb < k_blocks; ++kb, ring.next(), accs.next()) {
+                ok = warp_wait(&s->acc_empty[accs.stage], accs.parity ^ 1) &&
+                     warp_wait(&s->full[ring.stage], ring.parity);
+                if (!ok) break;
+                tcgen05_after_sync();
+                if (elect_one()) {
+                    const uint64_t da = desc_at(desc, ring.stage * kFp8Stage), db = desc_at(da, kM * kBlock);
 #pragma unroll
                     for (int k = 0; k < kBlock / 32; ++k)
-                        mma<1, true>(tmem + acc * kRows, operand_desc(sa + k * 32, 16), operand_desc(sb + k * 32, 16),
-                                     idesc, k > 0);
-                    mma_commit<1>(&s->empty[st]);
-                    mma_commit<1>(&s->acc_full[acc]);
+                        mma<1, true>(tmem + accs.stage * kRows, desc_at(da, k * 32), desc_at(db, k * 32), idesc, k > 0);
+                    mma_commit<1>(&s->empty[ring.stage]);
+                    mma_commit<1>(&s->acc_full[accs.stage]);
                 }
-            }
-            if (!ok) {
-                atomicOr(p.status, EP_ERR_TIMEOUT);
-                mma_commit<1>(&s->drain);
-                mbar_wait_bounded(&s->drain, 0);
+                __syncwarp();
             }
         }
-        __syncwarp();
+        if (!ok) {
+            atomicOr(p.status, EP_ERR_TIMEOUT);
+            if (elect_one()) mma_commit<1>(&s->drain);
+            __syncwarp();
+            warp_wait(&s->drain, 0);
+        }
     } else if (warp < 4) {
         const int tid = threadIdx.x - 64;
         int it = 0;
@@ -171,79 +179,74 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
         for (int g = blockIdx.x; g < tiles && ok; g += gridDim.x) {
             const Tile r = tile_at<kRows>(g, t, p.E, feature_tiles, tile_features);
             const int64_t first = t.first[r.e] + r.row0;
-            const int wf = (tid == 1 && gated ? p.gate_half : 0) + r.f0, Fw = gated ? 2 * p.F : p.F;
-            const float* const w_sf = args.w_sf + (static_cast<int64_t>(r.e) * (Fw / 128) + wf / 128) * k_blocks;
-            for (int kb = 0; kb < k_blocks; ++kb, ++it) {
-                const int sc = it % kScaleStages;
-                ok = mbar_wait_bounded(&s->sc_empty[sc], ((it / kScaleStages) & 1) ^ 1);
-                if (!ok) break;
-                for (int i = tid; i < kRows; i += 64) {
-                    const bool wanted = i < r.rows && EP_IN(first + i, p.rows);
-                    copy_word_async(&s->scales[sc][i],
-                                    args.x_sf + (wanted ? (first + i) * args.sf_row + kb * args.sf_block : 0), wanted);
+            const int Fw = gated ? 2 * p.F : p.F;
+            const float* const w_gate = args.w_sf + (static_cast<int64_t>(r.e) * (Fw / 128) + r.f0 / 128) * k_blocks;
+            const float* const w_up = w_gate + static_cast<int64_t>(p.gate_half / 128) * k_blocks;
+            const bool mine[2] = {tid < r.rows && EP_IN(first + tid, p.rows),
+                                  tid + 64 < r.rows && EP_IN(first + tid + 64, p.rows)};
+            const float* const x_sf = args.x_sf + (first + tid) * args.sf_row;
+            for (int kb0 = 0; kb0 < k_blocks && ok; kb0 += kScaleBatch) {
+                float x[2][kScaleBatch], wg[kScaleBatch], wu[kScaleBatch];
+#pragma unroll
+                for (int i = 0; i < kScaleBatch; ++i) {
+                    const int kb = kb0 + i;
+                    const bool in = kb < k_blocks;
+                    x[0][i] = in && mine[0] ? x_sf[kb * args.sf_block] : 0.0f;
+                    x[1][i] = in && mine[1] ? x_sf[64 * args.sf_row + kb * args.sf_block] : 0.0f;
+                    wg[i] = in ? w_gate[kb] : 0.0f;
+                    wu[i] = in ? w_up[kb] : 0.0f;
                 }
-                if (tid < 2) copy_word_async(&s->scales[sc][kRows + tid], w_sf + kb, true);
-                copies_arrive(&s->sc_full[sc]);
+#pragma unroll
+                for (int i = 0; i < kScaleBatch; ++i) {
+                    if (kb0 + i >= k_blocks || !ok) break;
+                    const int sc = it % kScaleStages;
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait_bounded(&s->sc_empty[sc], ((it / kScaleStages) & 1) ^ 1) ? 1 : 0) != 0;
+                    if (!ok) break;
+                    s->scales[sc][0][tid] = x[0][i] * wg[i];
+                    s->scales[sc][0][tid + 64] = x[1][i] * wg[i];
+                    if (gated) {
+                        s->scales[sc][1][tid] = x[0][i] * wu[i];
+                        s->scales[sc][1][tid + 64] = x[1][i] * wu[i];
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s->sc_full[sc]);
+                    ++it;
+                }
             }
         }
         if (!ok) atomicOr(p.status, EP_ERR_TIMEOUT);
-        asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
-        const int q = warp & 3, half = (warp - 4) / 4;
-        int it = 0;
+        const int q = warp & 3, c0 = (warp - 4) / 4 * 32;
+        const uint32_t column = tmem + static_cast<uint32_t>(c0) + (static_cast<uint32_t>(q * 32) << 16);
+        const int up = gated && (lane & 8) ? 1 : 0;
+        Ring<kAccs> accs;
+        Ring<kScaleStages> scs;
         bool ok = true;
         for (int g = blockIdx.x; g < tiles && ok; g += gridDim.x) {
             const Tile r = tile_at<kRows>(g, t, p.E, feature_tiles, tile_features);
-            const int first = t.first[r.e] + r.row0;
-            const int up = gated && (lane & 8) ? 1 : 0;
-            float sum[64];
+            uint64_t sum[16];
 #pragma unroll
-            for (int i = 0; i < 64; ++i) sum[i] = 0.0f;
-            for (int kb = 0; kb < k_blocks; ++kb, ++it) {
-                const int sc = it % kScaleStages, acc = it % kAccs;
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s->sc_full[sc], (it / kScaleStages) & 1) &&
-                                                     mbar_wait_bounded(&s->acc_full[acc], (it / kAccs) & 1)
-                                                 ? 1
-                                                 : 0) != 0;
+            for (int i = 0; i < 16; ++i) sum[i] = 0;
+            for (int kb = 0; kb < k_blocks; ++kb, accs.next(), scs.next()) {
+                ok = warp_wait(&s->sc_full[scs.stage], scs.parity) && warp_wait(&s->acc_full[accs.stage], accs.parity);
                 if (!ok) break;
                 tcgen05_after_sync();
-                const float ws = s->scales[sc][kRows + up];
-                const float2 w2 = make_float2(ws, ws), zero = make_float2(0.0f, 0.0f);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float v[32];
-                    tmem_load32(tmem + acc * kRows + half * 64 + c * 32 + (static_cast<uint32_t>(q * 32) << 16), v);
-                    if (c == 1) {
-                        tcgen05_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&s->acc_empty[acc]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 x = *reinterpret_cast<const float4*>(&s->scales[sc][half * 64 + c * 32 + i]);
-                        const float2 s0 = fma2(make_float2(x.x, x.y), w2, zero);
-                        const float2 s1 = fma2(make_float2(x.z, x.w), w2, zero);
-                        float* const o = sum + c * 32 + i;
-                        const float2 a = fma2(make_float2(v[i], v[i + 1]), s0, make_float2(o[0], o[1]));
-                        const float2 b = fma2(make_float2(v[i + 2], v[i + 3]), s1, make_float2(o[2], o[3]));
-                        o[0] = a.x;
-                        o[1] = a.y;
-                        o[2] = b.x;
-                        o[3] = b.y;
-                    }
-                }
+                float v[32];
+                tmem_load32(column + accs.stage * kRows, v);
+                tcgen05_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s->sc_empty[sc]);
+                if (lane == 0) mbar_arrive(&s->acc_empty[accs.stage]);
+                add_scaled(sum, v, s->scales[scs.stage][up] + c0);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s->sc_empty[scs.stage]);
             }
             if (!ok) break;
-            const float bias = bias_of(p, r, q, lane);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            if (c0 < r.rows) {
                 float v[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = sum[c * 32 + i];
-                if (half * 64 + c * 32 < r.rows)
-                    finish_columns<kProduct>(p, t, r, first, q, lane, bias, half * 64 + c * 32, v);
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(static_cast<uint32_t>(sum[i / 2] >> (i % 2 * 32)));
+                finish_columns<kProduct>(p, t, r, t.first[r.e] + r.row0, q, lane, bias_of(p, r, q, lane), c0, v);
             }
         }
         if (!ok) atomicOr(p.status, EP_ERR_TIMEOUT);

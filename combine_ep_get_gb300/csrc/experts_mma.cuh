@@ -94,8 +94,10 @@ __device__ __forceinline__ Tile tile_at(int g, const Table& t, int E, int featur
     local -= group * kGroupTiles * feature_tiles;
     const int in_group = min(kGroupTiles, n - group * kGroupTiles);
     const int f = local / in_group, row_tile = group * kGroupTiles + local % in_group;
-    // few tiles share an expert's rows evenly (each with its weights from L2)
-    const int per = n <= 4 ? ((cnt + n - 1) / n + 15) / 16 * 16 : NT;
+    // an expert's tiles share its rows evenly, unless the rounding to 16 would
+    // leave the last one without any
+    const int even = ((cnt + n - 1) / n + 15) / 16 * 16;
+    const int per = (n - 1) * even < cnt ? even : NT;
     r.row0 = row_tile * per;
     r.rows = min(per, cnt - r.row0);
     r.width = (r.rows + 15) / 16 * 16;
