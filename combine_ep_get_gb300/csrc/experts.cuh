@@ -72,6 +72,27 @@ cudaError_t launch_expert_gemm_bf16(const ExpertGemmParams& p, cudaStream_t stre
 cudaError_t launch_input_grad(const ExpertBackwardParams& p, const __nv_bfloat16* dz, cudaStream_t stream);
 cudaError_t launch_weight_grad(const ExpertBackwardParams& p, const __nv_bfloat16* dz, cudaStream_t stream);
 
+// launch_pdl with clusters of `cluster` CTAs.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_experts(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                           int cluster, Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    if (debug_enabled()) debug_launch(reinterpret_cast<const void*>(kernel), grid, block, smem, cluster);
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 // Workspace carve-ups shared by the size queries and the calls.
 constexpr int kBackwardTileRows = 64;   // rows of one partial column sum of dz
 constexpr int kBackwardStrip = 512;     // columns of one partial row sum

@@ -207,7 +207,7 @@ cudaError_t launch_expert_backward(const ExpertBackwardParams& given, cudaStream
         const int64_t tiles =
             (p.rows / kBackwardTileRows + p.E) * static_cast<int64_t>((p.N + kBackwardStrip - 1) / kBackwardStrip);
         const int grid = static_cast<int>(tiles < device_info().num_sms * 4 ? tiles : device_info().num_sms * 4);
-        const cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(kThreads), static_cast<size_t>(p.E) * 12, stream, p);
+        const cudaError_t e = launch_experts(kernel, dim3(grid), dim3(kThreads), static_cast<size_t>(p.E) * 12, stream, 1, p);
         if (e != cudaSuccess) return e;
     }
     if (p.dbias || p.d_row_weight) {
@@ -216,8 +216,8 @@ cudaError_t launch_expert_backward(const ExpertBackwardParams& given, cudaStream
         const int row_blocks = p.E < 64 ? 16 : p.E < 1024 ? 1024 / p.E : 1;
         const int64_t blocks = bias_blocks + (p.d_row_weight ? static_cast<int64_t>(row_blocks) * p.E : 0);
         if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-        const cudaError_t e = launch_pdl(backward_sums_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0,
-                                         stream, p, static_cast<int>(bias_blocks), row_blocks);
+        const cudaError_t e = launch_experts(backward_sums_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0,
+                                         stream, 1, p, static_cast<int>(bias_blocks), row_blocks);
         if (e != cudaSuccess) return e;
     }
     if (p.dx) {

@@ -269,7 +269,7 @@ cudaError_t launch_expert_gemm_fp8(const ExpertGemmParams& p, cudaStream_t strea
     if (e != cudaSuccess) return e;
     const int per = gated ? kM / 2 : kM;
     const int grid = std::max(1, std::min(device_info().num_sms, bound_tiles(p.rows / kRows + p.E, (p.N + per - 1) / per)));
-    return launch_pdl(experts_fp8_kernel, dim3(grid), dim3(kFp8Threads), smem, stream, a);
+    return launch_experts(experts_fp8_kernel, dim3(grid), dim3(kFp8Threads), smem, stream, 1, a);
 }
 
 }  // namespace epg

@@ -10,7 +10,8 @@
 // side.  Accumulators: fp32 in tensor memory, two of them, so that the
 // epilogue of one tile runs under the MMAs of the next.
 //
-// One CTA per SM walks the tiles (expert, rows, features): warp 0 issues the
+// One CTA per SM, or a pair of CTAs on a tile twice as wide in features, walks
+// the tiles (expert, rows, features): warp 0 issues the
 // tensor-map loads of 128-byte-swizzled operand tiles, 64 terms of the sum a
 // stage; warp 1 issues the MMAs; warps 4-7 read the accumulators, lane =
 // feature, and apply the epilogue.
@@ -63,10 +64,11 @@ bool encode_map(CUtensorMap* map, bool fp8, int rank, const void* base, const ui
 
 namespace {
 
-template <int kMode, int NT>
+template <int kMode, int NT, int kCtas>
 __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_constant__ MmaArgs p) {
-    using S = Shape<NT>;
+    using S = Shape<NT, kCtas>;
     constexpr bool kFew = kMode == kFewUp || kMode == kFewDown;
+    constexpr int kStep = 16 * kCtas;   // an MMA's rows come in steps of
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stages = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
     Barriers* s = reinterpret_cast<Barriers*>(stages + S::kStages * S::kStageBytes);
@@ -76,10 +78,12 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
     t.count = t.first + p.E;
     t.list = reinterpret_cast<int16_t*>(t.count + p.E);
     t.expert = t.list + p.T * p.K;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    const int tile_features = p.gate_half ? kM / 2 : kM;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
+    const int rank = kCtas == 2 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int cta_features = p.gate_half ? kM / 2 : kM, tile_features = cta_features * kCtas;
     const int feature_tiles = (p.F + tile_features - 1) / tile_features;
     const int k_blocks = (p.depth + kDepth - 1) / kDepth;
+    const int worker = blockIdx.x / kCtas, workers = gridDim.x / kCtas;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) {
@@ -88,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s->acc_full[i], 1);
-            mbar_init(&s->acc_empty[i], 4);
+            mbar_init(&s->acc_empty[i], 4 * kCtas);
         }
         mbar_init(&s->drain, 1);
         s->gave_up = 0;
@@ -96,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
         prefetch_map(&p.a);
         prefetch_map(&p.b);
     }
-    if (warp == 2) tmem_alloc<1>(&s->tmem, S::kColumns);
+    if (warp == 2) tmem_alloc<kCtas>(&s->tmem, S::kColumns);
     // The down product's kernel may start, and route, once every CTA of the
     // up product's has seen its own inputs complete.
     if (kMode != kFewDown) {
@@ -146,6 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
     }
     tcgen05_before_sync();
     __syncthreads();
+    if (kCtas == 2) cluster_sync();   // the pair's barriers are there for either
     tcgen05_after_sync();
     const uint32_t tmem = s->tmem;
     const int tiles = t.tile_end[p.E - 1] * feature_tiles;
@@ -166,95 +171,106 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
     }
 
     if (warp == 0) {
-        if (lane == 0) {
-            int it = 0;
-            bool ok = true;
-            for (int g = blockIdx.x; g < tiles && ok; g += gridDim.x) {
-                const Tile r = tile_at<NT>(g, t, p.E, feature_tiles, tile_features);
-                const int first = t.first[r.e] + r.row0;
-                const int boxes = kFew ? (r.rows + 3) / 4 : (r.rows + S::kBoxRows - 1) / S::kBoxRows;
-                const uint32_t bytes = kABytes + boxes * (kFew ? 4 : S::kBoxRows) * kDepth * 2;
-                for (int kb = 0; kb < k_blocks; ++kb, ++it) {
-                    const int st = it % S::kStages;
-                    ok = mbar_wait_bounded(&s->empty[st], ((it / S::kStages) & 1) ^ 1);
-                    if (!ok) break;
-                    uint8_t* sa = stages + st * S::kStageBytes;
-                    uint8_t* sb = sa + kABytes;
-                    const uint32_t bar = smem_addr(&s->full[st]);
-                    mbar_arrive_expect_tx(&s->full[st], bytes);
+        Ring<S::kStages> ring;
+        int issued = 0;
+        bool ok = true;
+        for (int g = worker; g < tiles && ok; g += workers) {
+            const Tile r = tile_at<NT, kStep>(g, t, p.E, feature_tiles, tile_features);
+            const int share = r.width / kCtas;   // the row operand's rows of each CTA
+            const auto boxes_of = [&](int who) {
+                const int rows = max(0, min(share, r.rows - who * share));
+                return kFew ? (rows + 3) / 4 : (rows + S::kBoxRows - 1) / S::kBoxRows;
+            };
+            const int first = t.first[r.e] + r.row0 + rank * share, boxes = boxes_of(rank);
+            const uint32_t bytes = kCtas * kABytes + (boxes_of(0) + (kCtas == 2 ? boxes_of(1) : 0)) *
+                                                         ((kFew ? 4 : S::kBoxRows) * kDepth * 2);
+            const int f0 = r.f0 + rank * cta_features;
+            // few tokens: lane i gathers rows 4 i .. 4 i + 3 (past the last one, the last)
+            int row[4] = {};
+            if (kFew && lane < boxes)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int entry = t.list[first + min(4 * lane + j, r.rows - 1)];
+                    row[j] = kMode == kFewUp ? entry / p.K : entry;
+                }
+            for (int kb = 0; kb < k_blocks; ++kb, ++issued, ring.next()) {
+                ok = warp_wait(&s->empty[ring.stage], ring.parity ^ 1);
+                if (!ok) break;
+                uint8_t* const sa = stages + ring.stage * S::kStageBytes;
+                uint8_t* const sb = sa + kABytes;
+                uint32_t bar = smem_addr(&s->full[ring.stage]);
+                if (kCtas == 2) bar = map_to_rank(bar, 0);
+                if (elect_one()) {
+                    if (rank == 0) mbar_arrive_expect_tx(&s->full[ring.stage], bytes);
                     if (kMode == kInputGrad) {
-                        tma_load_3d<1>(sa, &p.a, bar, r.f0, kb * kDepth, r.e);
-                        tma_load_3d<1>(sa + kABytes / 2, &p.a, bar, r.f0 + 64, kb * kDepth, r.e);
+                        tma_load_3d<kCtas>(sa, &p.a, bar, f0, kb * kDepth, r.e);
+                        tma_load_3d<kCtas>(sa + kABytes / 2, &p.a, bar, f0 + 64, kb * kDepth, r.e);
                     } else if (p.gate_half) {
-                        tma_load_5d<1>(sa, &p.a, bar, kb * kDepth, 0, 0, r.f0 / 8, r.e);
+                        tma_load_5d<kCtas>(sa, &p.a, bar, kb * kDepth, 0, 0, f0 / 8, r.e);
                     } else {
-                        tma_load_3d<1>(sa, &p.a, bar, kb * kDepth, r.f0, r.e);
+                        tma_load_3d<kCtas>(sa, &p.a, bar, kb * kDepth, f0, r.e);
                     }
-                    if (kFew) {
-                        for (int i = 0; i < boxes; ++i) {
-                            int row[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const int entry = t.list[first + min(4 * i + j, r.rows - 1)];
-                                row[j] = kMode == kFewUp ? entry / p.K : entry;
-                            }
-                            tma_gather4(sb + i * 4 * kDepth * 2, &p.b, bar, kb * kDepth, row[0], row[1], row[2], row[3]);
-                        }
-                    } else {
+                    if (!kFew)
                         for (int i = 0; i < boxes; ++i)
-                            tma_load_2d<1>(sb + i * S::kBoxRows * kDepth * 2, &p.b, bar, kb * kDepth,
-                                           first + i * S::kBoxRows);
-                    }
+                            tma_load_2d<kCtas>(sb + i * S::kBoxRows * kDepth * 2, &p.b, bar, kb * kDepth,
+                                               first + i * S::kBoxRows);
                 }
+                __syncwarp();
+                if (kFew && lane < boxes)
+                    tma_gather4(sb + lane * 4 * kDepth * 2, &p.b, bar, kb * kDepth, row[0], row[1], row[2], row[3]);
             }
-            if (!ok) atomicOr(p.status, EP_ERR_TIMEOUT);
-            // no copy may still be in flight when the CTA ends
-            for (int i = max(0, it - S::kStages); i < it; ++i)
-                if (!mbar_wait_bounded(&s->full[i % S::kStages], (i / S::kStages) & 1)) break;
         }
-        __syncwarp();
-    } else if (warp == 1) {
-        if (lane == 0) {
-            int it = 0, n = 0;
-            bool ok = true;
-            for (int g = blockIdx.x; g < tiles && ok; g += gridDim.x, ++n) {
-                const Tile r = tile_at<NT>(g, t, p.E, feature_tiles, tile_features);
-                const uint32_t idesc = instr_desc(false, kMode == kInputGrad, false, kM, r.width);
-                const uint32_t d = tmem + (n & 1) * NT;
-                ok = mbar_wait_bounded(&s->acc_empty[n & 1], ((n / 2) & 1) ^ 1);
+        if (!ok) atomicOr(p.status, EP_ERR_TIMEOUT);
+        // no copy may still be in flight when the CTA ends (a pair's end: rank 0 sees both CTAs')
+        if (rank == 0)
+            for (int i = max(0, issued - S::kStages); i < issued; ++i)
+                if (!warp_wait(&s->full[i % S::kStages], (i / S::kStages) & 1)) break;
+    } else if (warp == 1 && rank == 0) {
+        Ring<S::kStages> ring;
+        Ring<2> accs;
+        constexpr bool kMn = kMode == kInputGrad;
+        const uint64_t desc_a = operand_desc(smem_addr(stages), kMn ? kABytes / 2 : 16);
+        const uint64_t desc_b = operand_desc(smem_addr(stages) + kABytes, 16);
+        bool ok = true;
+        for (int g = worker; g < tiles && ok; g += workers, accs.next()) {
+            const Tile r = tile_at<NT, kStep>(g, t, p.E, feature_tiles, tile_features);
+            const uint32_t idesc = instr_desc(false, kMn, false, kM * kCtas, r.width);
+            const uint32_t d = tmem + accs.stage * NT;
+            ok = warp_wait(&s->acc_empty[accs.stage], accs.parity ^ 1);
+            tcgen05_after_sync();
+            for (int kb = 0; kb < k_blocks && ok; ++kb, ring.next()) {
+                ok = warp_wait(&s->full[ring.stage], ring.parity);
+                if (!ok) break;
                 tcgen05_after_sync();
-                for (int kb = 0; kb < k_blocks && ok; ++kb, ++it) {
-                    const int st = it % S::kStages;
-                    ok = mbar_wait_bounded(&s->full[st], (it / S::kStages) & 1);
-                    if (!ok) break;
-                    tcgen05_after_sync();
-                    const uint32_t sa = smem_addr(stages + st * S::kStageBytes), sb = sa + kABytes;
+                if (elect_one()) {
+                    const uint64_t a = desc_at(desc_a, ring.stage * S::kStageBytes);
+                    const uint64_t b = desc_at(desc_b, ring.stage * S::kStageBytes);
 #pragma unroll
-                    for (int k = 0; k < kDepth / 16; ++k) {
-                        const uint64_t a = kMode == kInputGrad ? operand_desc(sa + k * 2048, kABytes / 2)
-                                                               : operand_desc(sa + k * 32, 16);
-                        mma<1, false>(d, a, operand_desc(sb + k * 32, 16), idesc, kb > 0 || k > 0);
-                    }
-                    mma_commit<1>(&s->empty[st]);
+                    for (int k = 0; k < kDepth / 16; ++k)
+                        mma<kCtas, false>(d, desc_at(a, k * (kMn ? 2048 : 32)), desc_at(b, k * 32), idesc,
+                                          kb > 0 || k > 0);
+                    mma_commit<kCtas>(&s->empty[ring.stage]);
+                    if (kb == k_blocks - 1) mma_commit<kCtas>(&s->acc_full[accs.stage]);
                 }
-                if (ok) mma_commit<1>(&s->acc_full[n & 1]);
-            }
-            if (!ok) {
-                atomicOr(p.status, EP_ERR_TIMEOUT);
-                mma_commit<1>(&s->drain);
-                mbar_wait_bounded(&s->drain, 0);
+                __syncwarp();
             }
         }
-        __syncwarp();
+        if (!ok) {
+            atomicOr(p.status, EP_ERR_TIMEOUT);
+            if (elect_one()) mma_commit<kCtas>(&s->drain);
+            __syncwarp();
+            warp_wait(&s->drain, 0);
+        }
     } else if (warp >= 4) {
         const int q = warp - 4;
-        int n = 0;
-        for (int g = blockIdx.x; g < tiles; g += gridDim.x, ++n) {
-            const Tile r = tile_at<NT>(g, t, p.E, feature_tiles, tile_features);
+        Ring<2> accs;
+        for (int g = worker; g < tiles; g += workers, accs.next()) {
+            Tile r = tile_at<NT, kStep>(g, t, p.E, feature_tiles, tile_features);
+            r.f0 += rank * cta_features;
             const int first = t.first[r.e] + r.row0;
-            const uint32_t acc = tmem + (n & 1) * NT + (static_cast<uint32_t>(q * 32) << 16);
-            const bool ready =
-                __all_sync(0xffffffffu, mbar_wait_bounded(&s->acc_full[n & 1], (n / 2) & 1) ? 1 : 0) != 0;
+            const uint32_t acc = tmem + accs.stage * NT + (static_cast<uint32_t>(q * 32) << 16);
+            const float bias = kMode == kInputGrad ? 0.0f : bias_of(p, r, q, lane);
+            const bool ready = warp_wait(&s->acc_full[accs.stage], accs.parity);
             if (!ready) {
                 atomicOr(p.status, EP_ERR_TIMEOUT);
                 s->gave_up = 1;
@@ -262,7 +278,6 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
             if (kMode == kFewDown) named_barrier(1, 128);   // its barriers below are for all four warps
             if (kMode == kFewDown ? *reinterpret_cast<volatile int*>(&s->gave_up) != 0 : !ready) break;
             tcgen05_after_sync();
-            const float bias = kMode == kInputGrad ? 0.0f : bias_of(p, r, q, lane);
             for (int c0 = 0; c0 < r.width; c0 += 32) {
                 float v[32];
                 __syncwarp();
@@ -270,7 +285,12 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
                 if (c0 + 32 >= r.width) {
                     tcgen05_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&s->acc_empty[n & 1]);
+                    if (lane == 0) {
+                        if (kCtas == 1)
+                            mbar_arrive(&s->acc_empty[accs.stage]);
+                        else
+                            mbar_arrive_cluster(map_to_rank(smem_addr(&s->acc_empty[accs.stage]), 0));
+                    }
                 }
                 finish_columns<kMode>(p, t, r, first, q, lane, bias, c0, v);
             }
@@ -313,24 +333,39 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
         }
     }
     __syncthreads();
-    if (warp == 2) tmem_free<1>(tmem, S::kColumns);
+    if (kCtas == 2) cluster_sync();   // neither CTA of a pair ends while the other may still reach it
+    if (warp == 2) tmem_free<kCtas>(tmem, S::kColumns);
 }
 
-template <int NT>
+template <int NT, int kCtas>
 size_t smem_bytes(int E, int entries) {
-    using S = Shape<NT>;
+    using S = Shape<NT, kCtas>;
     return 1024 + S::kStages * S::kStageBytes + sizeof(Barriers) + static_cast<size_t>(E) * 12 +
            (entries > 0 ? static_cast<size_t>(entries) * 4 + EP_FEW_MAX_TOKENS * 2 : 0);
 }
 
-template <int kMode, int NT>
+// tiles_bound: at least as many tiles as there can be, for the grid.
+template <int kMode, int NT, int kCtas>
 cudaError_t launch(const MmaArgs& a, int tiles_bound, cudaStream_t stream) {
-    const size_t smem = smem_bytes<NT>(a.E, a.T * a.K);
-    const auto kernel = experts_mma_kernel<kMode, NT>;
+    const size_t smem = smem_bytes<NT, kCtas>(a.E, a.T * a.K);
+    const auto kernel = experts_mma_kernel<kMode, NT, kCtas>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    const int grid = std::max(1, std::min(device_info().num_sms, tiles_bound));
-    return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, stream, a);
+    const int workers = std::max(1, std::min(device_info().num_sms / kCtas, tiles_bound));
+    return launch_experts(kernel, dim3(workers * kCtas), dim3(kThreads), smem, stream, kCtas, a);
+}
+
+// Pairs of CTAs halve the row operand's copies into shared memory, whose
+// bandwidth (copies in, operands out) bounds one CTA's 128 x 256 tile; a call
+// that has no more tiles than pairs takes single CTAs, twice as many.
+template <int kMode>
+cudaError_t launch_rows(const MmaArgs& a, cudaStream_t stream) {
+    constexpr int NT = 256;
+    const int per = a.gate_half ? kM / 2 : kM;
+    const int64_t row_tiles = a.rows / NT + a.E;
+    const int pairs = bound_tiles(row_tiles, (a.F + 2 * per - 1) / (2 * per));
+    if (pairs * 2 > device_info().num_sms) return launch<kMode, NT, 2>(a, pairs, stream);
+    return launch<kMode, NT, 1>(a, bound_tiles(row_tiles, (a.F + per - 1) / per), stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -541,20 +576,16 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
 }  // namespace
 
 cudaError_t launch_expert_gemm_bf16(const ExpertGemmParams& p, cudaStream_t stream) {
-    constexpr int NT = 256;
-    const bool gated = p.act == EP_ACT_SWIGLU;
     MmaArgs a = product_args(p);
-    if (!(gated ? gated_map(&a.a, p.w, p.E, p.N, p.K) : weight_map(&a.a, p.w, p.E, p.Nw, p.K, kM)) ||
-        !row_map(&a.b, p.x, p.rows, p.K, Shape<NT>::kBoxRows))
+    if (!(a.gate_half ? gated_map(&a.a, p.w, p.E, p.N, p.K) : weight_map(&a.a, p.w, p.E, p.Nw, p.K, kM)) ||
+        !row_map(&a.b, p.x, p.rows, p.K, kDepth))
         return cudaErrorInvalidValue;
-    const int per = gated ? kM / 2 : kM;
-    return launch<kProduct, NT>(a, bound_tiles(p.rows / NT + p.E, (p.N + per - 1) / per), stream);
+    return launch_rows<kProduct>(a, stream);
 }
 
 cudaError_t launch_input_grad(const ExpertBackwardParams& p, const __nv_bfloat16* dz, cudaStream_t stream) {
-    constexpr int NT = 256;
     MmaArgs a{};
-    if (!weight_map(&a.a, p.w, p.E, p.Nw, p.K, kDepth) || !row_map(&a.b, dz, p.rows, p.Nw, Shape<NT>::kBoxRows))
+    if (!weight_map(&a.a, p.w, p.E, p.Nw, p.K, kDepth) || !row_map(&a.b, dz, p.rows, p.Nw, kDepth))
         return cudaErrorInvalidValue;
     a.depth = p.Nw;
     a.F = p.K;
@@ -564,7 +595,7 @@ cudaError_t launch_input_grad(const ExpertBackwardParams& p, const __nv_bfloat16
     a.counts = p.counts;
     a.y = p.dx;
     a.status = p.status;
-    return launch<kInputGrad, NT>(a, bound_tiles(p.rows / NT + p.E, (p.K + kM - 1) / kM), stream);
+    return launch_rows<kInputGrad>(a, stream);
 }
 
 cudaError_t launch_weight_grad(const ExpertBackwardParams& p, const __nv_bfloat16* dz, cudaStream_t stream) {
@@ -589,7 +620,7 @@ cudaError_t launch_weight_grad(const ExpertBackwardParams& p, const __nv_bfloat1
     const int64_t tiles = static_cast<int64_t>(p.E) * ((p.Nw + kM - 1) / kM) * ((p.K + kGradK - 1) / kGradK);
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
     const int grid = static_cast<int>(std::min<int64_t>(device_info().num_sms, tiles));
-    return launch_pdl(weight_grad_kernel, dim3(grid), dim3(kThreads), smem, stream, a);
+    return launch_experts(weight_grad_kernel, dim3(grid), dim3(kThreads), smem, stream, 1, a);
 }
 
 cudaError_t launch_few_tokens(const FewTokensParams& p, cudaStream_t stream) {
@@ -629,9 +660,9 @@ cudaError_t launch_few_tokens(const FewTokensParams& p, cudaStream_t stream) {
     down.out = p.out;
     const int entries = p.T * p.K, active = std::min(p.E, entries);
     const int per = gated ? kM / 2 : kM;
-    cudaError_t e = launch<kFewUp, NT>(up, bound_tiles(active + entries / NT, (p.I + per - 1) / per), stream);
+    cudaError_t e = launch<kFewUp, NT, 1>(up, bound_tiles(active + entries / NT, (p.I + per - 1) / per), stream);
     if (e != cudaSuccess) return e;
-    return launch<kFewDown, NT>(down, bound_tiles(active + entries / NT, (p.H + kM - 1) / kM), stream);
+    return launch<kFewDown, NT, 1>(down, bound_tiles(active + entries / NT, (p.H + kM - 1) / kM), stream);
 }
 
 }  // namespace epg

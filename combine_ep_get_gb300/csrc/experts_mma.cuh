@@ -43,12 +43,13 @@ struct MmaArgs {
     int32_t* status;
 };
 
-template <int NT>
+template <int NT, int kCtas>
 struct Shape {
-    static constexpr int kStageBytes = kABytes + NT * kDepth * 2;
+    static constexpr int kRows = NT / kCtas;   // of the row operand in one CTA
+    static constexpr int kStageBytes = kABytes + kRows * kDepth * 2;
     static constexpr int kStages = (192 * 1024) / kStageBytes < 10 ? (192 * 1024) / kStageBytes : 10;
-    static constexpr int kBoxRows = NT < 64 ? NT : 64;
-    static constexpr int kColumns = 2 * NT < 32 ? 32 : 2 * NT;   // of tensor memory
+    static constexpr int kBoxRows = 64;
+    static constexpr int kColumns = 2 * NT;    // of tensor memory
 };
 
 struct Barriers {
@@ -75,7 +76,7 @@ struct Tile {
     int e, row0, rows, width, f0;
 };
 
-template <int NT>
+template <int NT, int kStep = 16>
 __device__ __forceinline__ Tile tile_at(int g, const Table& t, int E, int feature_tiles, int tile_features) {
     int lo = 0, hi = E - 1;
     while (lo < hi) {
@@ -94,13 +95,13 @@ __device__ __forceinline__ Tile tile_at(int g, const Table& t, int E, int featur
     local -= group * kGroupTiles * feature_tiles;
     const int in_group = min(kGroupTiles, n - group * kGroupTiles);
     const int f = local / in_group, row_tile = group * kGroupTiles + local % in_group;
-    // an expert's tiles share its rows evenly, unless the rounding to 16 would
-    // leave the last one without any
-    const int even = ((cnt + n - 1) / n + 15) / 16 * 16;
+    // an expert's tiles share its rows evenly, unless the rounding to an MMA's
+    // step would leave the last one without any
+    const int even = ((cnt + n - 1) / n + kStep - 1) / kStep * kStep;
     const int per = (n - 1) * even < cnt ? even : NT;
     r.row0 = row_tile * per;
     r.rows = min(per, cnt - r.row0);
-    r.width = (r.rows + 15) / 16 * 16;
+    r.width = (r.rows + kStep - 1) / kStep * kStep;
     r.f0 = f * tile_features;
     return r;
 }
