@@ -5,32 +5,36 @@
 //
 // The scales change every 128 terms of the sum, so a block's product goes to
 // tensor memory by itself (four MMAs, the first overwriting) and sixteen warps
-// scale it and add it to fp32 sums in their registers, 32 a thread, while the
-// MMAs of the next blocks fill three more accumulators.  128 features x 128
-// rows a tile.  Two warps multiply row scales by weight scales ahead of their
-// use, so that a product's element costs one multiply-add (two elements an
-// instruction).
+// scale it and add it to fp32 sums in their registers, 64 a thread, while the
+// MMAs of the next block fill the other accumulator.
+//
+// Here the rows are the M side, 128 a tile, and 256 of the weights' features
+// the N side: a lane is a row, so a block's scale is one register a lane (with
+// lanes as features, as in the bf16 product, every warp read the scales of its
+// 32 rows from shared memory, whose bandwidth, already taken by the copies in
+// and the operands out, bounded the kernel).  SWIGLU: 8 gate and 8 up features
+// in turns (one box of a five-dimensional map).
 #include "experts_mma.cuh"
 
 namespace epg {
 namespace {
 
-constexpr int kFp8Threads = 640;
+constexpr int kFp8Warps = 19;          // loads, MMAs, scales, 16 that sum
+constexpr int kFp8Threads = kFp8Warps * 32;
 constexpr int kSumWarps = 16;
 constexpr int kRows = 128;             // rows of a tile
+constexpr int kFeatures = 256;         // features of a tile
+constexpr int kSumColumns = kFeatures / (kSumWarps / 4);
 constexpr int kBlock = 128;            // terms that share their scales: one stage
-constexpr int kFp8Stage = (kM + kRows) * kBlock;
-constexpr int kFp8Stages = 6;
-constexpr int kAccs = 4;
+constexpr int kRowBytes = kRows * kBlock;
+constexpr int kFp8Stage = kRowBytes + kFeatures * kBlock;
+constexpr int kFp8Stages = 4;
+constexpr int kAccs = 2;
 constexpr int kScaleStages = 8;
 constexpr int kScaleBatch = 8;         // blocks whose scales are asked for at once
-// A block's scales of the tile's rows, times the gate's (or only) weight scale
-// and times the up rows'; the second four words on, so that the two are read
-// from different banks.
-constexpr int kScaleWords = kRows + 4;
 
 struct Fp8Args {
-    MmaArgs m;
+    MmaArgs m;                   // m.a: the weights' map, m.b: the rows'
     const float* x_sf;           // element (d, b) at d * sf_row + b * sf_block
     int64_t sf_row, sf_block;
     const float* w_sf;           // [E][Nw / 128][K / 128]
@@ -39,9 +43,11 @@ struct Fp8Args {
 struct Fp8Shared {
     uint64_t full[kFp8Stages], empty[kFp8Stages], acc_full[kAccs], acc_empty[kAccs];
     uint64_t sc_full[kScaleStages], sc_empty[kScaleStages], drain;
-    alignas(16) float scales[kScaleStages][2][kScaleWords];
+    // a block's row scales times the two weight scales of the tile: of its
+    // first and last 128 features, or of its gate and up features
+    float scales[kScaleStages][2][kRows];
     uint32_t tmem;
-    int warp_sum[kFp8Threads / 32];
+    int warp_sum[kFp8Warps];
 };
 
 // Two fp32 multiply-adds in one instruction, each rounded as the scalar one;
@@ -54,17 +60,60 @@ __device__ __forceinline__ uint64_t pair(float lo, float hi) {
     asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
     return v;
 }
+__device__ __forceinline__ float part_of(const uint64_t* sum, int i) {
+    return __uint_as_float(static_cast<uint32_t>(sum[i / 2] >> (i % 2 * 32)));
+}
 
-// sum += v * scale, 32 columns; the scales lie in shared memory.
-__device__ __forceinline__ void add_scaled(uint64_t (&sum)[16], const float (&v)[32], const float* scale) {
+// The epilogue of 16 columns of a row: 16 features from f, or, gated, 8 from f
+// (8 gate columns, then 8 up ones).
+__device__ __forceinline__ void finish_row(const MmaArgs& p, int e, int64_t d, int f, float (&v)[16]) {
+    const bool gated = p.gate_half != 0;
+    const int Fw = gated ? 2 * p.F : p.F;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(scale + 4 * i);
-        fma2(sum[2 * i], pair(v[4 * i], v[4 * i + 1]), x.x);
-        fma2(sum[2 * i + 1], pair(v[4 * i + 2], v[4 * i + 3]), x.y);
+    for (int h = 0; h < 2; ++h) {
+        const int wrow = gated ? h * p.gate_half + f : f + 8 * h;
+        float* const u = v + 8 * h;
+        if (!gated && f + 8 * h >= p.F) break;
+        if (p.bias) {
+            const float4* const b = reinterpret_cast<const float4*>(p.bias + static_cast<int64_t>(e) * Fw + wrow);
+            const float4 b0 = b[0], b1 = b[1];
+            u[0] += b0.x;
+            u[1] += b0.y;
+            u[2] += b0.z;
+            u[3] += b0.w;
+            u[4] += b1.x;
+            u[5] += b1.y;
+            u[6] += b1.z;
+            u[7] += b1.w;
+        }
+        if (p.z)
+            st_v4(p.z + d * Fw + wrow,
+                  make_uint4(pack2(u[0], u[1]), pack2(u[2], u[3]), pack2(u[4], u[5]), pack2(u[6], u[7])));
+    }
+    const float w = p.row_weight ? p.row_weight[d] : 1.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (gated ? h > 0 : f + 8 * h >= p.F) break;
+        float* const u = v + 8 * h;
+        __nv_bfloat16* const out = p.y + d * p.F + f + 8 * h;
+        float a[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] = (gated ? silu(u[i]) * v[8 + i] : activate(u[i], p.act)) * w;
+        if (p.residual) {
+            const uint4 r = *reinterpret_cast<const uint4*>(p.residual + d * p.F + f + 8 * h);
+            const uint32_t words[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 b = unpack2(words[i]);
+                a[2 * i] += b.x;
+                a[2 * i + 1] += b.y;
+            }
+        }
+        st_v4(out, make_uint4(pack2(a[0], a[1]), pack2(a[2], a[3]), pack2(a[4], a[5]), pack2(a[6], a[7])));
     }
 }
 
+template <bool kGated>
 __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __grid_constant__ Fp8Args args) {
     const MmaArgs& p = args.m;
     extern __shared__ uint8_t smem_raw[];
@@ -75,9 +124,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
     t.first = t.tile_end + p.E;
     t.count = t.first + p.E;
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
-    const bool gated = p.gate_half != 0;
-    const int tile_features = gated ? kM / 2 : kM;
-    const int feature_tiles = (p.F + tile_features - 1) / tile_features;
+    constexpr int kTileFeatures = kGated ? kFeatures / 2 : kFeatures;
+    const int feature_tiles = (p.F + kTileFeatures - 1) / kTileFeatures;
     const int k_blocks = p.depth / kBlock;
 
     if (threadIdx.x == 0) {
@@ -90,7 +138,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
             mbar_init(&s->acc_empty[i], kSumWarps);
         }
         for (int i = 0; i < kScaleStages; ++i) {
-            mbar_init(&s->sc_full[i], 2);
+            mbar_init(&s->sc_full[i], 1);
             mbar_init(&s->sc_empty[i], kSumWarps);
         }
         mbar_init(&s->drain, 1);
@@ -98,7 +146,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
         prefetch_map(&p.a);
         prefetch_map(&p.b);
     }
-    if (warp == 2) tmem_alloc<1>(&s->tmem, kAccs * kRows);
+    if (warp == 2) tmem_alloc<1>(&s->tmem, kAccs * kFeatures);
     pdl_wait();
     pdl_launch_dependents();
     for (int e = threadIdx.x; e < p.E; e += kFp8Threads) {
@@ -119,21 +167,26 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
         int issued = 0;
         bool ok = true;
         for (int g = blockIdx.x; g < tiles && ok; g += gridDim.x) {
-            const Tile r = tile_at<kRows>(g, t, p.E, feature_tiles, tile_features);
+            const Tile r = tile_at<kRows>(g, t, p.E, feature_tiles, kTileFeatures);
             const int first = t.first[r.e] + r.row0, boxes = (r.rows + 63) / 64;
+            // the second 128 features, where there are any
+            const int halves = p.F - r.f0 > kTileFeatures / 2 ? 2 : 1;
             for (int kb = 0; kb < k_blocks; ++kb, ++issued, ring.next()) {
                 ok = warp_wait(&s->empty[ring.stage], ring.parity ^ 1);
                 if (!ok) break;
                 if (elect_one()) {
                     uint8_t* const sa = stages + ring.stage * kFp8Stage;
                     const uint32_t bar = smem_addr(&s->full[ring.stage]);
-                    mbar_arrive_expect_tx(&s->full[ring.stage], (kM + boxes * 64) * kBlock);
-                    if (gated)
-                        tma_load_5d<1>(sa, &p.a, bar, kb * kBlock, 0, 0, r.f0 / 8, r.e);
-                    else
-                        tma_load_3d<1>(sa, &p.a, bar, kb * kBlock, r.f0, r.e);
+                    mbar_arrive_expect_tx(&s->full[ring.stage], (boxes * 64 + halves * 128) * kBlock);
+                    for (int i = 0; i < halves; ++i) {
+                        uint8_t* const sb = sa + kRowBytes + i * 128 * kBlock;
+                        if (kGated)
+                            tma_load_5d<1>(sb, &p.a, bar, kb * kBlock, 0, 0, r.f0 / 8 + i * 8, r.e);
+                        else
+                            tma_load_3d<1>(sb, &p.a, bar, kb * kBlock, r.f0 + i * 128, r.e);
+                    }
                     for (int i = 0; i < boxes; ++i)
-                        tma_load_2d<1>(sa + (kM + i * 64) * kBlock, &p.b, bar, kb * kBlock, first + i * 64);
+                        tma_load_2d<1>(sa + i * 64 * kBlock, &p.b, bar, kb * kBlock, first + i * 64);
                 }
                 __syncwarp();
             }
@@ -148,18 +201,20 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
         const uint64_t desc = operand_desc(smem_addr(stages), 16);
         bool ok = true;
         for (int g = blockIdx.x; g < tiles && ok; g += gridDim.x) {
-            const Tile r = tile_at<kRows>(g, t, p.E, feature_tiles, tile_features);
-            const uint32_t idesc = instr_desc(true, false, false, kM, r.width);
+            const Tile r = tile_at<kRows>(g, t, p.E, feature_tiles, kTileFeatures);
+            const uint32_t idesc =
+                instr_desc(true, false, false, kM, p.F - r.f0 > kTileFeatures / 2 ? kFeatures : kFeatures / 2);
             for (int kb = 0; kb < k_blocks; ++kb, ring.next(), accs.next()) {
                 ok = warp_wait(&s->acc_empty[accs.stage], accs.parity ^ 1) &&
                      warp_wait(&s->full[ring.stage], ring.parity);
                 if (!ok) break;
                 tcgen05_after_sync();
                 if (elect_one()) {
-                    const uint64_t da = desc_at(desc, ring.stage * kFp8Stage), db = desc_at(da, kM * kBlock);
+                    const uint64_t da = desc_at(desc, ring.stage * kFp8Stage), db = desc_at(da, kRowBytes);
 #pragma unroll
                     for (int k = 0; k < kBlock / 32; ++k)
-                        mma<1, true>(tmem + accs.stage * kRows, desc_at(da, k * 32), desc_at(db, k * 32), idesc, k > 0);
+                        mma<1, true>(tmem + accs.stage * kFeatures, desc_at(da, k * 32), desc_at(db, k * 32), idesc,
+                                     k > 0);
                     mma_commit<1>(&s->empty[ring.stage]);
                     mma_commit<1>(&s->acc_full[accs.stage]);
                 }
@@ -172,87 +227,100 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
             __syncwarp();
             warp_wait(&s->drain, 0);
         }
-    } else if (warp < 4) {
-        const int tid = threadIdx.x - 64;
-        int it = 0;
+    } else if (warp == 2) {
+        // lane l: the scales of rows l, l + 32, l + 64, l + 96
+        Ring<kScaleStages> scs;
         bool ok = true;
         for (int g = blockIdx.x; g < tiles && ok; g += gridDim.x) {
-            const Tile r = tile_at<kRows>(g, t, p.E, feature_tiles, tile_features);
+            const Tile r = tile_at<kRows>(g, t, p.E, feature_tiles, kTileFeatures);
             const int64_t first = t.first[r.e] + r.row0;
-            const int Fw = gated ? 2 * p.F : p.F;
-            const float* const w_gate = args.w_sf + (static_cast<int64_t>(r.e) * (Fw / 128) + r.f0 / 128) * k_blocks;
-            const float* const w_up = w_gate + static_cast<int64_t>(p.gate_half / 128) * k_blocks;
-            const bool mine[2] = {tid < r.rows && EP_IN(first + tid, p.rows),
-                                  tid + 64 < r.rows && EP_IN(first + tid + 64, p.rows)};
-            const float* const x_sf = args.x_sf + (first + tid) * args.sf_row;
+            const int Fw = kGated ? 2 * p.F : p.F;
+            const float* const w0 = args.w_sf + (static_cast<int64_t>(r.e) * (Fw / 128) + r.f0 / 128) * k_blocks;
+            const int next = kGated ? p.gate_half / 128 : (p.F - r.f0 > 128 ? 1 : 0);
+            const float* const w1 = w0 + static_cast<int64_t>(next) * k_blocks;
+            const float* const x_sf = args.x_sf + (first + lane) * args.sf_row;
             for (int kb0 = 0; kb0 < k_blocks && ok; kb0 += kScaleBatch) {
-                float x[2][kScaleBatch], wg[kScaleBatch], wu[kScaleBatch];
+                float x[4][kScaleBatch], a[kScaleBatch], b[kScaleBatch];
 #pragma unroll
                 for (int i = 0; i < kScaleBatch; ++i) {
                     const int kb = kb0 + i;
                     const bool in = kb < k_blocks;
-                    x[0][i] = in && mine[0] ? x_sf[kb * args.sf_block] : 0.0f;
-                    x[1][i] = in && mine[1] ? x_sf[64 * args.sf_row + kb * args.sf_block] : 0.0f;
-                    wg[i] = in ? w_gate[kb] : 0.0f;
-                    wu[i] = in ? w_up[kb] : 0.0f;
+                    a[i] = in ? w0[kb] : 0.0f;
+                    b[i] = in ? w1[kb] : 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        x[j][i] = in && lane + 32 * j < r.rows && EP_IN(first + lane + 32 * j, p.rows)
+                                      ? x_sf[32 * j * args.sf_row + kb * args.sf_block]
+                                      : 0.0f;
                 }
 #pragma unroll
                 for (int i = 0; i < kScaleBatch; ++i) {
                     if (kb0 + i >= k_blocks || !ok) break;
-                    const int sc = it % kScaleStages;
-                    ok = __all_sync(0xffffffffu,
-                                    mbar_wait_bounded(&s->sc_empty[sc], ((it / kScaleStages) & 1) ^ 1) ? 1 : 0) != 0;
+                    ok = warp_wait(&s->sc_empty[scs.stage], scs.parity ^ 1);
                     if (!ok) break;
-                    s->scales[sc][0][tid] = x[0][i] * wg[i];
-                    s->scales[sc][0][tid + 64] = x[1][i] * wg[i];
-                    if (gated) {
-                        s->scales[sc][1][tid] = x[0][i] * wu[i];
-                        s->scales[sc][1][tid + 64] = x[1][i] * wu[i];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        s->scales[scs.stage][0][lane + 32 * j] = x[j][i] * a[i];
+                        s->scales[scs.stage][1][lane + 32 * j] = x[j][i] * b[i];
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&s->sc_full[sc]);
-                    ++it;
+                    if (lane == 0) mbar_arrive(&s->sc_full[scs.stage]);
+                    scs.next();
                 }
             }
         }
         if (!ok) atomicOr(p.status, EP_ERR_TIMEOUT);
     } else {
-        const int q = warp & 3, c0 = (warp - 4) / 4 * 32;
-        const uint32_t column = tmem + static_cast<uint32_t>(c0) + (static_cast<uint32_t>(q * 32) << 16);
-        const int up = gated && (lane & 8) ? 1 : 0;
+        const int q = warp & 3, group = (warp - 3) / 4, row = q * 32 + lane;
+        const uint32_t column = tmem + group * kSumColumns + (static_cast<uint32_t>(q * 32) << 16);
         Ring<kAccs> accs;
         Ring<kScaleStages> scs;
         bool ok = true;
         for (int g = blockIdx.x; g < tiles && ok; g += gridDim.x) {
-            const Tile r = tile_at<kRows>(g, t, p.E, feature_tiles, tile_features);
-            uint64_t sum[16];
+            const Tile r = tile_at<kRows>(g, t, p.E, feature_tiles, kTileFeatures);
+            uint64_t sum[kSumColumns / 2];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sum[i] = 0;
+            for (int i = 0; i < kSumColumns / 2; ++i) sum[i] = 0;
             for (int kb = 0; kb < k_blocks; ++kb, accs.next(), scs.next()) {
                 ok = warp_wait(&s->sc_full[scs.stage], scs.parity) && warp_wait(&s->acc_full[accs.stage], accs.parity);
                 if (!ok) break;
                 tcgen05_after_sync();
-                float v[32];
-                tmem_load32(column + accs.stage * kRows, v);
-                tcgen05_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s->acc_empty[accs.stage]);
-                add_scaled(sum, v, s->scales[scs.stage][up] + c0);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s->sc_empty[scs.stage]);
+                const float f0 = s->scales[scs.stage][kGated ? 0 : group / 2][row];
+                const float f1 = kGated ? s->scales[scs.stage][1][row] : f0;
+                const uint64_t s0 = pair(f0, f0), s1 = pair(f1, f1);
+#pragma unroll
+                for (int c = 0; c < kSumColumns / 16; ++c) {
+                    float v[16];
+                    tmem_load16(column + accs.stage * kFeatures + c * 16, v);
+                    if (c == kSumColumns / 16 - 1) {
+                        tcgen05_before_sync();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&s->acc_empty[accs.stage]);
+                            mbar_arrive(&s->sc_empty[scs.stage]);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) fma2(sum[c * 8 + i], pair(v[2 * i], v[2 * i + 1]), i < 4 ? s0 : s1);
+                }
             }
             if (!ok) break;
-            if (c0 < r.rows) {
-                float v[32];
+            const int64_t d = static_cast<int64_t>(t.first[r.e]) + r.row0 + row;
+            if (row < r.rows && EP_IN(d, p.rows))
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(static_cast<uint32_t>(sum[i / 2] >> (i % 2 * 32)));
-                finish_columns<kProduct>(p, t, r, t.first[r.e] + r.row0, q, lane, bias_of(p, r, q, lane), c0, v);
-            }
+                for (int c = 0; c < kSumColumns / 16; ++c) {
+                    const int f = r.f0 + (group * kSumColumns + c * 16) / (kGated ? 2 : 1);
+                    float v[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = part_of(sum + c * 8, i);
+                    if (f < p.F) finish_row(p, r.e, d, f, v);
+                }
+            __syncwarp();
         }
         if (!ok) atomicOr(p.status, EP_ERR_TIMEOUT);
     }
     __syncthreads();
-    if (warp == 2) tmem_free<1>(tmem, kAccs * kRows);
+    if (warp == 2) tmem_free<1>(tmem, kAccs * kFeatures);
 }
 
 }  // namespace
@@ -260,16 +328,17 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
 cudaError_t launch_expert_gemm_fp8(const ExpertGemmParams& p, cudaStream_t stream) {
     const bool gated = p.act == EP_ACT_SWIGLU;
     Fp8Args a{product_args(p), p.x_sf, p.sf_row, p.sf_block, p.w_sf};
-    if (!(gated ? gated_map(&a.m.a, p.w, p.E, p.N, p.K, true) : weight_map(&a.m.a, p.w, p.E, p.Nw, p.K, kM, true)) ||
+    if (!(gated ? gated_map(&a.m.a, p.w, p.E, p.N, p.K, true) : weight_map(&a.m.a, p.w, p.E, p.Nw, p.K, 128, true)) ||
         !row_map(&a.m.b, p.x, p.rows, p.K, 64, true))
         return cudaErrorInvalidValue;
     const size_t smem = 1024 + kFp8Stages * kFp8Stage + sizeof(Fp8Shared) + static_cast<size_t>(p.E) * 12;
-    const cudaError_t e = cudaFuncSetAttribute(experts_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
+    const auto kernel = gated ? experts_fp8_kernel<true> : experts_fp8_kernel<false>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    const int per = gated ? kM / 2 : kM;
+    const int per = gated ? kFeatures / 2 : kFeatures;
     const int grid = std::max(1, std::min(device_info().num_sms, bound_tiles(p.rows / kRows + p.E, (p.N + per - 1) / per)));
-    return launch_experts(experts_fp8_kernel, dim3(grid), dim3(kFp8Threads), smem, stream, 1, a);
+    return launch_experts(kernel, dim3(grid), dim3(kFp8Threads), smem, stream, 1, a);
 }
 
 }  // namespace epg
