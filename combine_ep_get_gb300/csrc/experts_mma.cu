@@ -388,42 +388,45 @@ struct GradArgs {
     int32_t* status;
 };
 
+template <int kCtas>
 struct GradShape {
-    static constexpr int kStageBytes = (kM + kGradK) * kDepth * 2;
-    static constexpr int kStages = 4;
+    static constexpr int kColumnsOfX = kGradK / kCtas;   // in one CTA
+    static constexpr int kStageBytes = (kM + kColumnsOfX) * kDepth * 2;
+    static constexpr int kStages = 192 * 1024 / kStageBytes;
     static constexpr int kColumns = 2 * kGradK;
 };
 
+template <int kCtas>
 __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_constant__ GradArgs p) {
-    using S = GradShape;
+    using S = GradShape<kCtas>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stages = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
     Barriers* s = reinterpret_cast<Barriers*>(stages + S::kStages * S::kStageBytes);
     int* s_first = reinterpret_cast<int*>(s + 1);
     int* s_count = s_first + p.E;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    const int n_tiles = (p.Nw + kM - 1) / kM, k_tiles = (p.K + kGradK - 1) / kGradK;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
+    const int rank = kCtas == 2 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int n_tiles = (p.Nw + kM * kCtas - 1) / (kM * kCtas), k_tiles = (p.K + kGradK - 1) / kGradK;
     const int tiles = p.E * n_tiles * k_tiles;
+    const int worker = blockIdx.x / kCtas, workers = gridDim.x / kCtas;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(&s->full[i], 1);
             mbar_init(&s->empty[i], 1);
+            mbar_init(&s->tail_full[i], 1);
+            mbar_init(&s->cleared[i], 2 * kCtas);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s->acc_full[i], 1);
-            mbar_init(&s->acc_empty[i], 4);
-        }
-        for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(&s->tail_full[i], 1);
-            mbar_init(&s->cleared[i], 2);
+            mbar_init(&s->acc_empty[i], 4 * kCtas);
         }
         mbar_init(&s->drain, 1);
         fence_mbar_init();
         prefetch_map(&p.dz);
         prefetch_map(&p.x);
     }
-    if (warp == 2) tmem_alloc<1>(&s->tmem, S::kColumns);
+    if (warp == 2) tmem_alloc<kCtas>(&s->tmem, S::kColumns);
     pdl_wait();
     pdl_launch_dependents();
     for (int e = threadIdx.x; e < p.E; e += kThreads) {
@@ -433,92 +436,121 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
     }
     tcgen05_before_sync();
     __syncthreads();
+    if (kCtas == 2) cluster_sync();   // the pair's barriers are there for either
     tcgen05_after_sync();
     const uint32_t tmem = s->tmem;
     const auto expert_of = [&](int g) { return g / (n_tiles * k_tiles); };
-    const auto n0_of = [&](int g) { return g % (n_tiles * k_tiles) % n_tiles * kM; };
+    const auto n0_of = [&](int g) { return g % (n_tiles * k_tiles) % n_tiles * (kM * kCtas); };
     const auto k0_of = [&](int g) { return g % (n_tiles * k_tiles) / n_tiles * kGradK; };
+    // Arrive on a barrier of the CTA that issues the MMAs.
+    const auto arrive_issuer = [&](uint64_t* bar) {
+        if (kCtas == 1)
+            mbar_arrive(bar);
+        else
+            mbar_arrive_cluster(map_to_rank(smem_addr(bar), 0));
+    };
 
     if (warp == 0) {
-        if (lane == 0) {
-            int it = 0;
-            uint32_t tail_bits = 0, full_bits = 0, last_tail = 0;   // parities of the stages' next loads
-            bool ok = true;
-            for (int g = blockIdx.x; g < tiles && ok; g += gridDim.x) {
-                const int e = expert_of(g), n0 = n0_of(g), k0 = k0_of(g), cnt = s_count[e], first = s_first[e];
-                const int a_boxes = min(2, (p.Nw - n0 + 63) / 64), b_boxes = min(4, (p.K - k0 + 63) / 64);
-                for (int r = 0; r < cnt; r += kDepth, ++it) {
-                    const int st = it % S::kStages;
-                    ok = mbar_wait_bounded(&s->empty[st], ((it / S::kStages) & 1) ^ 1);
-                    if (!ok) break;
-                    uint8_t* sa = stages + st * S::kStageBytes;
-                    const bool tail = r + kDepth > cnt;
-                    uint64_t* const full = tail ? &s->tail_full[st] : &s->full[st];
-                    (tail ? tail_bits : full_bits) ^= 1u << st;
-                    last_tail = (last_tail & ~(1u << st)) | (static_cast<uint32_t>(tail) << st);
-                    const uint32_t bar = smem_addr(full);
-                    mbar_arrive_expect_tx(full, (a_boxes + b_boxes) * 8192);
-                    for (int i = 0; i < a_boxes; ++i) tma_load_2d<1>(sa + i * 8192, &p.dz, bar, n0 + 64 * i, first + r);
-                    for (int i = 0; i < b_boxes; ++i)
-                        tma_load_2d<1>(sa + kABytes + i * 8192, &p.x, bar, k0 + 64 * i, first + r);
+        Ring<S::kStages> ring;
+        int issued = 0;
+        uint32_t tail_bits = 0, full_bits = 0, last_tail = 0;   // parities of the stages' next loads
+        bool ok = true;
+        for (int g = worker; g < tiles && ok; g += workers) {
+            const int e = expert_of(g), n0 = n0_of(g), k0 = k0_of(g), cnt = s_count[e], first = s_first[e];
+            const auto a_boxes = [&](int who) { return max(0, min(2, (p.Nw - n0 - who * kM + 63) / 64)); };
+            const auto b_boxes = [&](int who) {
+                return max(0, min(S::kColumnsOfX / 64, (p.K - k0 - who * S::kColumnsOfX + 63) / 64));
+            };
+            const int mine_a = a_boxes(rank), mine_b = b_boxes(rank);
+            const int all = a_boxes(0) + b_boxes(0) + (kCtas == 2 ? a_boxes(1) + b_boxes(1) : 0);
+            for (int r = 0; r < cnt; r += kDepth, ++issued, ring.next()) {
+                ok = warp_wait(&s->empty[ring.stage], ring.parity ^ 1);
+                if (!ok) break;
+                const uint32_t bit = 1u << ring.stage;
+                const bool tail = r + kDepth > cnt;
+                (tail ? tail_bits : full_bits) ^= bit;
+                last_tail = tail ? last_tail | bit : last_tail & ~bit;
+                if (elect_one()) {
+                    uint8_t* const sa = stages + ring.stage * S::kStageBytes;
+                    uint8_t* const sb = sa + kABytes;
+                    const int nx = n0 + rank * kM, kx = k0 + rank * S::kColumnsOfX;
+                    if (tail) {   // each CTA's own barrier: its warps clear rows first
+                        const uint32_t bar = smem_addr(&s->tail_full[ring.stage]);
+                        mbar_arrive_expect_tx(&s->tail_full[ring.stage], (mine_a + mine_b) * 8192);
+                        for (int i = 0; i < mine_a; ++i)
+                            tma_load_2d<1>(sa + i * 8192, &p.dz, bar, nx + 64 * i, first + r);
+                        for (int i = 0; i < mine_b; ++i)
+                            tma_load_2d<1>(sb + i * 8192, &p.x, bar, kx + 64 * i, first + r);
+                    } else {
+                        uint32_t bar = smem_addr(&s->full[ring.stage]);
+                        if (kCtas == 2) bar = map_to_rank(bar, 0);
+                        if (rank == 0) mbar_arrive_expect_tx(&s->full[ring.stage], all * 8192);
+                        for (int i = 0; i < mine_a; ++i)
+                            tma_load_2d<kCtas>(sa + i * 8192, &p.dz, bar, nx + 64 * i, first + r);
+                        for (int i = 0; i < mine_b; ++i)
+                            tma_load_2d<kCtas>(sb + i * 8192, &p.x, bar, kx + 64 * i, first + r);
+                    }
                 }
-            }
-            if (!ok) atomicOr(p.status, EP_ERR_TIMEOUT);
-            // no copy may still be in flight when the CTA ends
-            for (int st = 0; st < S::kStages && st < it; ++st) {
-                const bool tail = (last_tail >> st) & 1;
-                if (!mbar_wait_bounded(tail ? &s->tail_full[st] : &s->full[st],
-                                       (((tail ? tail_bits : full_bits) >> st) & 1) ^ 1))
-                    break;
+                __syncwarp();
             }
         }
-        __syncwarp();
-    } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = instr_desc(false, true, true, kM, kGradK);
-            int it = 0, n = 0;
-            uint32_t tail_bits = 0, full_bits = 0;
-            bool ok = true;
-            for (int g = blockIdx.x; g < tiles && ok; g += gridDim.x) {
-                const int cnt = s_count[expert_of(g)];
-                if (cnt == 0) continue;
-                const uint32_t d = tmem + (n & 1) * kGradK;
-                ok = mbar_wait_bounded(&s->acc_empty[n & 1], ((n / 2) & 1) ^ 1);
+        if (!ok) atomicOr(p.status, EP_ERR_TIMEOUT);
+        // no copy may still be in flight when the CTA ends (a pair's end: rank 0 sees both CTAs')
+        for (int st = 0; st < S::kStages && st < issued; ++st) {
+            const bool tail = (last_tail >> st) & 1;
+            if (!tail && rank != 0) continue;
+            if (!warp_wait(tail ? &s->tail_full[st] : &s->full[st], (((tail ? tail_bits : full_bits) >> st) & 1) ^ 1))
+                break;
+        }
+    } else if (warp == 1 && rank == 0) {
+        const uint32_t idesc = instr_desc(false, true, true, kM * kCtas, kGradK);
+        const uint64_t desc_a = operand_desc(smem_addr(stages), 8192);
+        const uint64_t desc_b = operand_desc(smem_addr(stages) + kABytes, 8192);
+        Ring<S::kStages> ring;
+        Ring<2> accs;
+        uint32_t tail_bits = 0, full_bits = 0;
+        bool ok = true;
+        for (int g = worker; g < tiles && ok; g += workers) {
+            const int cnt = s_count[expert_of(g)];
+            if (cnt == 0) continue;
+            const uint32_t d = tmem + accs.stage * kGradK;
+            ok = warp_wait(&s->acc_empty[accs.stage], accs.parity ^ 1);
+            tcgen05_after_sync();
+            for (int r = 0; r < cnt && ok; r += kDepth, ring.next()) {
+                const bool tail = r + kDepth > cnt;
+                ok = warp_wait(tail ? &s->cleared[ring.stage] : &s->full[ring.stage],
+                               ((tail ? tail_bits : full_bits) >> ring.stage) & 1);
+                (tail ? tail_bits : full_bits) ^= 1u << ring.stage;
+                if (!ok) break;
                 tcgen05_after_sync();
-                for (int r = 0; r < cnt && ok; r += kDepth, ++it) {
-                    const int st = it % S::kStages;
-                    const bool tail = r + kDepth > cnt;
-                    ok = mbar_wait_bounded(tail ? &s->cleared[st] : &s->full[st],
-                                           ((tail ? tail_bits : full_bits) >> st) & 1);
-                    (tail ? tail_bits : full_bits) ^= 1u << st;
-                    if (!ok) break;
-                    tcgen05_after_sync();
-                    const uint32_t sa = smem_addr(stages + st * S::kStageBytes), sb = sa + kABytes;
+                if (elect_one()) {
+                    const uint64_t a = desc_at(desc_a, ring.stage * S::kStageBytes);
+                    const uint64_t b = desc_at(desc_b, ring.stage * S::kStageBytes);
 #pragma unroll
                     for (int k = 0; k < kDepth / 16; ++k)
-                        mma<1, false>(d, operand_desc(sa + k * 2048, 8192), operand_desc(sb + k * 2048, 8192), idesc,
-                                      r > 0 || k > 0);
-                    mma_commit<1>(&s->empty[st]);
+                        mma<kCtas, false>(d, desc_at(a, k * 2048), desc_at(b, k * 2048), idesc, r > 0 || k > 0);
+                    mma_commit<kCtas>(&s->empty[ring.stage]);
+                    if (r + kDepth >= cnt) mma_commit<kCtas>(&s->acc_full[accs.stage]);
                 }
-                if (ok) mma_commit<1>(&s->acc_full[n & 1]);
-                ++n;
+                __syncwarp();
             }
-            if (!ok) {
-                atomicOr(p.status, EP_ERR_TIMEOUT);
-                mma_commit<1>(&s->drain);
-                mbar_wait_bounded(&s->drain, 0);
-            }
+            accs.next();
         }
-        __syncwarp();
-    } else if (warp < 4) {
+        if (!ok) {
+            atomicOr(p.status, EP_ERR_TIMEOUT);
+            if (elect_one()) mma_commit<kCtas>(&s->drain);
+            __syncwarp();
+            warp_wait(&s->drain, 0);
+        }
+    } else if (warp == 2 || warp == 3) {
         int it = 0;
         uint32_t tail_bits = 0;
-        for (int g = blockIdx.x; g < tiles; g += gridDim.x) {
+        for (int g = worker; g < tiles; g += workers) {
             const int cnt = s_count[expert_of(g)], blocks = (cnt + kDepth - 1) / kDepth, valid = cnt % kDepth;
             it += blocks;
             if (valid == 0) continue;
             const int st = (it - 1) % S::kStages;
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&s->tail_full[st], (tail_bits >> st) & 1) ? 1 : 0)) {
+            if (!warp_wait(&s->tail_full[st], (tail_bits >> st) & 1)) {
                 atomicOr(p.status, EP_ERR_TIMEOUT);
                 break;
             }
@@ -526,18 +558,18 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
             // whole 128-byte rows of every 64-column box, so the swizzle does not matter
             const int clear = (kDepth - valid) * 8;
             uint8_t* base = stages + st * S::kStageBytes + valid * 128;
-            for (int box = 0; box < (kM + kGradK) / 64; ++box)
+            for (int box = 0; box < (kM + S::kColumnsOfX) / 64; ++box)
                 for (int i = (warp - 2) * 32 + lane; i < clear; i += 64)
                     *reinterpret_cast<uint4*>(base + box * 8192 + i * 16) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s->cleared[st]);
+            if (lane == 0) arrive_issuer(&s->cleared[st]);
         }
-    } else {
+    } else if (warp >= 4) {
         const int q = warp - 4;
-        int n = 0;
-        for (int g = blockIdx.x; g < tiles; g += gridDim.x) {
-            const int e = expert_of(g), n0 = n0_of(g), k0 = k0_of(g), cnt = s_count[e];
+        Ring<2> accs;
+        for (int g = worker; g < tiles; g += workers) {
+            const int e = expert_of(g), n0 = n0_of(g) + rank * kM, k0 = k0_of(g), cnt = s_count[e];
             const int row = n0 + q * 32 + lane;
             __nv_bfloat16* out = p.dw + (static_cast<int64_t>(e) * p.Nw + row) * p.K + k0;
             const int columns = row < p.Nw && EP_IN(e, p.E) ? min(kGradK, p.K - k0) : 0;
@@ -545,12 +577,12 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
                 for (int c = 0; c < columns; c += 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
                 continue;
             }
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&s->acc_full[n & 1], (n / 2) & 1) ? 1 : 0)) {
+            if (!warp_wait(&s->acc_full[accs.stage], accs.parity)) {
                 atomicOr(p.status, EP_ERR_TIMEOUT);
                 break;
             }
             tcgen05_after_sync();
-            const uint32_t acc = tmem + (n & 1) * kGradK + (static_cast<uint32_t>(q * 32) << 16);
+            const uint32_t acc = tmem + accs.stage * kGradK + (static_cast<uint32_t>(q * 32) << 16);
             for (int c0 = 0; c0 < kGradK; c0 += 32) {
                 float v[32];
                 __syncwarp();
@@ -558,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
                 if (c0 + 32 == kGradK) {
                     tcgen05_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&s->acc_empty[n & 1]);
+                    if (lane == 0) arrive_issuer(&s->acc_empty[accs.stage]);
                 }
 #pragma unroll
                 for (int c = 0; c < 32; c += 8)
@@ -566,11 +598,24 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
                         st_v4(out + c0 + c, make_uint4(pack2(v[c], v[c + 1]), pack2(v[c + 2], v[c + 3]),
                                                        pack2(v[c + 4], v[c + 5]), pack2(v[c + 6], v[c + 7])));
             }
-            ++n;
+            accs.next();
         }
     }
     __syncthreads();
-    if (warp == 2) tmem_free<1>(tmem, S::kColumns);
+    if (kCtas == 2) cluster_sync();   // neither CTA of a pair ends while the other may still reach it
+    if (warp == 2) tmem_free<kCtas>(tmem, S::kColumns);
+}
+
+template <int kCtas>
+cudaError_t launch_grad(const GradArgs& a, int64_t tiles, cudaStream_t stream) {
+    using S = GradShape<kCtas>;
+    const auto kernel = weight_grad_kernel<kCtas>;
+    const size_t smem = 1024 + S::kStages * S::kStageBytes + sizeof(Barriers) + 8 * static_cast<size_t>(a.E);
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const int workers = static_cast<int>(std::min<int64_t>(device_info().num_sms / kCtas, tiles));
+    return launch_experts(kernel, dim3(std::max(1, workers) * kCtas), dim3(kThreads), smem, stream, kCtas, a);
 }
 
 }  // namespace
@@ -613,14 +658,13 @@ cudaError_t launch_weight_grad(const ExpertBackwardParams& p, const __nv_bfloat1
     a.counts = p.counts;
     a.dw = p.dw;
     a.status = p.status;
-    const size_t smem = 1024 + GradShape::kStages * GradShape::kStageBytes + sizeof(Barriers) + 8 * p.E;
-    cudaError_t e = cudaFuncSetAttribute(weight_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    const int64_t tiles = static_cast<int64_t>(p.E) * ((p.Nw + kM - 1) / kM) * ((p.K + kGradK - 1) / kGradK);
-    if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-    const int grid = static_cast<int>(std::min<int64_t>(device_info().num_sms, tiles));
-    return launch_experts(weight_grad_kernel, dim3(grid), dim3(kThreads), smem, stream, 1, a);
+    const auto tiles = [&](int n) {
+        return static_cast<int64_t>(p.E) * ((p.Nw + n - 1) / n) * ((p.K + kGradK - 1) / kGradK);
+    };
+    if (tiles(kM) > INT32_MAX) return cudaErrorInvalidValue;
+    // pairs, as for the rows' products, unless they would leave SMs idle
+    if (tiles(2 * kM) * 2 > device_info().num_sms) return launch_grad<2>(a, tiles(2 * kM), stream);
+    return launch_grad<1>(a, tiles(kM), stream);
 }
 
 cudaError_t launch_few_tokens(const FewTokensParams& p, cudaStream_t stream) {

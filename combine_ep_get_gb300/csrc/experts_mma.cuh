@@ -54,7 +54,7 @@ struct Shape {
 
 struct Barriers {
     uint64_t full[12], empty[12], acc_full[2], acc_empty[2], drain;
-    uint64_t tail_full[4], cleared[4];   // weight gradient: an expert's last stage
+    uint64_t tail_full[6], cleared[6];   // weight gradient: an expert's last stage
     uint32_t tmem;
     int total_tiles;
     int warp_sum[8];
