@@ -24,5 +24,6 @@ _BINDING_NAMES = (
 def __getattr__(name):
     if name in _BINDING_NAMES:
         from . import binding
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)
+        return value
     raise AttributeError(name)

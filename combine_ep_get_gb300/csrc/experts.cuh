@@ -69,8 +69,10 @@ cudaError_t launch_few_tokens(const FewTokensParams& p, cudaStream_t stream);
 // The parts of these on the tensor cores.
 cudaError_t launch_expert_gemm_fp8(const ExpertGemmParams& p, cudaStream_t stream);
 cudaError_t launch_expert_gemm_bf16(const ExpertGemmParams& p, cudaStream_t stream);
-cudaError_t launch_input_grad(const ExpertBackwardParams& p, const __nv_bfloat16* dz, cudaStream_t stream);
-cudaError_t launch_weight_grad(const ExpertBackwardParams& p, const __nv_bfloat16* dz, cudaStream_t stream);
+cudaError_t launch_input_grad(const ExpertBackwardParams& p, const __nv_bfloat16* dz, bool wait_late,
+                              cudaStream_t stream);
+cudaError_t launch_weight_grad(const ExpertBackwardParams& p, const __nv_bfloat16* dz, bool wait_late,
+                               cudaStream_t stream);
 
 // launch_pdl with clusters of `cluster` CTAs.
 template <typename... KArgs, typename... Args>
@@ -94,8 +96,8 @@ cudaError_t launch_experts(void (*kernel)(KArgs...), dim3 grid, dim3 block, size
 }
 
 // Workspace carve-ups shared by the size queries and the calls.
-constexpr int kBackwardTileRows = 64;   // rows of one partial column sum of dz
-constexpr int kBackwardStrip = 512;     // columns of one partial row sum
+constexpr int kBackwardTileRows = 32;   // rows of one partial column sum of dz
+constexpr int kBackwardStrip = 256;     // columns of one partial row sum
 struct BackwardWorkspace {
     size_t off_dz, off_part, off_weight, total;
 };
@@ -127,29 +129,29 @@ inline FewWorkspace few_workspace(int T, int K, int H, int I) {
 // result plus |z| 2^-24 of it, far below the bf16 that it is rounded to; the
 // exact forms' branches cost the FP8 product's epilogue more than its stores.
 __device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+// The normal distribution function: erf by Abramowitz and Stegun, Handbook of
+// Mathematical Functions, 7.1.26 (off by at most 1.5e-7, the size of fp32's
+// own error in 1 + erf), whose exponential the density takes too.
+__device__ __forceinline__ float normal_cdf(float z, float* density) {
+    const float e = __expf(-0.5f * z * z);   // exp(-x^2), x = |z| / sqrt(2)
+    const float t = __fdividef(1.0f, fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.0f));
+    const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                                0.254829592f);
+    const float upper = 0.5f * poly * e;     // 1 - Phi(|z|)
+    *density = 0.39894228f * e;
+    return z < 0.0f ? upper : 1.0f - upper;
+}
 __device__ __forceinline__ float activate(float z, int act) {
     switch (act) {
         case EP_ACT_RELU: return fmaxf(z, 0.0f);
-        case EP_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+        case EP_ACT_GELU: {
+            float density;
+            return z * normal_cdf(z, &density);
+        }
         case EP_ACT_SILU: return silu(z);
         default: return z;
     }
 }
-// Its derivative.
-__device__ __forceinline__ float silu_slope(float z) {
-    const float s = 1.0f / (1.0f + expf(-z));
-    return s * (1.0f + z * (1.0f - s));
-}
-__device__ __forceinline__ float activate_slope(float z, int act) {
-    switch (act) {
-        case EP_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
-        case EP_ACT_GELU:
-            return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
-        case EP_ACT_SILU: return silu_slope(z);
-        default: return 1.0f;
-    }
-}
-
 // Rows of expert e that lie inside the arrays; the rest is skipped and flagged.
 __device__ __forceinline__ int expert_rows(const int32_t* offset, const int32_t* counts, int e, int64_t rows,
                                            int64_t* first, int32_t* status) {

@@ -3,9 +3,9 @@
 // (experts_mma.cu).
 //
 // The activation's pass reads dy and z and writes dz, each once: it is bound
-// by memory.  A block takes 64 rows of one expert x 512 columns (a strip),
+// by memory.  A block takes 32 rows of one expert x 256 columns (a strip),
 // each thread 8 neighbouring columns (16-byte loads and stores) of every
-// fourth row.  The bias' gradient is the sum of dz down the rows: 64 rows in
+// eighth row.  The bias' gradient is the sum of dz down the rows: 32 rows in
 // a block's registers, before dz is rounded, the blocks' sums then added in
 // order by a second kernel.  The row weights' gradient is the sum along a row
 // of dy * act(z): a strip's sum by shuffles, the strips' sums added in order
@@ -18,6 +18,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kVecs = kBackwardStrip / 8;      // 8-column vectors of a strip
 constexpr int kRowLanes = kThreads / kVecs;    // rows at a time
+constexpr int kAhead = kBackwardTileRows / kRowLanes;   // rows of a thread
+static_assert(kVecs == 32, "a warp has a row of the strip");
 
 __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -59,19 +61,41 @@ __device__ __forceinline__ Tables row_tables(const ExpertBackwardParams& p, int*
     return t;
 }
 
-template <bool kGated>
+// act(z) and its derivative together (not for the gated one).  exp by the
+// hardware's exponential: off by about 2^-22 (1 + |z|) of the result.
+template <int kAct>
+__device__ __forceinline__ void activate_both(float z, float* a, float* slope) {
+    if (kAct == EP_ACT_RELU) {
+        *a = fmaxf(z, 0.0f);
+        *slope = z > 0.0f ? 1.0f : 0.0f;
+    } else if (kAct == EP_ACT_GELU) {
+        float density;
+        const float cdf = normal_cdf(z, &density);
+        *a = z * cdf;
+        *slope = fmaf(z, density, cdf);
+    } else if (kAct == EP_ACT_SILU || kAct == EP_ACT_SWIGLU) {
+        const float s = __fdividef(1.0f, 1.0f + __expf(-z));
+        *a = z * s;
+        *slope = s * (1.0f + z * (1.0f - s));
+    } else {
+        *a = z;
+        *slope = 1.0f;
+    }
+}
+
+template <int kAct>
 __global__ void __launch_bounds__(kThreads) activation_backward_kernel(const __grid_constant__ ExpertBackwardParams p) {
+    constexpr bool kGated = kAct == EP_ACT_SWIGLU;
     extern __shared__ int tables[];
     __shared__ int warp_sum[kThreads / 32];
     __shared__ float sums[kRowLanes][kBackwardStrip];
-    __shared__ float row_sum[kBackwardTileRows][kVecs / 32];
     pdl_wait();
     pdl_launch_dependents();
     const Tables t = row_tables(p, tables, warp_sum);
     const int strips = (p.N + kBackwardStrip - 1) / kBackwardStrip;
     const int row_tiles = t.tile_end[p.E - 1];
     const int vec = threadIdx.x % kVecs, row_lane = threadIdx.x / kVecs;
-    const bool need_z = p.act != EP_ACT_NONE || p.d_row_weight;
+    const bool need_z = kAct != EP_ACT_NONE || p.d_row_weight;
     for (int64_t g = blockIdx.x; g < static_cast<int64_t>(row_tiles) * strips; g += gridDim.x) {
         const int tile = static_cast<int>(g / strips), strip = static_cast<int>(g % strips);
         int lo = 0, hi = p.E - 1;
@@ -86,45 +110,55 @@ __global__ void __launch_bounds__(kThreads) activation_backward_kernel(const __g
         const int rows = min(kBackwardTileRows, t.count[lo] - row0);
         const int64_t first = static_cast<int64_t>(t.first[lo]) + row0;
         const int n = strip * kBackwardStrip + vec * 8;
-        float sum[kGated ? 2 : 1][8] = {};
-        for (int r = row_lane; r < kBackwardTileRows; r += kRowLanes) {
-            const int64_t d = first + r;
-            float dot = 0.0f;
-            if (r < rows && n < p.N && EP_IN(d, p.rows)) {
-                float dy[8], z[8], u[8], dz[8], du[8];
-                unpack8(ld_stream_v4(p.dy + d * p.N + n), dy);
-                if (need_z) unpack8(ld_stream_v4(p.z + d * p.Nw + n), z);
-                if (kGated) unpack8(ld_stream_v4(p.z + d * p.Nw + p.N + n), u);
-                const float w = p.row_weight ? p.row_weight[d] : 1.0f;
+        // a thread's rows are all asked for before the first is used; rows and
+        // columns that are not there are zeros
+        uint4 dy_v[kAhead], z_v[kAhead], u_v[kAhead];
+        float w_v[kAhead];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float da = dy[i] * w;
-                    if (kGated) {
-                        const float s = 1.0f / (1.0f + expf(-z[i])), a = z[i] * s;
-                        dz[i] = da * u[i] * (s * (1.0f + z[i] * (1.0f - s)));
-                        du[i] = da * a;
-                        sum[kGated ? 1 : 0][i] += du[i];
-                        dot = fmaf(dy[i], a * u[i], dot);
-                    } else {
-                        dz[i] = p.act == EP_ACT_NONE ? da : da * activate_slope(z[i], p.act);
-                        if (p.d_row_weight) dot = fmaf(dy[i], activate(z[i], p.act), dot);
-                    }
-                    sum[0][i] += dz[i];
-                }
-                if (p.dz) {
-                    st_v4(p.dz + d * p.Nw + n, pack8(dz));
-                    if (kGated) st_v4(p.dz + d * p.Nw + p.N + n, pack8(du));
-                }
-            }
-            if (p.d_row_weight) {
-                for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-                if ((threadIdx.x & 31) == 0) row_sum[r][vec / 32] = dot;
-            }
+        for (int j = 0; j < kAhead; ++j) {
+            const int r = row_lane + j * kRowLanes;
+            const int64_t d = first + r;
+            const bool here = n < p.N && r < rows && EP_IN(d, p.rows);
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            dy_v[j] = here ? ld_stream_v4(p.dy + d * p.N + n) : zero;
+            z_v[j] = here && need_z ? ld_stream_v4(p.z + d * p.Nw + n) : zero;
+            if (kGated) u_v[j] = here ? ld_stream_v4(p.z + d * p.Nw + p.N + n) : zero;
+            w_v[j] = here && p.row_weight ? p.row_weight[d] : 1.0f;
         }
-        if (p.d_row_weight) {
-            __syncthreads();
-            if (threadIdx.x < rows && EP_IN(first + threadIdx.x, p.rows))
-                p.weight_part[strip * p.rows + first + threadIdx.x] = row_sum[threadIdx.x][0] + row_sum[threadIdx.x][1];
+        float sum[kGated ? 2 : 1][8] = {};
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int r = row_lane + j * kRowLanes;
+            const int64_t d = first + r;
+            const bool here = n < p.N && r < rows && EP_IN(d, p.rows);
+            float dy[8], z[8], u[8], dz[8], du[8], dot = 0.0f;
+            unpack8(dy_v[j], dy);
+            unpack8(z_v[j], z);
+            if (kGated) unpack8(u_v[j], u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float da = dy[i] * w_v[j];
+                float a, slope;
+                activate_both<kAct>(z[i], &a, &slope);
+                if (kGated) {
+                    dz[i] = da * u[i] * slope;
+                    du[i] = da * a;
+                    sum[kGated ? 1 : 0][i] += du[i];
+                    a *= u[i];
+                } else {
+                    dz[i] = da * slope;
+                }
+                sum[0][i] += dz[i];
+                dot = fmaf(dy[i], a, dot);
+            }
+            if (p.dz && here) {
+                st_v4(p.dz + d * p.Nw + n, pack8(dz));
+                if (kGated) st_v4(p.dz + d * p.Nw + p.N + n, pack8(du));
+            }
+            if (p.d_row_weight) {   // a row of the strip is one warp's
+                for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                if (vec == 0 && r < rows && EP_IN(d, p.rows)) p.weight_part[strip * p.rows + d] = dot;
+            }
         }
         if (p.dbias)
             for (int half = 0; half < (kGated ? 2 : 1); ++half) {
@@ -139,7 +173,6 @@ __global__ void __launch_bounds__(kThreads) activation_backward_kernel(const __g
                         p.bias_part[static_cast<int64_t>(tile) * p.Nw + half * p.N + strip * kBackwardStrip + c] = v;
                     }
             }
-        __syncthreads();
     }
 }
 
@@ -202,12 +235,15 @@ cudaError_t launch_expert_backward(const ExpertBackwardParams& given, cudaStream
     const __nv_bfloat16* dz = plain ? p.dy : p.dz;
     if (plain || (!p.dx && !p.dw)) p.dz = nullptr;
     if (p.rows > 0 && (p.dz || p.dbias || p.d_row_weight)) {
-        const auto kernel =
-            p.act == EP_ACT_SWIGLU ? activation_backward_kernel<true> : activation_backward_kernel<false>;
+        void (*const kernels[])(ExpertBackwardParams) = {
+            activation_backward_kernel<EP_ACT_NONE>, activation_backward_kernel<EP_ACT_RELU>,
+            activation_backward_kernel<EP_ACT_GELU>, activation_backward_kernel<EP_ACT_SILU>,
+            activation_backward_kernel<EP_ACT_SWIGLU>};
         const int64_t tiles =
             (p.rows / kBackwardTileRows + p.E) * static_cast<int64_t>((p.N + kBackwardStrip - 1) / kBackwardStrip);
-        const int grid = static_cast<int>(tiles < device_info().num_sms * 4 ? tiles : device_info().num_sms * 4);
-        const cudaError_t e = launch_experts(kernel, dim3(grid), dim3(kThreads), static_cast<size_t>(p.E) * 12, stream, 1, p);
+        const int grid = static_cast<int>(tiles < device_info().num_sms * 8 ? tiles : device_info().num_sms * 8);
+        const cudaError_t e = launch_experts(kernels[p.act], dim3(grid), dim3(kThreads),
+                                              static_cast<size_t>(p.E) * 12, stream, 1, p);
         if (e != cudaSuccess) return e;
     }
     if (p.dbias || p.d_row_weight) {
@@ -220,11 +256,16 @@ cudaError_t launch_expert_backward(const ExpertBackwardParams& given, cudaStream
                                          stream, 1, p, static_cast<int>(bias_blocks), row_blocks);
         if (e != cudaSuccess) return e;
     }
+    // Both products need only dz.  A kernel between them and dz's has waited
+    // for dz before it let them start, so they need not wait for it to end
+    // until they end themselves: each fills the SMs that the one before frees.
+    bool late = p.dbias || p.d_row_weight;
     if (p.dx) {
-        const cudaError_t e = launch_input_grad(p, dz, stream);
+        const cudaError_t e = launch_input_grad(p, dz, late, stream);
         if (e != cudaSuccess) return e;
+        late = true;
     }
-    return p.dw ? launch_weight_grad(p, dz, stream) : cudaSuccess;
+    return p.dw ? launch_weight_grad(p, dz, late, stream) : cudaSuccess;
 }
 
 }  // namespace epg

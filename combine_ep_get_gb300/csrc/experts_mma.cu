@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
     // The down product's kernel may start, and route, once every CTA of the
     // up product's has seen its own inputs complete.
     if (kMode != kFewDown) {
-        pdl_wait();
+        if (!p.wait_late) pdl_wait();
         pdl_launch_dependents();
     }
 
@@ -332,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
             }
         }
     }
+    if (p.wait_late) pdl_wait();
     __syncthreads();
     if (kCtas == 2) cluster_sync();   // neither CTA of a pair ends while the other may still reach it
     if (warp == 2) tmem_free<kCtas>(tmem, S::kColumns);
@@ -380,19 +381,21 @@ constexpr int kGradK = 256;      // columns of a tile
 
 struct GradArgs {
     CUtensorMap dz, x;           // boxes of 64 columns x 64 rows
+    CUtensorMap out;             // dw, boxes of 64 columns x 32 rows
     int Nw, K, E;
     int64_t rows;
     const int32_t* expert_offset;
     const int32_t* counts;
-    __nv_bfloat16* dw;           // [E][Nw][K]
     int32_t* status;
+    int wait_late;               // as in MmaArgs
 };
 
 template <int kCtas>
 struct GradShape {
     static constexpr int kColumnsOfX = kGradK / kCtas;   // in one CTA
     static constexpr int kStageBytes = (kM + kColumnsOfX) * kDepth * 2;
-    static constexpr int kStages = 192 * 1024 / kStageBytes;
+    static constexpr int kStages = 160 * 1024 / kStageBytes;
+    static constexpr int kOutBytes = 4 * 2 * 4096;   // two boxes of dw for each warp of the epilogue
     static constexpr int kColumns = 2 * kGradK;
 };
 
@@ -401,7 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
     using S = GradShape<kCtas>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stages = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
-    Barriers* s = reinterpret_cast<Barriers*>(stages + S::kStages * S::kStageBytes);
+    uint8_t* boxes = stages + S::kStages * S::kStageBytes;
+    Barriers* s = reinterpret_cast<Barriers*>(boxes + S::kOutBytes);
     int* s_first = reinterpret_cast<int*>(s + 1);
     int* s_count = s_first + p.E;
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
@@ -427,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
         prefetch_map(&p.x);
     }
     if (warp == 2) tmem_alloc<kCtas>(&s->tmem, S::kColumns);
-    pdl_wait();
+    if (!p.wait_late) pdl_wait();
     pdl_launch_dependents();
     for (int e = threadIdx.x; e < p.E; e += kThreads) {
         int64_t first;
@@ -570,37 +574,56 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
         Ring<2> accs;
         for (int g = worker; g < tiles; g += workers) {
             const int e = expert_of(g), n0 = n0_of(g) + rank * kM, k0 = k0_of(g), cnt = s_count[e];
-            const int row = n0 + q * 32 + lane;
-            __nv_bfloat16* out = p.dw + (static_cast<int64_t>(e) * p.Nw + row) * p.K + k0;
-            const int columns = row < p.Nw && EP_IN(e, p.E) ? min(kGradK, p.K - k0) : 0;
-            if (cnt == 0) {
-                for (int c = 0; c < columns; c += 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
-                continue;
+            const int row0 = n0 + q * 32;
+            const bool rows_here = row0 < p.Nw;   // the rows past Nw in a box are not stored
+            if (cnt > 0) {
+                if (!warp_wait(&s->acc_full[accs.stage], accs.parity)) {
+                    atomicOr(p.status, EP_ERR_TIMEOUT);
+                    break;
+                }
+                tcgen05_after_sync();
             }
-            if (!warp_wait(&s->acc_full[accs.stage], accs.parity)) {
-                atomicOr(p.status, EP_ERR_TIMEOUT);
-                break;
-            }
-            tcgen05_after_sync();
             const uint32_t acc = tmem + accs.stage * kGradK + (static_cast<uint32_t>(q * 32) << 16);
-            for (int c0 = 0; c0 < kGradK; c0 += 32) {
-                float v[32];
+            for (int c0 = 0; c0 < kGradK; c0 += 64) {
+                // 32 rows x 64 columns through shared memory: a warp storing
+                // 16 bytes of 32 rows at a time kept its loads waiting
+                uint8_t* const box = boxes + (q * 2 + (c0 / 64 & 1)) * 4096;
+                if (lane == 0) bulk_wait_read<1>();   // the box two stores ago
                 __syncwarp();
-                tmem_load32(acc + c0, v);
-                if (c0 + 32 == kGradK) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float v[32];
+                    if (cnt > 0) {
+                        tmem_load32(acc + c0 + 32 * h, v);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 32; c += 8)
+                        *reinterpret_cast<uint4*>(box + lane * 128 + ((4 * h + c / 8) ^ (lane & 7)) * 16) =
+                            make_uint4(pack2(v[c], v[c + 1]), pack2(v[c + 2], v[c + 3]), pack2(v[c + 4], v[c + 5]),
+                                       pack2(v[c + 6], v[c + 7]));
+                }
+                if (cnt > 0 && c0 + 64 == kGradK) {
                     tcgen05_before_sync();
                     __syncwarp();
                     if (lane == 0) arrive_issuer(&s->acc_empty[accs.stage]);
                 }
-#pragma unroll
-                for (int c = 0; c < 32; c += 8)
-                    if (c0 + c < columns)
-                        st_v4(out + c0 + c, make_uint4(pack2(v[c], v[c + 1]), pack2(v[c + 2], v[c + 3]),
-                                                       pack2(v[c + 4], v[c + 5]), pack2(v[c + 6], v[c + 7])));
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (rows_here && k0 + c0 < p.K) tma_store_3d(&p.out, box, k0 + c0, row0, e);
+                    bulk_commit();
+                }
             }
+            if (cnt == 0) continue;
             accs.next();
         }
+        if (lane == 0) bulk_wait_all<0>();
+        __syncwarp();
     }
+    if (p.wait_late) pdl_wait();
     __syncthreads();
     if (kCtas == 2) cluster_sync();   // neither CTA of a pair ends while the other may still reach it
     if (warp == 2) tmem_free<kCtas>(tmem, S::kColumns);
@@ -610,7 +633,7 @@ template <int kCtas>
 cudaError_t launch_grad(const GradArgs& a, int64_t tiles, cudaStream_t stream) {
     using S = GradShape<kCtas>;
     const auto kernel = weight_grad_kernel<kCtas>;
-    const size_t smem = 1024 + S::kStages * S::kStageBytes + sizeof(Barriers) + 8 * static_cast<size_t>(a.E);
+    const size_t smem = 1024 + S::kStages * S::kStageBytes + S::kOutBytes + sizeof(Barriers) + 8 * static_cast<size_t>(a.E);
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
@@ -628,7 +651,8 @@ cudaError_t launch_expert_gemm_bf16(const ExpertGemmParams& p, cudaStream_t stre
     return launch_rows<kProduct>(a, stream);
 }
 
-cudaError_t launch_input_grad(const ExpertBackwardParams& p, const __nv_bfloat16* dz, cudaStream_t stream) {
+cudaError_t launch_input_grad(const ExpertBackwardParams& p, const __nv_bfloat16* dz, bool wait_late,
+                              cudaStream_t stream) {
     MmaArgs a{};
     if (!weight_map(&a.a, p.w, p.E, p.Nw, p.K, kDepth) || !row_map(&a.b, dz, p.rows, p.Nw, kDepth))
         return cudaErrorInvalidValue;
@@ -640,15 +664,18 @@ cudaError_t launch_input_grad(const ExpertBackwardParams& p, const __nv_bfloat16
     a.counts = p.counts;
     a.y = p.dx;
     a.status = p.status;
+    a.wait_late = wait_late;
     return launch_rows<kInputGrad>(a, stream);
 }
 
-cudaError_t launch_weight_grad(const ExpertBackwardParams& p, const __nv_bfloat16* dz, cudaStream_t stream) {
+cudaError_t launch_weight_grad(const ExpertBackwardParams& p, const __nv_bfloat16* dz, bool wait_late,
+                               cudaStream_t stream) {
     GradArgs a{};
+    a.wait_late = wait_late;
     // no rows: nothing is loaded, but a map needs an extent
     const int64_t rows = std::max<int64_t>(p.rows, 1);
     if (!row_map(&a.dz, p.rows > 0 ? dz : p.dw, rows, p.Nw, kDepth) ||
-        !row_map(&a.x, p.rows > 0 ? p.x : p.dw, rows, p.K, kDepth))
+        !row_map(&a.x, p.rows > 0 ? p.x : p.dw, rows, p.K, kDepth) || !weight_map(&a.out, p.dw, p.E, p.Nw, p.K, 32))
         return cudaErrorInvalidValue;
     a.Nw = p.Nw;
     a.K = p.K;
@@ -656,7 +683,6 @@ cudaError_t launch_weight_grad(const ExpertBackwardParams& p, const __nv_bfloat1
     a.rows = p.rows;
     a.expert_offset = p.expert_offset;
     a.counts = p.counts;
-    a.dw = p.dw;
     a.status = p.status;
     const auto tiles = [&](int n) {
         return static_cast<int64_t>(p.E) * ((p.Nw + n - 1) / n) * ((p.K + kGradK - 1) / kGradK);

@@ -41,6 +41,7 @@ struct MmaArgs {
     int done_words;
     __nv_bfloat16* out;           // [T][F]
     int32_t* status;
+    int wait_late;                // the inputs are complete: wait for the kernel before only at the end
 };
 
 template <int NT, int kCtas>

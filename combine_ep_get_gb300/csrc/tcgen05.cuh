@@ -100,6 +100,11 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* m, uin
             "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::
                 "r"(smem_addr(dst)), "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v) : "memory");
 }
+// A box from shared to global memory, in the issuing thread's bulk group.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(m),
+                 "r"(smem_addr(src)), "r"(x), "r"(y), "r"(z) : "memory");
+}
 // Four rows of a map whose box is one row high, by their indices.
 __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* m, uint32_t bar, int x, int r0, int r1,
                                             int r2, int r3) {
