@@ -13,7 +13,7 @@
 // One CTA per SM, or a pair of CTAs on a tile twice as wide in features, walks
 // the tiles (expert, rows, features): warp 0 issues the
 // tensor-map loads of 128-byte-swizzled operand tiles, 64 terms of the sum a
-// stage; warp 1 issues the MMAs; warps 4-7 read the accumulators, lane =
+// stage; warp 1 issues the MMAs; warps 4-11 read the accumulators, lane =
 // feature, and apply the epilogue.
 //
 // SWIGLU: the 128 features of a tile are, in turns, 8 gate rows and the 8 up
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s->acc_full[i], 1);
-            mbar_init(&s->acc_empty[i], 4 * kCtas);
+            mbar_init(&s->acc_empty[i], kReadWarps * kCtas);
         }
         mbar_init(&s->drain, 1);
         s->gave_up = 0;
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
             warp_wait(&s->drain, 0);
         }
     } else if (warp >= 4) {
-        const int q = warp - 4;
+        const int q = warp & 3, turn = (warp - 4) / 4;
         Ring<2> accs;
         for (int g = worker; g < tiles; g += workers, accs.next()) {
             Tile r = tile_at<NT, kStep>(g, t, p.E, feature_tiles, tile_features);
@@ -275,14 +275,16 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
                 atomicOr(p.status, EP_ERR_TIMEOUT);
                 s->gave_up = 1;
             }
-            if (kMode == kFewDown) named_barrier(1, 128);   // its barriers below are for all four warps
+            if (kMode == kFewDown) named_barrier(1, kReadWarps * 32);   // its barriers below are for all of these warps
             if (kMode == kFewDown ? *reinterpret_cast<volatile int*>(&s->gave_up) != 0 : !ready) break;
             tcgen05_after_sync();
-            for (int c0 = 0; c0 < r.width; c0 += 32) {
+            const int last = (r.width - 1) / 32;   // 32-column step
+            for (int step = turn; step == turn || step <= last; step += 2) {
+                const int c0 = step * 32;
                 float v[32];
                 __syncwarp();
-                tmem_load32(acc + c0, v);
-                if (c0 + 32 >= r.width) {
+                if (step <= last) tmem_load32(acc + c0, v);
+                if (step + 2 > last) {
                     tcgen05_before_sync();
                     __syncwarp();
                     if (lane == 0) {
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
                             mbar_arrive_cluster(map_to_rank(smem_addr(&s->acc_empty[accs.stage]), 0));
                     }
                 }
-                finish_columns<kMode>(p, t, r, first, q, lane, bias, c0, v);
+                if (step <= last) finish_columns<kMode>(p, t, r, first, q, lane, bias, c0, v);
             }
             if (kMode == kFewDown) {
                 // the tokens whose last expert this was: their sum over the
@@ -300,8 +302,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
                 const int tid = threadIdx.x - 128;
                 if (tid == 0) s->completed = 0;
                 __threadfence();
-                named_barrier(1, 128);
-                for (int j = tid; j < r.rows; j += 128) {
+                named_barrier(1, kReadWarps * 32);
+                for (int j = tid; j < r.rows; j += kReadWarps * 32) {
                     const int tok = t.list[first + j] / p.K;
                     int experts = 0;
                     for (int k = 0; k < p.K; ++k) experts += t.expert[tok * p.K + k] >= 0;
@@ -311,10 +313,10 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
                         t.expert[p.T * p.K + atomicAdd(&s->completed, 1)] = static_cast<int16_t>(tok);
                     }
                 }
-                named_barrier(1, 128);
+                named_barrier(1, kReadWarps * 32);
                 const int m = s->completed;
-                const int feature = r.f0 + tid;
-                for (int i = 0; i < m; ++i) {
+                const int feature = r.f0 + tid % kM;
+                for (int i = tid / kM; i < m; i += kReadWarps * 32 / kM) {
                     const int tok = t.expert[p.T * p.K + i];
                     if (feature >= p.F || !EP_IN(tok, p.T)) continue;
                     float sum = 0.0f;
@@ -328,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
                     if (p.residual) sum += __bfloat162float(p.residual[at]);
                     p.out[at] = __float2bfloat16(sum);
                 }
-                named_barrier(1, 128);
+                named_barrier(1, kReadWarps * 32);
             }
         }
     }
@@ -394,8 +396,8 @@ template <int kCtas>
 struct GradShape {
     static constexpr int kColumnsOfX = kGradK / kCtas;   // in one CTA
     static constexpr int kStageBytes = (kM + kColumnsOfX) * kDepth * 2;
-    static constexpr int kStages = 160 * 1024 / kStageBytes;
-    static constexpr int kOutBytes = 4 * 2 * 4096;   // two boxes of dw for each warp of the epilogue
+    static constexpr int kOutBytes = kReadWarps * 4096;   // a box of dw for each warp of the epilogue
+    static constexpr int kStages = (208 * 1024 - kOutBytes) / kStageBytes;
     static constexpr int kColumns = 2 * kGradK;
 };
 
@@ -423,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s->acc_full[i], 1);
-            mbar_init(&s->acc_empty[i], 4 * kCtas);
+            mbar_init(&s->acc_empty[i], kReadWarps * kCtas);
         }
         mbar_init(&s->drain, 1);
         fence_mbar_init();
@@ -570,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
             if (lane == 0) arrive_issuer(&s->cleared[st]);
         }
     } else if (warp >= 4) {
-        const int q = warp - 4;
+        const int q = warp & 3, turn = (warp - 4) / 4;
         Ring<2> accs;
         for (int g = worker; g < tiles; g += workers) {
             const int e = expert_of(g), n0 = n0_of(g) + rank * kM, k0 = k0_of(g), cnt = s_count[e];
@@ -584,11 +586,11 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
                 tcgen05_after_sync();
             }
             const uint32_t acc = tmem + accs.stage * kGradK + (static_cast<uint32_t>(q * 32) << 16);
-            for (int c0 = 0; c0 < kGradK; c0 += 64) {
+            for (int c0 = turn * 64; c0 < kGradK; c0 += 128) {
                 // 32 rows x 64 columns through shared memory: a warp storing
                 // 16 bytes of 32 rows at a time kept its loads waiting
-                uint8_t* const box = boxes + (q * 2 + (c0 / 64 & 1)) * 4096;
-                if (lane == 0) bulk_wait_read<1>();   // the box two stores ago
+                uint8_t* const box = boxes + (warp - 4) * 4096;
+                if (lane == 0) bulk_wait_read<0>();   // the store before
                 __syncwarp();
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -605,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
                             make_uint4(pack2(v[c], v[c + 1]), pack2(v[c + 2], v[c + 3]), pack2(v[c + 4], v[c + 5]),
                                        pack2(v[c + 6], v[c + 7]));
                 }
-                if (cnt > 0 && c0 + 64 == kGradK) {
+                if (cnt > 0 && c0 + 128 >= kGradK) {
                     tcgen05_before_sync();
                     __syncwarp();
                     if (lane == 0) arrive_issuer(&s->acc_empty[accs.stage]);

@@ -10,7 +10,8 @@
 namespace epg {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kReadWarps = 8;   // that read accumulators: two for each 32 lanes, taking turns at the columns
+constexpr int kThreads = 128 + kReadWarps * 32;
 constexpr int kM = 128;          // features of a tile
 constexpr int kDepth = 64;       // terms of the sum in a stage (128 bytes of bf16)
 constexpr int kABytes = kM * kDepth * 2;
@@ -58,7 +59,7 @@ struct Barriers {
     uint64_t tail_full[6], cleared[6];   // weight gradient: an expert's last stage
     uint32_t tmem;
     int total_tiles;
-    int warp_sum[8];
+    int warp_sum[kThreads / 32];
     int gave_up;                  // a wait of the epilogue ran out
     int completed;                // few tokens, down: tokens whose last expert this tile was
 };
