@@ -1,6 +1,8 @@
 // Parameter blocks and launchers of the experts' operators (experts*.cu).
 #pragma once
 
+#include <atomic>
+
 #include <cuda_bf16.h>
 
 #include "ep_internal.cuh"
@@ -73,6 +75,19 @@ cudaError_t launch_input_grad(const ExpertBackwardParams& p, const __nv_bfloat16
                               cudaStream_t stream);
 cudaError_t launch_weight_grad(const ExpertBackwardParams& p, const __nv_bfloat16* dz, bool wait_late,
                                cudaStream_t stream);
+
+// Lets a kernel use all the shared memory a block may have, once for a device
+// (`done` is the kernel's own; a second thread that does it too does no harm).
+constexpr int kMaxDevices = 64;
+inline cudaError_t allow_all_smem(const void* kernel, std::atomic<bool>* done) {
+    const DeviceInfo& info = device_info();
+    const bool known = info.device >= 0 && info.device < kMaxDevices;
+    if (known && done[info.device].load(std::memory_order_acquire)) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, info.max_smem_optin);
+    if (e == cudaSuccess && known) done[info.device].store(true, std::memory_order_release);
+    return e;
+}
 
 // launch_pdl with clusters of `cluster` CTAs.
 template <typename... KArgs, typename... Args>

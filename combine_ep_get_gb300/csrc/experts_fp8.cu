@@ -333,8 +333,8 @@ cudaError_t launch_expert_gemm_fp8(const ExpertGemmParams& p, cudaStream_t strea
         return cudaErrorInvalidValue;
     const size_t smem = 1024 + kFp8Stages * kFp8Stage + sizeof(Fp8Shared) + static_cast<size_t>(p.E) * 12;
     const auto kernel = gated ? experts_fp8_kernel<true> : experts_fp8_kernel<false>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    static std::atomic<bool> ready[2][kMaxDevices];
+    const cudaError_t e = allow_all_smem(reinterpret_cast<const void*>(kernel), ready[gated]);
     if (e != cudaSuccess) return e;
     const int per = gated ? kFeatures / 2 : kFeatures;
     const int grid = std::max(1, std::min(device_info().num_sms, bound_tiles(p.rows / kRows + p.E, (p.N + per - 1) / per)));

@@ -155,15 +155,15 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
     const uint32_t tmem = s->tmem;
     const int tiles = t.tile_end[p.E - 1] * feature_tiles;
 
-    if (kMode == kFewDown) {
-        pdl_wait();
-        pdl_launch_dependents();
+    if (kMode == kFewDown && (warp != 0 || worker >= tiles)) pdl_wait();
+    if (kMode == kFewDown) pdl_launch_dependents();
+    if (kMode == kFewDown && warp >= 4) {
         // tokens of no expert: their residual, or zeros
         for (int tok = blockIdx.x; tok < p.T; tok += gridDim.x) {
             bool any = false;
             for (int k = 0; k < p.K; ++k) any |= t.expert[tok * p.K + k] >= 0;
             if (!any)
-                for (int f = threadIdx.x; f < p.F; f += kThreads) {
+                for (int f = threadIdx.x - 128; f < p.F; f += kReadWarps * 32) {
                     const int64_t at = static_cast<int64_t>(tok) * p.F + f;
                     p.out[at] = p.residual ? p.residual[at] : __float2bfloat16(0.0f);
                 }
@@ -193,15 +193,12 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
                     const int entry = t.list[first + min(4 * lane + j, r.rows - 1)];
                     row[j] = kMode == kFewUp ? entry / p.K : entry;
                 }
-            for (int kb = 0; kb < k_blocks; ++kb, ++issued, ring.next()) {
-                ok = warp_wait(&s->empty[ring.stage], ring.parity ^ 1);
-                if (!ok) break;
-                uint8_t* const sa = stages + ring.stage * S::kStageBytes;
-                uint8_t* const sb = sa + kABytes;
-                uint32_t bar = smem_addr(&s->full[ring.stage]);
+            const auto load_weights = [&](int stage, int kb) {
+                uint8_t* const sa = stages + stage * S::kStageBytes;
+                uint32_t bar = smem_addr(&s->full[stage]);
                 if (kCtas == 2) bar = map_to_rank(bar, 0);
                 if (elect_one()) {
-                    if (rank == 0) mbar_arrive_expect_tx(&s->full[ring.stage], bytes);
+                    if (rank == 0) mbar_arrive_expect_tx(&s->full[stage], bytes);
                     if (kMode == kInputGrad) {
                         tma_load_3d<kCtas>(sa, &p.a, bar, f0, kb * kDepth, r.e);
                         tma_load_3d<kCtas>(sa + kABytes / 2, &p.a, bar, f0 + 64, kb * kDepth, r.e);
@@ -210,14 +207,37 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
                     } else {
                         tma_load_3d<kCtas>(sa, &p.a, bar, kb * kDepth, f0, r.e);
                     }
-                    if (!kFew)
-                        for (int i = 0; i < boxes; ++i)
-                            tma_load_2d<kCtas>(sb + i * S::kBoxRows * kDepth * 2, &p.b, bar, kb * kDepth,
-                                               first + i * S::kBoxRows);
                 }
                 __syncwarp();
-                if (kFew && lane < boxes)
-                    tma_gather4(sb + lane * 4 * kDepth * 2, &p.b, bar, kb * kDepth, row[0], row[1], row[2], row[3]);
+            };
+            const auto load_rows = [&](int stage, int kb) {
+                uint8_t* const sb = stages + stage * S::kStageBytes + kABytes;
+                uint32_t bar = smem_addr(&s->full[stage]);
+                if (kCtas == 2) bar = map_to_rank(bar, 0);
+                if (kFew) {
+                    if (lane < boxes)
+                        tma_gather4(sb + lane * 4 * kDepth * 2, &p.b, bar, kb * kDepth, row[0], row[1], row[2], row[3]);
+                } else if (elect_one()) {
+                    for (int i = 0; i < boxes; ++i)
+                        tma_load_2d<kCtas>(sb + i * S::kBoxRows * kDepth * 2, &p.b, bar, kb * kDepth,
+                                           first + i * S::kBoxRows);
+                }
+                __syncwarp();
+            };
+            // the down product's first weights come while the up product ends
+            int early = 0;
+            if (kMode == kFewDown && issued == 0) {
+                early = min(S::kStages, k_blocks);
+                for (int kb = 0; kb < early; ++kb) load_weights(kb, kb);
+                pdl_wait();
+            }
+            for (int kb = 0; kb < k_blocks; ++kb, ++issued, ring.next()) {
+                if (issued >= early) {   // (not the first tile: early is 0)
+                    ok = warp_wait(&s->empty[ring.stage], ring.parity ^ 1);
+                    if (!ok) break;
+                    load_weights(ring.stage, kb);
+                }
+                load_rows(ring.stage, kb);
             }
         }
         if (!ok) atomicOr(p.status, EP_ERR_TIMEOUT);
@@ -352,7 +372,8 @@ template <int kMode, int NT, int kCtas>
 cudaError_t launch(const MmaArgs& a, int tiles_bound, cudaStream_t stream) {
     const size_t smem = smem_bytes<NT, kCtas>(a.E, a.T * a.K);
     const auto kernel = experts_mma_kernel<kMode, NT, kCtas>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    static std::atomic<bool> ready[kMaxDevices];
+    const cudaError_t e = allow_all_smem(reinterpret_cast<const void*>(kernel), ready);
     if (e != cudaSuccess) return e;
     const int workers = std::max(1, std::min(device_info().num_sms / kCtas, tiles_bound));
     return launch_experts(kernel, dim3(workers * kCtas), dim3(kThreads), smem, stream, kCtas, a);
@@ -636,8 +657,8 @@ cudaError_t launch_grad(const GradArgs& a, int64_t tiles, cudaStream_t stream) {
     using S = GradShape<kCtas>;
     const auto kernel = weight_grad_kernel<kCtas>;
     const size_t smem = 1024 + S::kStages * S::kStageBytes + S::kOutBytes + sizeof(Barriers) + 8 * static_cast<size_t>(a.E);
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    static std::atomic<bool> ready[kMaxDevices];
+    const cudaError_t e = allow_all_smem(reinterpret_cast<const void*>(kernel), ready);
     if (e != cudaSuccess) return e;
     const int workers = static_cast<int>(std::min<int64_t>(device_info().num_sms / kCtas, tiles));
     return launch_experts(kernel, dim3(std::max(1, workers) * kCtas), dim3(kThreads), smem, stream, kCtas, a);
