@@ -158,7 +158,7 @@ __device__ __forceinline__ float normal_cdf(float z, float* density) {
 }
 __device__ __forceinline__ float activate(float z, int act) {
     switch (act) {
-        case EP_ACT_RELU: return fmaxf(z, 0.0f);
+        case EP_ACT_RELU: return z < 0.0f ? 0.0f : z;   // NaN stays
         case EP_ACT_GELU: {
             float density;
             return z * normal_cdf(z, &density);

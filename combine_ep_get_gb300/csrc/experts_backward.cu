@@ -66,7 +66,7 @@ __device__ __forceinline__ Tables row_tables(const ExpertBackwardParams& p, int*
 template <int kAct>
 __device__ __forceinline__ void activate_both(float z, float* a, float* slope) {
     if (kAct == EP_ACT_RELU) {
-        *a = fmaxf(z, 0.0f);
+        *a = z < 0.0f ? 0.0f : z;
         *slope = z > 0.0f ? 1.0f : 0.0f;
     } else if (kAct == EP_ACT_GELU) {
         float density;

@@ -49,7 +49,8 @@ template <int NT, int kCtas>
 struct Shape {
     static constexpr int kRows = NT / kCtas;   // of the row operand in one CTA
     static constexpr int kStageBytes = kABytes + kRows * kDepth * 2;
-    static constexpr int kStages = (192 * 1024) / kStageBytes < 10 ? (192 * 1024) / kStageBytes : 10;
+    // few tokens (64 rows) keep room for 4096 entries beside 2048 experts' tables
+    static constexpr int kStages = (NT == 64 ? 172 : 192) * 1024 / kStageBytes;
     static constexpr int kBoxRows = 64;
     static constexpr int kColumns = 2 * NT;    // of tensor memory
 };

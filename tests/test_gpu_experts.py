@@ -145,6 +145,30 @@ def test_product_fp8(counts, K, N, act, col):
     run_product(counts, K, N, act, bias=True, rw=True, res=True, save=True, fp8=True, col_major=col, gap=1, seed=K)
 
 
+def test_product_fp8_many_experts():
+    rng = np.random.Generator(np.random.PCG64(7))
+    run_product(rng.integers(0, 4, size=2048).tolist(), 128, 128, "swiglu", fp8=True, seed=7)
+
+
+@pytest.mark.parametrize("act", list(ACTS))
+def test_nan_and_infinity_follow_the_activation(act):
+    """NaN rows give NaN; +inf pre-activations give what the formula gives."""
+    from gpu_path import B
+    off, cnt, rows = blocks([3])
+    x = torch.zeros((rows, 64), dtype=torch.bfloat16, device="cuda")
+    x[0, 0], x[1, 0], x[2, 0] = NAN, float("inf"), 2.0
+    w = torch.zeros((1, 32 if act == "swiglu" else 16, 64), dtype=torch.bfloat16, device="cuda")
+    w[:, :, 0] = 1.0
+    y = torch.zeros((rows, 16), dtype=torch.bfloat16, device="cuda")
+    st = status()
+    B.ep_expert_gemm(x, w, off, cnt, y, st, activation=ACTS[act])
+    assert int(st.item()) == 0
+    assert bool(torch.isnan(y[0].float()).all()) and bool((y[1] == float("inf")).all())
+    a, e = ref.activate(torch.full((1, w.shape[1]), 2.0, dtype=torch.float64, device="cuda"),
+                        torch.zeros((1, w.shape[1]), dtype=torch.float64, device="cuda"), act)
+    ref.check(y[2:], a, ref.bf16_bound(a, e))
+
+
 def test_product_without_rows():
     from gpu_path import B
     off, cnt, _ = blocks([0, 0])
@@ -380,6 +404,7 @@ def run_few(T, K, E, H, I, act="swiglu", bias=False, res=False, mode="distinct",
     idx = to_dev(idx)
     Iw = 2 * I if act == "swiglu" else I
     x, tw = normal(g, T, H), torch.rand((T, K), generator=g, device="cuda") - 0.2
+    tw[idx == -1] = NAN     # masked entries' weights are not read into anything
     wu, wd = normal(g, E, Iw, H, std=H ** -0.5), normal(g, E, H, I, std=I ** -0.5)
     named = torch.unique(idx)
     off = torch.ones(E, dtype=torch.bool, device="cuda")
@@ -424,7 +449,7 @@ def test_few_activations(act):
 @pytest.mark.parametrize("T,K,E,H,I", [
     (1, 1, 1, 8, 8), (1, 8, 16, 256, 128), (2, 4, 7, 72, 200), (16, 8, 64, 512, 256), (17, 2, 3, 264, 1000),
     (128, 8, 32, 256, 192), (256, 16, 24, 128, 64), (256, 1, 2, 136, 72), (33, 16, 2048, 64, 64),
-    (64, 4, 256, 1024, 384),
+    (64, 4, 256, 1024, 384), (256, 16, 2048, 64, 64),
 ])
 def test_few_sizes(T, K, E, H, I):
     run_few(T, K, E, H, I, seed=T + K + E)
