@@ -17,7 +17,7 @@ _BINDING_NAMES = (
     "ep_bounds_checked", "EP_BF16", "EP_FP8_E4M3",
     "ep_expert_gemm", "ep_expert_gemm_backward", "ep_expert_gemm_backward_workspace_bytes",
     "ep_moe_few_tokens", "ep_moe_few_tokens_workspace_bytes", "EP_ACT_NONE", "EP_ACT_RELU", "EP_ACT_GELU",
-    "EP_ACT_SILU", "EP_ACT_SWIGLU",
+    "EP_ACT_SILU", "EP_ACT_SWIGLU", "EP_FEW_MAX_TOKENS", "EP_FEW_MAX_TOPK",
 )
 
 
