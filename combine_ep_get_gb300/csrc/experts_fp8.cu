@@ -30,7 +30,6 @@ constexpr int kRowBytes = kRows * kBlock;
 constexpr int kFp8Stage = kRowBytes + kFeatures * kBlock;
 constexpr int kFp8Stages = 4;
 constexpr int kAccs = 2;
-constexpr int kScaleStages = 8;
 constexpr int kScaleBatch = 8;         // blocks whose scales are asked for at once
 
 struct Fp8Args {
@@ -41,11 +40,11 @@ struct Fp8Args {
 };
 
 struct Fp8Shared {
-    uint64_t full[kFp8Stages], empty[kFp8Stages], acc_full[kAccs], acc_empty[kAccs];
-    uint64_t sc_full[kScaleStages], sc_empty[kScaleStages], drain;
+    // acc_full: the MMAs of a block and its scales; acc_empty: both may be overwritten
+    uint64_t full[kFp8Stages], empty[kFp8Stages], acc_full[kAccs], acc_empty[kAccs], drain;
     // a block's row scales times the two weight scales of the tile: of its
     // first and last 128 features, or of its gate and up features
-    float scales[kScaleStages][2][kRows];
+    float scales[kAccs][2][kRows];
     uint32_t tmem;
     int warp_sum[kFp8Warps];
 };
@@ -134,12 +133,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
             mbar_init(&s->empty[i], 1);
         }
         for (int i = 0; i < kAccs; ++i) {
-            mbar_init(&s->acc_full[i], 1);
+            mbar_init(&s->acc_full[i], 2);
             mbar_init(&s->acc_empty[i], kSumWarps);
-        }
-        for (int i = 0; i < kScaleStages; ++i) {
-            mbar_init(&s->sc_full[i], 1);
-            mbar_init(&s->sc_empty[i], kSumWarps);
         }
         mbar_init(&s->drain, 1);
         fence_mbar_init();
@@ -229,7 +224,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
         }
     } else if (warp == 2) {
         // lane l: the scales of rows l, l + 32, l + 64, l + 96
-        Ring<kScaleStages> scs;
+        Ring<kAccs> accs;
         bool ok = true;
         for (int g = blockIdx.x; g < tiles && ok; g += gridDim.x) {
             const Tile r = tile_at<kRows>(g, t, p.E, feature_tiles, kTileFeatures);
@@ -256,16 +251,16 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
 #pragma unroll
                 for (int i = 0; i < kScaleBatch; ++i) {
                     if (kb0 + i >= k_blocks || !ok) break;
-                    ok = warp_wait(&s->sc_empty[scs.stage], scs.parity ^ 1);
+                    ok = warp_wait(&s->acc_empty[accs.stage], accs.parity ^ 1);
                     if (!ok) break;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        s->scales[scs.stage][0][lane + 32 * j] = x[j][i] * a[i];
-                        s->scales[scs.stage][1][lane + 32 * j] = x[j][i] * b[i];
+                        s->scales[accs.stage][0][lane + 32 * j] = x[j][i] * a[i];
+                        s->scales[accs.stage][1][lane + 32 * j] = x[j][i] * b[i];
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&s->sc_full[scs.stage]);
-                    scs.next();
+                    if (lane == 0) mbar_arrive(&s->acc_full[accs.stage]);
+                    accs.next();
                 }
             }
         }
@@ -274,19 +269,18 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
         const int q = warp & 3, group = (warp - 3) / 4, row = q * 32 + lane;
         const uint32_t column = tmem + group * kSumColumns + (static_cast<uint32_t>(q * 32) << 16);
         Ring<kAccs> accs;
-        Ring<kScaleStages> scs;
         bool ok = true;
         for (int g = blockIdx.x; g < tiles && ok; g += gridDim.x) {
             const Tile r = tile_at<kRows>(g, t, p.E, feature_tiles, kTileFeatures);
             uint64_t sum[kSumColumns / 2];
 #pragma unroll
             for (int i = 0; i < kSumColumns / 2; ++i) sum[i] = 0;
-            for (int kb = 0; kb < k_blocks; ++kb, accs.next(), scs.next()) {
-                ok = warp_wait(&s->sc_full[scs.stage], scs.parity) && warp_wait(&s->acc_full[accs.stage], accs.parity);
+            for (int kb = 0; kb < k_blocks; ++kb, accs.next()) {
+                ok = warp_wait(&s->acc_full[accs.stage], accs.parity);
                 if (!ok) break;
                 tcgen05_after_sync();
-                const float f0 = s->scales[scs.stage][kGated ? 0 : group / 2][row];
-                const float f1 = kGated ? s->scales[scs.stage][1][row] : f0;
+                const float f0 = s->scales[accs.stage][kGated ? 0 : group / 2][row];
+                const float f1 = kGated ? s->scales[accs.stage][1][row] : f0;
                 const uint64_t s0 = pair(f0, f0), s1 = pair(f1, f1);
 #pragma unroll
                 for (int c = 0; c < kSumColumns / 16; ++c) {
@@ -295,10 +289,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
                     if (c == kSumColumns / 16 - 1) {
                         tcgen05_before_sync();
                         __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(&s->acc_empty[accs.stage]);
-                            mbar_arrive(&s->sc_empty[scs.stage]);
-                        }
+                        if (lane == 0) mbar_arrive(&s->acc_empty[accs.stage]);
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) fma2(sum[c * 8 + i], pair(v[2 * i], v[2 * i + 1]), i < 4 ? s0 : s1);
