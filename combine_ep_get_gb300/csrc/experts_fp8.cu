@@ -49,20 +49,6 @@ struct Fp8Shared {
     int warp_sum[kFp8Warps];
 };
 
-// Two fp32 multiply-adds in one instruction, each rounded as the scalar one;
-// pairs stay in 64-bit registers, or their packing would cost what it saves.
-__device__ __forceinline__ void fma2(uint64_t& sum, uint64_t a, uint64_t b) {
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(sum) : "l"(a), "l"(b));
-}
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-    uint64_t v;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
-    return v;
-}
-__device__ __forceinline__ float part_of(const uint64_t* sum, int i) {
-    return __uint_as_float(static_cast<uint32_t>(sum[i / 2] >> (i % 2 * 32)));
-}
-
 // The epilogue of 16 columns of a row: 16 features from f, or, gated, 8 from f
 // (8 gate columns, then 8 up ones).
 __device__ __forceinline__ void finish_row(const MmaArgs& p, int e, int64_t d, int f, float (&v)[16]) {
@@ -272,16 +258,15 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
         bool ok = true;
         for (int g = blockIdx.x; g < tiles && ok; g += gridDim.x) {
             const Tile r = tile_at<kRows>(g, t, p.E, feature_tiles, kTileFeatures);
-            uint64_t sum[kSumColumns / 2];
+            float sum[kSumColumns];
 #pragma unroll
-            for (int i = 0; i < kSumColumns / 2; ++i) sum[i] = 0;
+            for (int i = 0; i < kSumColumns; ++i) sum[i] = 0.0f;
             for (int kb = 0; kb < k_blocks; ++kb, accs.next()) {
                 ok = warp_wait(&s->acc_full[accs.stage], accs.parity);
                 if (!ok) break;
                 tcgen05_after_sync();
                 const float f0 = s->scales[accs.stage][kGated ? 0 : group / 2][row];
                 const float f1 = kGated ? s->scales[accs.stage][1][row] : f0;
-                const uint64_t s0 = pair(f0, f0), s1 = pair(f1, f1);
 #pragma unroll
                 for (int c = 0; c < kSumColumns / 16; ++c) {
                     float v[16];
@@ -292,7 +277,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
                         if (lane == 0) mbar_arrive(&s->acc_empty[accs.stage]);
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) fma2(sum[c * 8 + i], pair(v[2 * i], v[2 * i + 1]), i < 4 ? s0 : s1);
+                    for (int i = 0; i < 16; ++i) sum[c * 16 + i] = fmaf(v[i], i < 8 ? f0 : f1, sum[c * 16 + i]);
                 }
             }
             if (!ok) break;
@@ -303,7 +288,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
                     const int f = r.f0 + (group * kSumColumns + c * 16) / (kGated ? 2 : 1);
                     float v[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = part_of(sum + c * 8, i);
+                    for (int i = 0; i < 16; ++i) v[i] = sum[c * 16 + i];
                     if (f < p.F) finish_row(p, r.e, d, f, v);
                 }
             __syncwarp();

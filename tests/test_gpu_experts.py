@@ -145,6 +145,11 @@ def test_product_fp8(counts, K, N, act, col):
     run_product(counts, K, N, act, bias=True, rw=True, res=True, save=True, fp8=True, col_major=col, gap=1, seed=K)
 
 
+@pytest.mark.parametrize("K,N,act", [(384, 1024, "swiglu"), (256, 2176, "gelu")])
+def test_product_fp8_full_experts(K, N, act):
+    run_product([300, 0, 513, 257, 1000], K, N, act, bias=True, rw=True, res=True, save=True, fp8=True, gap=1, seed=N)
+
+
 def test_product_fp8_many_experts():
     rng = np.random.Generator(np.random.PCG64(7))
     run_product(rng.integers(0, 4, size=2048).tolist(), 128, 128, "swiglu", fp8=True, seed=7)
