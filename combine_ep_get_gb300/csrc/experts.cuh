@@ -167,6 +167,26 @@ __device__ __forceinline__ float activate(float z, int act) {
         default: return z;
     }
 }
+// The activation of n values; which one it is is asked once.
+template <int N>
+__device__ __forceinline__ void activate_all(float (&v)[N], int act) {
+    switch (act) {
+        case EP_ACT_RELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = activate(v[i], EP_ACT_RELU);
+            break;
+        case EP_ACT_GELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = activate(v[i], EP_ACT_GELU);
+            break;
+        case EP_ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = activate(v[i], EP_ACT_SILU);
+            break;
+        default: break;
+    }
+}
+
 // Rows of expert e that lie inside the arrays; the rest is skipped and flagged.
 __device__ __forceinline__ int expert_rows(const int32_t* offset, const int32_t* counts, int e, int64_t rows,
                                            int64_t* first, int32_t* status) {

@@ -290,6 +290,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
             const int first = t.first[r.e] + r.row0;
             const uint32_t acc = tmem + accs.stage * NT + (static_cast<uint32_t>(q * 32) << 16);
             const float bias = kMode == kInputGrad ? 0.0f : bias_of(p, r, q, lane);
+            Ahead ahead;
+            ask_ahead<kMode>(p, t, r, first, q, lane, turn * 32, &ahead);
             const bool ready = warp_wait(&s->acc_full[accs.stage], accs.parity);
             if (!ready) {
                 atomicOr(p.status, EP_ERR_TIMEOUT);
@@ -314,7 +316,9 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
                             mbar_arrive_cluster(map_to_rank(smem_addr(&s->acc_empty[accs.stage]), 0));
                     }
                 }
-                if (step <= last) finish_columns<kMode>(p, t, r, first, q, lane, bias, c0, v);
+                const Ahead now = ahead;
+                if (step + 2 <= last) ask_ahead<kMode>(p, t, r, first, q, lane, c0 + 64, &ahead);
+                if (step <= last) finish_columns<kMode>(p, t, r, first, q, lane, bias, c0, v, now);
             }
             if (kMode == kFewDown) {
                 // the tokens whose last expert this was: their sum over the

@@ -117,11 +117,12 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
-// Four-byte stores of two neighbouring features: the lanes of a pair trade
-// so that the even lane holds both features of token j, the odd one of j + 1.
-__device__ __forceinline__ float2 trade_pair(float first, float second, int lane) {
-    const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? first : second, 1);
-    return lane & 1 ? make_float2(got, second) : make_float2(first, got);
+// Two neighbouring lanes hold two neighbouring features, each of two tokens as
+// a pair of bf16: trading halves gives each lane both features of one token
+// (the even lane the first's, the odd one the second's), and back.
+__device__ __forceinline__ uint32_t trade_halves(uint32_t w, int lane) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, w, 1);
+    return __byte_perm(w, got, lane & 1 ? 0x3276 : 0x5410);
 }
 
 // A lane's feature of y and its row of W within the expert.
@@ -143,94 +144,133 @@ __device__ __forceinline__ float bias_of(const MmaArgs& p, const Tile& r, int q,
     return p.bias && l.f < p.F ? p.bias[static_cast<int64_t>(r.e) * Fw + l.wrow] : 0.0f;
 }
 
-// The epilogue of 32 of a tile's columns (its rows row0 + c0 ...), lane =
-// feature, q = the warp's 32 lanes of the accumulator.
+// The 32 columns c0 .. of a tile (its rows) as one lane sees them.  Stores and
+// loads of bf16 are four bytes, two neighbouring features of one token: a
+// lane's i-th is column `column0 + i * step`, 64 bytes of a row from 16 lanes
+// (gated: 32 from 8).
+template <int kMode>
+struct Columns {
+    static constexpr bool kFew = kMode == kFewUp || kMode == kFewDown;
+    const MmaArgs& p;
+    const Table& t;
+    int first, left, column0;   // first: of the 32; left: columns there are
+
+    __device__ __forceinline__ Columns(const MmaArgs& args, const Table& table, const Tile& r, int first_row, int lane,
+                                       int c0)
+        : p(args), t(table), first(first_row + c0), left(r.rows - c0) {
+        column0 = p.gate_half ? ((lane & 8) ? 1 : 0) + 2 * (lane & 1) : (lane & 1);
+    }
+    __device__ __forceinline__ int64_t row_of(int c) const {   // of column c of the 32
+        return kFew ? static_cast<int64_t>(t.list[first + c]) : static_cast<int64_t>(first) + c;
+    }
+    __device__ __forceinline__ bool has(int c) const { return c < left && EP_IN(row_of(c), p.rows); }
+    // A lane's words of rows of `pitch` elements, from feature f; none if !ok.
+    template <int kStep, class F>
+    __device__ __forceinline__ void words(__nv_bfloat16* base, int pitch, int f, bool ok, F use) const {
+        if (kFew) {
+#pragma unroll
+            for (int i = 0; i < 32 / kStep; ++i)
+                if (ok && has(column0 + i * kStep))
+                    use(i, reinterpret_cast<uint32_t*>(base + row_of(column0 + i * kStep) * pitch + f));
+        } else {
+            __nv_bfloat16* at = base + row_of(column0) * pitch + f;
+            const int64_t next = static_cast<int64_t>(kStep) * pitch;
+            const int here = ok ? left - column0 : 0;
+#pragma unroll
+            for (int i = 0; i < 32 / kStep; ++i, at += next)
+                if (i * kStep < here && EP_IN(row_of(column0 + i * kStep), p.rows))
+                    use(i, reinterpret_cast<uint32_t*>(at));
+        }
+    }
+};
+
+// What the epilogue of 32 columns reads: asked for before it is needed.  (The
+// residual may be y itself: its loads would have to wait for the stores
+// before them.)
+struct Ahead {
+    uint32_t residual[16];
+    float row_weight;   // of column `lane`
+};
+template <int kMode>
+__device__ __forceinline__ void ask_ahead(const MmaArgs& p, const Table& t, const Tile& r, int first, int q, int lane,
+                                          int c0, Ahead* a) {
+    if (kMode != kProduct || (!p.row_weight && !p.residual)) return;
+    const Columns<kMode> m(p, t, r, first, lane, c0);
+    const Lane l = lane_of(p, r, q, lane);
+    if (p.row_weight) a->row_weight = m.has(lane) ? p.row_weight[m.row_of(lane)] : 0.0f;
+    if (p.residual) {
+        __nv_bfloat16* const from = const_cast<__nv_bfloat16*>(p.residual);
+        const auto take = [&](int i, const uint32_t* at) { a->residual[i] = *at; };
+        if (p.gate_half)
+            m.template words<4>(from, p.F, l.f & ~1, l.f < p.F, take);
+        else
+            m.template words<2>(from, p.F, l.f & ~1, l.f < p.F, take);
+    }
+}
+
+// Row weight, residual and store of a lane's feature in N tokens, two for each
+// word: i-th word, o[2 i] and o[2 i + 1].  column(i): of o[i].
+template <int kMode, int kStep, class F>
+__device__ __forceinline__ void store_rows(const MmaArgs& p, const Columns<kMode>& m, const Lane& l, int lane,
+                                           const Ahead& ahead, float (&o)[64 / kStep], F column) {
+    if (kMode == kProduct && p.row_weight)
+#pragma unroll
+        for (int i = 0; i < 64 / kStep; ++i) o[i] *= __shfl_sync(0xffffffffu, ahead.row_weight, column(i));
+    if (kMode == kProduct && p.residual)
+#pragma unroll
+        for (int i = 0; i < 32 / kStep; ++i) {
+            const float2 s = unpack2(trade_halves(ahead.residual[i], lane));
+            o[2 * i] += s.x;
+            o[2 * i + 1] += s.y;
+        }
+    uint32_t w[32 / kStep];
+#pragma unroll
+    for (int i = 0; i < 32 / kStep; ++i) w[i] = trade_halves(pack2(o[2 * i], o[2 * i + 1]), lane);
+    m.template words<kStep>(p.y, p.F, l.f & ~1, l.f < p.F, [&](int i, uint32_t* at) { *at = w[i]; });
+}
+
+// The epilogue of 32 of a tile's columns, lane = feature, q = the warp's 32
+// lanes of the accumulator.
 template <int kMode>
 __device__ __forceinline__ void finish_columns(const MmaArgs& p, const Table& t, const Tile& r, int first, int q,
-                                               int lane, float bias, int c0, float (&v)[32]) {
-    constexpr bool kFew = kMode == kFewUp || kMode == kFewDown;
+                                               int lane, float bias, int c0, float (&v)[32], const Ahead& ahead) {
+    const Columns<kMode> m(p, t, r, first, lane, c0);
     const Lane l = lane_of(p, r, q, lane);
-    const bool gated = p.gate_half != 0, up = l.up, f_ok = l.f < p.F;
-    const int f = l.f, wrow = l.wrow, Fw = gated ? 2 * p.F : p.F;
-    const auto row_of = [&](int j) -> int64_t {
-        return kFew ? static_cast<int64_t>(t.list[first + j]) : static_cast<int64_t>(first) + j;
-    };
+    const bool gated = p.gate_half != 0;
     if (kMode != kInputGrad)
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] += bias;
     if (kMode == kFewDown) {
 #pragma unroll 8
         for (int j = 0; j < 32; ++j)
-            if (c0 + j < r.rows && f_ok && EP_IN(row_of(c0 + j), p.rows))
-                p.part[row_of(c0 + j) * p.F + f] = v[j];
+            if (l.f < p.F && m.has(j)) p.part[m.row_of(j) * p.F + l.f] = v[j];
         return;
     }
     if (kMode == kProduct && p.z) {
+        // tokens 2 i and 2 i + 1, whatever the activation
+        Columns<kMode> mz = m;
+        mz.column0 = lane & 1;
+        uint32_t w[16];
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-            const float2 w = trade_pair(v[j], v[j + 1], lane);
-            const int c = c0 + j + (lane & 1);
-            if (c < r.rows && f_ok && EP_IN(row_of(c), p.rows))
-                *reinterpret_cast<uint32_t*>(p.z + row_of(c) * Fw + (wrow & ~1)) = pack2(w.x, w.y);
-        }
+        for (int i = 0; i < 16; ++i) w[i] = trade_halves(pack2(v[2 * i], v[2 * i + 1]), lane);
+        mz.template words<2>(p.z, gated ? 2 * p.F : p.F, l.wrow & ~1, l.f < p.F,
+                             [&](int i, uint32_t* at) { *at = w[i]; });
     }
-    // What each of the lane's 16 pairs of features adds and is
-    // scaled by, all asked for before the first store: the
-    // residual may be y itself, so a load would have to wait for
-    // the stores before it.
-    const auto column = [&](int i) {   // of pair i
-        return gated ? c0 + 4 * i + (up ? 1 : 0) + 2 * (lane & 1) : c0 + 2 * i + (lane & 1);
-    };
-    const int pairs = gated ? 8 : 16;
-    uint32_t add[16];
-    float scale[16];
-    if (kMode == kProduct && p.residual) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (i < pairs)
-                add[i] = column(i) < r.rows && f_ok && EP_IN(row_of(column(i)), p.rows)
-                             ? *reinterpret_cast<const uint32_t*>(p.residual + row_of(column(i)) * p.F + (f & ~1))
-                             : 0u;
-    }
-    if (kMode == kProduct && p.row_weight) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (i < pairs)
-                scale[i] = column(i) < r.rows && EP_IN(row_of(column(i)), p.rows)
-                               ? p.row_weight[row_of(column(i))]
-                               : 0.0f;
-    }
-    const auto store = [&](int i, float2 a) {
-        if (kMode == kProduct && p.row_weight) {
-            a.x *= scale[i];
-            a.y *= scale[i];
-        }
-        if (kMode == kProduct && p.residual) {
-            const float2 b = unpack2(add[i]);
-            a.x += b.x;
-            a.y += b.y;
-        }
-        const int c = column(i);
-        if (c < r.rows && f_ok && EP_IN(row_of(c), p.rows))
-            *reinterpret_cast<uint32_t*>(p.y + row_of(c) * p.F + (f & ~1)) = pack2(a.x, a.y);
-    };
     if (kMode != kInputGrad && gated) {
+        const bool up = l.up;
+        float o[16];
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
-            // gate lanes take token j (then j + 2), up lanes token j + 1 (j + 3)
+            // gate lanes take tokens j and j + 2, up lanes tokens j + 1 and j + 3
             const float g0 = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + 1], 8);
             const float g1 = __shfl_xor_sync(0xffffffffu, up ? v[j + 2] : v[j + 3], 8);
-            const float a0 = up ? silu(g0) * v[j + 1] : silu(v[j]) * g0;
-            const float a1 = up ? silu(g1) * v[j + 3] : silu(v[j + 2]) * g1;
-            store(j / 4, trade_pair(a0, a1, lane));
+            o[j / 2] = up ? silu(g0) * v[j + 1] : silu(v[j]) * g0;
+            o[j / 2 + 1] = up ? silu(g1) * v[j + 3] : silu(v[j + 2]) * g1;
         }
+        store_rows<kMode, 4>(p, m, l, lane, ahead, o, [&](int i) { return 2 * i + (up ? 1 : 0); });
     } else {
-        if (kMode != kInputGrad && p.act != EP_ACT_NONE) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = activate(v[j], p.act);
-        }
-#pragma unroll
-        for (int j = 0; j < 32; j += 2) store(j / 2, trade_pair(v[j], v[j + 1], lane));
+        if (kMode != kInputGrad) activate_all(v, p.act);
+        store_rows<kMode, 2>(p, m, l, lane, ahead, v, [](int i) { return i; });
     }
 }
 
