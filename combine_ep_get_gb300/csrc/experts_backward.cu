@@ -176,16 +176,16 @@ __global__ void __launch_bounds__(kThreads) activation_backward_kernel(const __g
     }
 }
 
-// The partial sums, in order: blocks of 32 columns of every expert's dbias,
-// then row_blocks blocks for every expert's rows of d_row_weight.
-constexpr int kSumColumns = 32;
+// The partial sums, in order: blocks of `columns` columns of every expert's
+// dbias, kThreads / columns threads taking turns at a column's row tiles, then
+// row_blocks blocks for every expert's rows of d_row_weight.
 __global__ void __launch_bounds__(kThreads) backward_sums_kernel(const __grid_constant__ ExpertBackwardParams p,
-                                                                 int bias_blocks, int row_blocks) {
+                                                                 int columns, int bias_blocks, int row_blocks) {
     __shared__ int warp_sum[kThreads / 32];
-    __shared__ float sums[kThreads / kSumColumns][kSumColumns];
+    __shared__ float sums[kThreads];
     pdl_wait();
     pdl_launch_dependents();
-    const int column_blocks = (p.Nw + kSumColumns - 1) / kSumColumns;
+    const int column_blocks = (p.Nw + columns - 1) / columns;
     int64_t first;
     if (static_cast<int>(blockIdx.x) >= bias_blocks) {
         const int block = blockIdx.x - bias_blocks, e = block / row_blocks;
@@ -198,8 +198,8 @@ __global__ void __launch_bounds__(kThreads) backward_sums_kernel(const __grid_co
         }
         return;
     }
-    const int e = blockIdx.x / column_blocks, c = threadIdx.x % kSumColumns, part = threadIdx.x / kSumColumns;
-    const int n = blockIdx.x % column_blocks * kSumColumns + c;
+    const int e = blockIdx.x / column_blocks, c = threadIdx.x % columns, part = threadIdx.x / columns;
+    const int n = blockIdx.x % column_blocks * columns + c, parts = kThreads / columns;
     // row tiles of the experts before this one
     int before = 0;
     for (int i = threadIdx.x; i < e; i += kThreads)
@@ -215,15 +215,14 @@ __global__ void __launch_bounds__(kThreads) backward_sums_kernel(const __grid_co
     float v = 0.0f;
     if (n < p.Nw)
 #pragma unroll 8
-        for (int i = part; i < tiles; i += kThreads / kSumColumns)
-            v += p.bias_part[static_cast<int64_t>(before + i) * p.Nw + n];
-    sums[part][c] = v;
-    __syncthreads();
-    if (part == 0 && n < p.Nw) {
-        v = 0.0f;
-        for (int i = 0; i < kThreads / kSumColumns; ++i) v += sums[i][c];
-        p.dbias[static_cast<int64_t>(e) * p.Nw + n] = v;
+        for (int i = part; i < tiles; i += parts) v += p.bias_part[static_cast<int64_t>(before + i) * p.Nw + n];
+    if (parts > 1) {
+        sums[threadIdx.x] = v;
+        __syncthreads();
+        if (part > 0) return;
+        for (int i = 1; i < parts; ++i) v += sums[i * columns + c];
     }
+    if (n < p.Nw) p.dbias[static_cast<int64_t>(e) * p.Nw + n] = v;
 }
 
 }  // namespace
@@ -247,13 +246,15 @@ cudaError_t launch_expert_backward(const ExpertBackwardParams& given, cudaStream
         if (e != cudaSuccess) return e;
     }
     if (p.dbias || p.d_row_weight) {
-        const int64_t bias_blocks =
-            p.dbias ? static_cast<int64_t>(p.E) * ((p.Nw + kSumColumns - 1) / kSumColumns) : 0;
+        // few row tiles an expert: a thread a column; many: eight threads
+        const int64_t tiles = p.rows / kBackwardTileRows / p.E;
+        const int columns = tiles < 8 ? 256 : tiles < 32 ? 64 : 32;
+        const int64_t bias_blocks = p.dbias ? static_cast<int64_t>(p.E) * ((p.Nw + columns - 1) / columns) : 0;
         const int row_blocks = p.E < 64 ? 16 : p.E < 1024 ? 1024 / p.E : 1;
         const int64_t blocks = bias_blocks + (p.d_row_weight ? static_cast<int64_t>(row_blocks) * p.E : 0);
         if (blocks > INT32_MAX) return cudaErrorInvalidValue;
         const cudaError_t e = launch_experts(backward_sums_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0,
-                                         stream, 1, p, static_cast<int>(bias_blocks), row_blocks);
+                                         stream, 1, p, columns, static_cast<int>(bias_blocks), row_blocks);
         if (e != cudaSuccess) return e;
     }
     // Both products need only dz.  A kernel between them and dz's has waited

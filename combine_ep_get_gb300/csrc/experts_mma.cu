@@ -611,7 +611,14 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
                 tcgen05_after_sync();
             }
             const uint32_t acc = tmem + accs.stage * kGradK + (static_cast<uint32_t>(q * 32) << 16);
-            for (int c0 = turn * 64; c0 < kGradK; c0 += 128) {
+            const int width = rows_here ? min(kGradK, p.K - k0) : 0;
+            const auto release = [&] {   // the accumulator has been read
+                tcgen05_before_sync();
+                __syncwarp();
+                if (lane == 0) arrive_issuer(&s->acc_empty[accs.stage]);
+            };
+            if (cnt > 0 && turn * 64 >= width) release();
+            for (int c0 = turn * 64; c0 < width; c0 += 128) {
                 // 32 rows x 64 columns through shared memory: a warp storing
                 // 16 bytes of 32 rows at a time kept its loads waiting
                 uint8_t* const box = boxes + (warp - 4) * 4096;
@@ -632,20 +639,15 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
                             make_uint4(pack2(v[c], v[c + 1]), pack2(v[c + 2], v[c + 3]), pack2(v[c + 4], v[c + 5]),
                                        pack2(v[c + 6], v[c + 7]));
                 }
-                if (cnt > 0 && c0 + 128 >= kGradK) {
-                    tcgen05_before_sync();
-                    __syncwarp();
-                    if (lane == 0) arrive_issuer(&s->acc_empty[accs.stage]);
-                }
+                if (cnt > 0 && c0 + 128 >= width) release();
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    if (rows_here && k0 + c0 < p.K) tma_store_3d(&p.out, box, k0 + c0, row0, e);
+                    tma_store_3d(&p.out, box, k0 + c0, row0, e);
                     bulk_commit();
                 }
             }
-            if (cnt == 0) continue;
-            accs.next();
+            if (cnt > 0) accs.next();
         }
         if (lane == 0) bulk_wait_all<0>();
         __syncwarp();
