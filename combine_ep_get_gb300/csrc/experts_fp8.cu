@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
                         else
                             tma_load_3d<1>(sb, &p.a, bar, kb * kBlock, r.f0 + i * 128, r.e);
                     }
-                    for (int i = 0; i < boxes; ++i)
+                    for (int i = 0; i < boxes && !(kTestDropFirstLoad && blockIdx.x == 0 && issued == 0); ++i)
                         tma_load_2d<1>(sa + i * 64 * kBlock, &p.b, bar, kb * kBlock, first + i * 64);
                 }
                 __syncwarp();

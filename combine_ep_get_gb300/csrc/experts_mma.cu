@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
                 __syncwarp();
             };
             const auto load_rows = [&](int stage, int kb) {
+                if (kTestDropFirstLoad && worker == 0 && issued == 0) return;
                 uint8_t* const sb = stages + stage * S::kStageBytes + kABytes;
                 uint32_t bar = smem_addr(&s->full[stage]);
                 if (kCtas == 2) bar = map_to_rank(bar, 0);
@@ -505,12 +506,13 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
                     uint8_t* const sa = stages + ring.stage * S::kStageBytes;
                     uint8_t* const sb = sa + kABytes;
                     const int nx = n0 + rank * kM, kx = k0 + rank * S::kColumnsOfX;
+                    const bool drop = kTestDropFirstLoad && worker == 0 && issued == 0;
                     if (tail) {   // each CTA's own barrier: its warps clear rows first
                         const uint32_t bar = smem_addr(&s->tail_full[ring.stage]);
                         mbar_arrive_expect_tx(&s->tail_full[ring.stage], (mine_a + mine_b) * 8192);
                         for (int i = 0; i < mine_a; ++i)
                             tma_load_2d<1>(sa + i * 8192, &p.dz, bar, nx + 64 * i, first + r);
-                        for (int i = 0; i < mine_b; ++i)
+                        for (int i = 0; i < mine_b && !drop; ++i)
                             tma_load_2d<1>(sb + i * 8192, &p.x, bar, kx + 64 * i, first + r);
                     } else {
                         uint32_t bar = smem_addr(&s->full[ring.stage]);
@@ -518,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
                         if (rank == 0) mbar_arrive_expect_tx(&s->full[ring.stage], all * 8192);
                         for (int i = 0; i < mine_a; ++i)
                             tma_load_2d<kCtas>(sa + i * 8192, &p.dz, bar, nx + 64 * i, first + r);
-                        for (int i = 0; i < mine_b; ++i)
+                        for (int i = 0; i < mine_b && !drop; ++i)
                             tma_load_2d<kCtas>(sb + i * 8192, &p.x, bar, kx + 64 * i, first + r);
                     }
                 }

@@ -17,6 +17,15 @@ constexpr int kDepth = 64;       // terms of the sum in a stage (128 bytes of bf
 constexpr int kABytes = kM * kDepth * 2;
 constexpr int kGroupTiles = 16;  // row tiles whose features are walked together, for the L2
 
+// Test-only builds (EP_TEST_DROP_FIRST_LOAD): the first CTA, or pair, announces
+// its first rows on a barrier and never loads them, so that the wait for them
+// runs out.
+#ifdef EP_TEST_DROP_FIRST_LOAD
+constexpr bool kTestDropFirstLoad = true;
+#else
+constexpr bool kTestDropFirstLoad = false;
+#endif
+
 enum Mode { kProduct, kInputGrad, kFewUp, kFewDown };
 
 struct MmaArgs {
