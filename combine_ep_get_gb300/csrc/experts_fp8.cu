@@ -186,8 +186,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
             const uint32_t idesc =
                 instr_desc(true, false, false, kM, p.F - r.f0 > kTileFeatures / 2 ? kFeatures : kFeatures / 2);
             for (int kb = 0; kb < k_blocks; ++kb, ring.next(), accs.next()) {
-                ok = warp_wait(&s->acc_empty[accs.stage], accs.parity ^ 1) &&
-                     warp_wait(&s->full[ring.stage], ring.parity);
+                ok = warp_wait(&s->full[ring.stage], ring.parity) &&
+                     warp_wait(&s->acc_empty[accs.stage], accs.parity ^ 1);
                 if (!ok) break;
                 tcgen05_after_sync();
                 if (elect_one()) {
@@ -196,8 +196,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
                     for (int k = 0; k < kBlock / 32; ++k)
                         mma<1, true>(tmem + accs.stage * kFeatures, desc_at(da, k * 32), desc_at(db, k * 32), idesc,
                                      k > 0);
-                    mma_commit<1>(&s->empty[ring.stage]);
                     mma_commit<1>(&s->acc_full[accs.stage]);
+                    mma_commit<1>(&s->empty[ring.stage]);
                 }
                 __syncwarp();
             }
