@@ -12,8 +12,17 @@
 // the N side: a lane is a row, so a block's scale is one register a lane (with
 // lanes as features, as in the bf16 product, every warp read the scales of its
 // 32 rows from shared memory, whose bandwidth, already taken by the copies in
-// and the operands out, bounded the kernel).  SWIGLU: 8 gate and 8 up features
+// and the operands out, bounded the kernel: 1.15 PFLOP/s).  SWIGLU: 8 gate and 8 up features
 // in turns (one box of a five-dimensional map).
+//
+// What bounds it: with 512 rows an expert the summing warps (a block of 128
+// terms takes them ~700 of the ~1000 cycles, the MMAs 512): 64 experts x 512
+// rows, [4096, 7168] weights, 0.93 ms = 2.1 PFLOP/s (1.05 ms after seconds of it,
+// under the power limit).  Tried and slower: pairs of CTAs on 256 rows (278
+// against 240 us on 16 experts x 512 rows; shared memory is freed, the summing
+// warps have as much to do and the pair waits for both), eight summing warps
+// with 64 columns each (615 us).  With 32 rows an expert the weights bound it:
+// 1.95 GB in 0.291-0.297 ms = 6.6 TB/s.
 #include "experts_mma.cuh"
 
 namespace epg {

@@ -3,22 +3,38 @@
 // products of the few-token layer.
 //
 // D[feature, row] = sum over k of W[feature, k] * rows[row, k].  The weights'
-// features are the M side (128 a tile, always full) and an expert's rows the
-// N side, whose width an MMA may choose in steps of 16: a tile takes the rows
+// features are the M side (128 a CTA, always full) and an expert's rows the N
+// side, whose width an MMA may choose in steps of 16: a tile takes the rows
 // an expert has instead of padding them to 128, and the weights, which are
 // what a call with few rows per expert has to read, stream through the wide
 // side.  Accumulators: fp32 in tensor memory, two of them, so that the
 // epilogue of one tile runs under the MMAs of the next.
 //
 // One CTA per SM, or a pair of CTAs on a tile twice as wide in features, walks
-// the tiles (expert, rows, features): warp 0 issues the
-// tensor-map loads of 128-byte-swizzled operand tiles, 64 terms of the sum a
-// stage; warp 1 issues the MMAs; warps 4-11 read the accumulators, lane =
-// feature, and apply the epilogue.
+// the tiles (expert, rows, features): warp 0 issues the tensor-map loads of
+// 128-byte-swizzled operand tiles, 64 terms of the sum a stage; warp 1 issues
+// the MMAs; warps 4-11 read the accumulators, lane = feature, and apply the
+// epilogue.  SWIGLU: the 128 features of a CTA are, in turns, 8 gate rows and
+// the 8 up rows that belong to them (one box of a five-dimensional map), so
+// one exchange between lanes 8 apart brings each pair together.
 //
-// SWIGLU: the 128 features of a tile are, in turns, 8 gate rows and the 8 up
-// rows that belong to them (one box of a five-dimensional map), so one
-// exchange between lanes 8 apart brings each pair together.
+// What bounds it.  Below about 290 rows an expert the weights' bytes do: 256
+// experts x 128 rows, [4096, 7168] weights each, 15.6 GB in 2.27-2.32 ms = 6.7-6.9
+// TB/s.  Above, the tensor cores: 4096 x 7168 x 7168 with bias, GELU and
+// residual 229 us, tensor pipe 86% busy (input gradient, nothing in its
+// epilogue: 94%); seconds of it run at the power limit, 1.60 PFLOP/s where a
+// library product of the same sizes without epilogue reaches 1.73.  With one
+// CTA a tile shared memory bounds it (a stage of 64 terms: 48 KB in, 48 KB
+// out, 768 cycles at 128 B each; measured ~800): pairs halve each CTA's share
+// of the rows (1.58 -> 1.87 PFLOP/s, 4096 x 7168 x 7168 alone).
+//
+// Few tokens: the same walk over the experts that some token names, with the
+// tokens' rows gathered by index.  Each CTA sorts topk_idx itself.  The up
+// product leaves h, rounded to bf16 for the down product's tensor cores, the
+// down product fp32 rows for each (token, slot); whichever tile completes a
+// token's last expert sums the token's rows, k ascending, so the order of the
+// sum does not depend on timing.  Bound by the weights: one token, 8 experts
+// of 88 MB, 705 MB in 115 us = 6.1 TB/s; 128 tokens, 22 GB in 3.14 ms = 7.0 TB/s.
 #include "experts_mma.cuh"
 
 namespace epg {
@@ -402,7 +418,9 @@ cudaError_t launch_rows(const MmaArgs& a, cudaStream_t stream) {
 // Both operands are read as they lie, rows of the sum outermost (MN-major
 // descriptors), 128 n x 256 k a tile.  The last stage of an expert may hold
 // rows of the next one, or padding with anything in it: two warps clear those
-// rows of both operands in shared memory before the MMAs read them.
+// rows of both operands in shared memory before the MMAs read them.  32
+// experts x 1024 rows, dw [4096, 7168] each: 1.22 ms, 1.58 PFLOP/s (8 experts x
+// 2048 rows: tensor pipe 90% busy); one CTA a tile 1.50 ms.
 // ---------------------------------------------------------------------------
 
 constexpr int kGradK = 256;      // columns of a tile
