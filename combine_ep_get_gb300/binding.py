@@ -130,10 +130,18 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it, which costs a
+# call more than all of its checks; torch.cuda.current_stream() where a torch
+# has no such shortcut.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _check(code, what):
@@ -352,43 +360,53 @@ def ep_combine_hierarchical(y, topk_idx, topk_weights, num_experts, num_ranks, r
     return _check(code, "ep_combine_hierarchical")
 
 
-def _dense(**tensors):
-    """Every given tensor is contiguous (the library takes no strides)."""
-    for name, t in tensors.items():
-        assert t is None or t.is_contiguous(), "%s must be contiguous" % name
+def _take(t, dtype, shape, name):
+    """Address of a contiguous tensor of this type and shape (the library
+    takes no strides); None stays None."""
+    if t is None:
+        return None
+    assert t.dtype is dtype and t.shape == shape and t.is_contiguous(), \
+        "%s: a contiguous %s tensor of shape %s is wanted" % (name, dtype, tuple(shape))
+    return t.data_ptr()
+
+
+def _blocks(expert_offset, num_tokens_per_expert, E):
+    """Addresses of the experts' blocks (offsets may go on past the last expert's)."""
+    assert expert_offset.dtype is torch.int32 and expert_offset.numel() >= E and expert_offset.is_contiguous()
+    return expert_offset.data_ptr(), _take(num_tokens_per_expert, torch.int32, (E,), "num_tokens_per_expert")
 
 
 def ep_expert_gemm(x, w, expert_offset, num_tokens_per_expert, y, d_status, bias=None, activation=EP_ACT_NONE,
                    row_weight=None, residual=None, z=None, x_sf=None, w_sf=None, sf_col_major=False, stream=None):
     """Experts' matrix product over the expanded receive rows, with bias,
     activation, row weight and residual in its epilogue (see the C header).
-    x and w are bf16, or both float8_e4m3fn (or uint8 codes) with x_sf and w_sf; a layout's expert_offset and
-    num_tokens_per_expert say which rows are whose.  y (and z, the
-    pre-activation for the backward call) are written at the experts' rows."""
+    x [rows, k] and w [E, n_w, k] are bf16, or both float8_e4m3fn (or uint8
+    codes) with x_sf and w_sf; a layout's expert_offset and
+    num_tokens_per_expert say which rows are whose.  y [rows, n] (and z
+    [rows, n_w], the pre-activation for the backward call) are written at the
+    experts' rows."""
+    bf16, f32 = torch.bfloat16, torch.float32
     rows, k_dim = x.shape
-    E, n_w = w.shape[0], w.shape[1]
-    n_dim = n_w // 2 if activation == EP_ACT_SWIGLU else n_w
+    E, n_w, _ = w.shape
+    gated = activation == EP_ACT_SWIGLU
+    assert not gated or n_w % 2 == 0
+    n_dim = n_w // 2 if gated else n_w
     fp8 = x.element_size() == 1
-    assert x.dtype == w.dtype and (fp8 or x.dtype == torch.bfloat16) and w.shape[2] == k_dim
-    assert activation != EP_ACT_SWIGLU or n_w % 2 == 0
-    assert y.dtype == torch.bfloat16 and tuple(y.shape) == (rows, n_dim)
-    assert z is None or (z.dtype == torch.bfloat16 and tuple(z.shape) == (rows, n_w))
-    assert residual is None or (residual.dtype == torch.bfloat16 and residual.shape == y.shape)
-    assert bias is None or (bias.dtype == torch.float32 and tuple(bias.shape) == (E, n_w))
-    assert row_weight is None or (row_weight.dtype == torch.float32 and row_weight.numel() == rows)
+    kind = x.dtype if fp8 else bf16
+    scales = scale_weights = None
     if fp8:
-        assert x_sf is not None and w_sf is not None and x_sf.dtype == w_sf.dtype == torch.float32
+        assert kind in (torch.float8_e4m3fn, torch.uint8)
         stride = (rows + 3) // 4 * 4 if sf_col_major else rows
-        assert x_sf.numel() >= stride * (k_dim // 128)
-        assert tuple(w_sf.shape) == (E, n_w // 128, k_dim // 128)
-    assert expert_offset.dtype == num_tokens_per_expert.dtype == torch.int32
-    assert expert_offset.numel() >= E and num_tokens_per_expert.numel() == E
-    _dense(x=x, w=w, y=y, z=z, residual=residual, bias=bias, row_weight=row_weight, x_sf=x_sf, w_sf=w_sf,
-           expert_offset=expert_offset, num_tokens_per_expert=num_tokens_per_expert)
-    code = _lib.ep_expert_gemm(_ptr(x), _ptr(x_sf), 1 if sf_col_major else 0, _ptr(w), _ptr(w_sf),
-                               EP_FP8_E4M3 if fp8 else EP_BF16, _ptr(bias), activation, _ptr(row_weight),
-                               _ptr(residual), rows, k_dim, n_dim, E, _ptr(expert_offset),
-                               _ptr(num_tokens_per_expert), _ptr(y), _ptr(z), _ptr(d_status), _stream(stream))
+        assert x_sf.dtype is f32 and x_sf.numel() >= stride * (k_dim // 128) and x_sf.is_contiguous()
+        scales, scale_weights = x_sf.data_ptr(), _take(w_sf, f32, (E, n_w // 128, k_dim // 128), "w_sf")
+    first, count = _blocks(expert_offset, num_tokens_per_expert, E)
+    code = _lib.ep_expert_gemm(_take(x, kind, (rows, k_dim), "x"), scales, 1 if sf_col_major else 0,
+                               _take(w, kind, (E, n_w, k_dim), "w"), scale_weights, EP_FP8_E4M3 if fp8 else EP_BF16,
+                               _take(bias, f32, (E, n_w), "bias"), activation,
+                               _take(row_weight, f32, (rows,), "row_weight"),
+                               _take(residual, bf16, (rows, n_dim), "residual"), rows, k_dim, n_dim, E, first, count,
+                               _take(y, bf16, (rows, n_dim), "y"), _take(z, bf16, (rows, n_w), "z"), _ptr(d_status),
+                               _stream(stream))
     return _check(code, "ep_expert_gemm")
 
 
@@ -398,26 +416,21 @@ def ep_expert_gemm_backward_workspace_bytes(num_rows, n_dim, num_experts, activa
 
 def ep_expert_gemm_backward(dy, x, w, z, expert_offset, num_tokens_per_expert, workspace, d_status, dx=None, dw=None,
                             dbias=None, d_row_weight=None, activation=EP_ACT_NONE, row_weight=None, stream=None):
-    """Gradients of ep_expert_gemm for its rows, weights, bias and row weights
-    (each where its output is given; see the C header).  The residual's
-    gradient is dy itself."""
+    """Gradients of ep_expert_gemm (bf16) for its rows, weights, bias and row
+    weights, each where its output is given (see the C header).  The
+    residual's gradient is dy itself."""
+    bf16, f32 = torch.bfloat16, torch.float32
     rows, n_dim = dy.shape
     E, n_w, k_dim = (w if w is not None else dw).shape
     assert n_w == (2 * n_dim if activation == EP_ACT_SWIGLU else n_dim)
-    for t, shape in ((dy, (rows, n_dim)), (x, (rows, k_dim)), (w, (E, n_w, k_dim)), (z, (rows, n_w)),
-                     (dx, (rows, k_dim)), (dw, (E, n_w, k_dim))):
-        assert t is None or (t.dtype == torch.bfloat16 and tuple(t.shape) == shape)
-    for t, n in ((dbias, E * n_w), (row_weight, rows), (d_row_weight, rows)):
-        assert t is None or (t.dtype == torch.float32 and t.numel() == n)
-    assert expert_offset.dtype == num_tokens_per_expert.dtype == torch.int32
-    assert expert_offset.numel() >= E and num_tokens_per_expert.numel() == E
-    _dense(dy=dy, x=x, w=w, z=z, dx=dx, dw=dw, dbias=dbias, row_weight=row_weight, d_row_weight=d_row_weight,
-           expert_offset=expert_offset, num_tokens_per_expert=num_tokens_per_expert, workspace=workspace)
-    code = _lib.ep_expert_gemm_backward(_ptr(dy), _ptr(x), _ptr(w), _ptr(z), activation, _ptr(row_weight), rows,
-                                        k_dim, n_dim, E, _ptr(expert_offset), _ptr(num_tokens_per_expert), _ptr(dx),
-                                        _ptr(dw), _ptr(dbias), _ptr(d_row_weight), _ptr(workspace),
-                                        workspace.numel() * workspace.element_size(), _ptr(d_status),
-                                        _stream(stream))
+    first, count = _blocks(expert_offset, num_tokens_per_expert, E)
+    assert workspace.is_contiguous()
+    code = _lib.ep_expert_gemm_backward(
+        _take(dy, bf16, (rows, n_dim), "dy"), _take(x, bf16, (rows, k_dim), "x"), _take(w, bf16, (E, n_w, k_dim), "w"),
+        _take(z, bf16, (rows, n_w), "z"), activation, _take(row_weight, f32, (rows,), "row_weight"), rows, k_dim, n_dim,
+        E, first, count, _take(dx, bf16, (rows, k_dim), "dx"), _take(dw, bf16, (E, n_w, k_dim), "dw"),
+        _take(dbias, f32, (E, n_w), "dbias"), _take(d_row_weight, f32, (rows,), "d_row_weight"), _ptr(workspace),
+        workspace.nbytes, _ptr(d_status), _stream(stream))
     return _check(code, "ep_expert_gemm_backward")
 
 
@@ -428,22 +441,19 @@ def ep_moe_few_tokens_workspace_bytes(num_tokens, num_topk, hidden, inner, num_e
 def ep_moe_few_tokens(x, topk_idx, topk_weights, w_up, w_down, workspace, out, d_status, bias_up=None, bias_down=None,
                       residual=None, activation=EP_ACT_SWIGLU, stream=None):
     """A whole mixture-of-experts layer for at most EP_FEW_MAX_TOKENS tokens,
-    in two kernels (see the C header)."""
+    in two kernels (see the C header): x and out [T, H], w_up [E, n_w, H],
+    w_down [E, H, inner], bf16."""
+    bf16, f32 = torch.bfloat16, torch.float32
     T, H = x.shape
     K = topk_idx.shape[1]
-    E, n_w = w_up.shape[0], w_up.shape[1]
+    E, n_w, _ = w_up.shape
     inner = w_down.shape[2]
     assert n_w == (2 * inner if activation == EP_ACT_SWIGLU else inner)
-    assert topk_idx.dtype == torch.int64 and topk_weights.dtype == torch.float32
-    assert tuple(topk_idx.shape) == tuple(topk_weights.shape) == (T, K)
-    for t, shape in ((x, (T, H)), (w_up, (E, n_w, H)), (w_down, (E, H, inner)), (residual, (T, H)), (out, (T, H))):
-        assert t is None or (t.dtype == torch.bfloat16 and tuple(t.shape) == shape)
-    for t, shape in ((bias_up, (E, n_w)), (bias_down, (E, H))):
-        assert t is None or (t.dtype == torch.float32 and tuple(t.shape) == shape)
-    _dense(x=x, topk_idx=topk_idx, topk_weights=topk_weights, w_up=w_up, w_down=w_down, bias_up=bias_up,
-           bias_down=bias_down, residual=residual, out=out, workspace=workspace)
-    code = _lib.ep_moe_few_tokens(_ptr(x), _ptr(topk_idx), _ptr(topk_weights), _ptr(w_up), _ptr(bias_up), activation,
-                                  _ptr(w_down), _ptr(bias_down), _ptr(residual), T, H, inner, K, E, _ptr(workspace),
-                                  workspace.numel() * workspace.element_size(), _ptr(out), _ptr(d_status),
-                                  _stream(stream))
+    assert workspace.is_contiguous()
+    code = _lib.ep_moe_few_tokens(
+        _take(x, bf16, (T, H), "x"), _take(topk_idx, torch.int64, (T, K), "topk_idx"),
+        _take(topk_weights, f32, (T, K), "topk_weights"), _take(w_up, bf16, (E, n_w, H), "w_up"),
+        _take(bias_up, f32, (E, n_w), "bias_up"), activation, _take(w_down, bf16, (E, H, inner), "w_down"),
+        _take(bias_down, f32, (E, H), "bias_down"), _take(residual, bf16, (T, H), "residual"), T, H, inner, K, E,
+        _ptr(workspace), workspace.nbytes, _take(out, bf16, (T, H), "out"), _ptr(d_status), _stream(stream))
     return _check(code, "ep_moe_few_tokens")
