@@ -94,12 +94,16 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
     t.count = t.first + p.E;
     t.list = reinterpret_cast<int16_t*>(t.count + p.E);
     t.expert = t.list + p.T * p.K;
+    t.named = reinterpret_cast<uint8_t*>(t.expert + p.T * p.K + EP_FEW_MAX_TOKENS);
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const int rank = kCtas == 2 ? static_cast<int>(cluster_ctarank()) : 0;
     const int cta_features = p.gate_half ? kM / 2 : kM, tile_features = cta_features * kCtas;
     const int feature_tiles = (p.F + tile_features - 1) / tile_features;
-    const int k_blocks = (p.depth + kDepth - 1) / kDepth;
-    const int worker = blockIdx.x / kCtas, workers = gridDim.x / kCtas;
+    // a cluster's CTAs each take a piece of the sum (few tiles, long sums)
+    const int split = kCtas == 1 ? p.split : 1, piece = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int k_blocks = (p.depth + kDepth - 1) / kDepth, k_each = (k_blocks + split - 1) / split;
+    const int kb_begin = piece * k_each, kb_end = min(k_blocks, kb_begin + k_each);
+    const int worker = blockIdx.x / (kCtas * split), workers = gridDim.x / (kCtas * split);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) {
@@ -132,29 +136,48 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
             if (!ok && e != -1 && kMode == kFewUp && blockIdx.x == 0) atomicOr(p.status, EP_ERR_INVALID_INDEX);
             t.expert[i] = ok ? static_cast<int16_t>(e) : static_cast<int16_t>(-1);
         }
-        for (int e = threadIdx.x; e < p.E; e += kThreads) t.count[e] = 0;
+        // how many of each expert's lie in each warp's share of the entries
+        // (counted where the stages will be), then where each share's begin
+        constexpr int kWarps = kThreads / 32;
+        const int entries = p.T * p.K, share = (entries + kThreads - 1) / kThreads * 32;
+        uint32_t* const at = reinterpret_cast<uint32_t*>(stages);   // [kWarps][E]
+        for (int i = threadIdx.x; i < kWarps * p.E; i += kThreads) at[i] = 0;
         if (kMode == kFewUp && blockIdx.x == 0)
             for (int i = threadIdx.x; i < p.done_words; i += kThreads) p.done[i] = 0;
         __syncthreads();
-        for (int i = threadIdx.x; i < p.T * p.K; i += kThreads)
-            if (t.expert[i] >= 0) atomicAdd(&t.count[t.expert[i]], 1);
+        const int begin = warp * share, end = min(entries, begin + share);
+        for (int i = begin + lane; i < end; i += 32)
+            if (t.expert[i] >= 0) atomicAdd(&at[warp * p.E + t.expert[i]], 1u);
+        for (int tok = threadIdx.x; tok < p.T; tok += kThreads) {
+            int n = 0;
+            for (int k = 0; k < p.K; ++k) n += t.expert[tok * p.K + k] >= 0;
+            t.named[tok] = static_cast<uint8_t>(n);
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < p.E; e += kThreads) {
+            uint32_t sum = 0;
+            for (int w = 0; w < kWarps; ++w) {
+                const uint32_t n = at[w * p.E + e];
+                at[w * p.E + e] = sum;
+                sum += n;
+            }
+            t.count[e] = static_cast<int>(sum);
+        }
         __syncthreads();
         scan_experts<kThreads>(p.E, t.first, s->warp_sum, [&](int e) { return t.count[e]; });
         scan_experts<kThreads>(p.E, t.tile_end, s->warp_sum, [&](int e) { return (t.count[e] + NT - 1) / NT; });
-        // first[e] now ends expert e's entries; filling from the last entry
-        // down turns it into their start
-        if (warp == 0)
-            for (int i0 = (p.T * p.K - 1) / 32 * 32; i0 >= 0; i0 -= 32) {
-                const int i = i0 + lane, e = i < p.T * p.K ? t.expert[i] : -1;
-                const unsigned same = __match_any_sync(0xffffffffu, e);
-                if (e >= 0) {
-                    const int at = t.first[e] - __popc(same >> lane);
-                    t.list[at] = static_cast<int16_t>(i);
-                }
-                __syncwarp();
-                if (e >= 0 && (same >> lane) == 1u) t.first[e] -= __popc(same);
-                __syncwarp();
-            }
+        for (int e = threadIdx.x; e < p.E; e += kThreads) t.first[e] -= t.count[e];   // ends to beginnings
+        __syncthreads();
+        for (int i0 = begin; i0 < end; i0 += 32) {
+            const int i = i0 + lane, e = i < end ? t.expert[i] : -1;
+            const unsigned same = __match_any_sync(0xffffffffu, e), before = same & ((1u << lane) - 1);
+            uint32_t* const mine = at + warp * p.E + e;
+            if (e >= 0) t.list[t.first[e] + *mine + __popc(before)] = static_cast<int16_t>(i);
+            __syncwarp();
+            if (e >= 0 && before == 0) *mine += __popc(same);
+            __syncwarp();
+        }
+        fence_proxy_async_smem();   // before the stages are loaded
     } else {
         for (int e = threadIdx.x; e < p.E; e += kThreads) {
             int64_t first;
@@ -185,6 +208,42 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
                 }
         }
     }
+
+    // Few tokens, down, by the warps that read accumulators: the tokens whose
+    // last expert this tile was get their sum over the experts, k ascending,
+    // whoever came last.  The tile's rows in every `of`-th 32 are this CTA's.
+    const auto sum_tokens = [&](const Tile& r, int first, int of, int which) {
+        const int tid = threadIdx.x - 128;
+        if (tid == 0) s->completed = 0;
+        __threadfence();
+        named_barrier(1, kReadWarps * 32);
+        for (int j = tid; j < r.rows; j += kReadWarps * 32) {
+            if (j / 32 % of != which) continue;
+            const int tok = t.list[first + j] / p.K;
+            const uint32_t before = atomicAdd(&p.done[(r.f0 / kM) * p.T + tok], 1u);
+            if (before + 1 == t.named[tok]) {
+                __threadfence();
+                t.expert[p.T * p.K + atomicAdd(&s->completed, 1)] = static_cast<int16_t>(tok);
+            }
+        }
+        named_barrier(1, kReadWarps * 32);
+        const int m = s->completed, feature = r.f0 + tid % kM;
+        for (int i = tid / kM; i < m; i += kReadWarps * 32 / kM) {
+            const int tok = t.expert[p.T * p.K + i];
+            if (feature >= p.F || !EP_IN(tok, p.T)) continue;
+            float sum = 0.0f;
+            for (int k = 0; k < p.K; ++k) {
+                const int entry = tok * p.K + k;
+                if (t.expert[entry] >= 0)
+                    sum = fmaf(p.topk_weights[entry], __ldcg(p.part + static_cast<int64_t>(entry) * p.F + feature),
+                               sum);
+            }
+            const int64_t at = static_cast<int64_t>(tok) * p.F + feature;
+            if (p.residual) sum += __bfloat162float(p.residual[at]);
+            p.out[at] = __float2bfloat16(sum);
+        }
+        named_barrier(1, kReadWarps * 32);
+    };
 
     if (warp == 0) {
         Ring<S::kStages> ring;
@@ -244,11 +303,11 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
             // the down product's first weights come while the up product ends
             int early = 0;
             if (kMode == kFewDown && issued == 0) {
-                early = min(S::kStages, k_blocks);
-                for (int kb = 0; kb < early; ++kb) load_weights(kb, kb);
+                early = min(S::kStages, kb_end - kb_begin);
+                for (int i = 0; i < early; ++i) load_weights(i, kb_begin + i);
                 pdl_wait();
             }
-            for (int kb = 0; kb < k_blocks; ++kb, ++issued, ring.next()) {
+            for (int kb = kb_begin; kb < kb_end; ++kb, ++issued, ring.next()) {
                 if (issued >= early) {   // (not the first tile: early is 0)
                     ok = warp_wait(&s->empty[ring.stage], ring.parity ^ 1);
                     if (!ok) break;
@@ -275,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
             const uint32_t d = tmem + accs.stage * NT;
             ok = warp_wait(&s->acc_empty[accs.stage], accs.parity ^ 1);
             tcgen05_after_sync();
-            for (int kb = 0; kb < k_blocks && ok; ++kb, ring.next()) {
+            for (int kb = kb_begin; kb < kb_end && ok; ++kb, ring.next()) {
                 ok = warp_wait(&s->full[ring.stage], ring.parity);
                 if (!ok) break;
                 tcgen05_after_sync();
@@ -285,9 +344,9 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
 #pragma unroll
                     for (int k = 0; k < kDepth / 16; ++k)
                         mma<kCtas, false>(d, desc_at(a, k * (kMn ? 2048 : 32)), desc_at(b, k * 32), idesc,
-                                          kb > 0 || k > 0);
+                                          kb > kb_begin || k > 0);
                     mma_commit<kCtas>(&s->empty[ring.stage]);
-                    if (kb == k_blocks - 1) mma_commit<kCtas>(&s->acc_full[accs.stage]);
+                    if (kb == kb_end - 1) mma_commit<kCtas>(&s->acc_full[accs.stage]);
                 }
                 __syncwarp();
             }
@@ -318,6 +377,16 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
             if (kMode == kFewDown ? *reinterpret_cast<volatile int*>(&s->gave_up) != 0 : !ready) break;
             tcgen05_after_sync();
             const int last = (r.width - 1) / 32;   // 32-column step
+            if (split > 1) {   // the only tile: this piece's sums, [column][feature], where the stages were
+                for (int step = turn; step <= last; step += 2) {
+                    float v[32];
+                    tmem_load32(acc + step * 32, v);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        reinterpret_cast<float*>(stages)[(step * 32 + j) * kM + q * 32 + lane] = v[j];
+                }
+                continue;
+            }
             for (int step = turn; step == turn || step <= last; step += 2) {
                 const int c0 = step * 32;
                 float v[32];
@@ -337,47 +406,36 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
                 if (step + 2 <= last) ask_ahead<kMode>(p, t, r, first, q, lane, c0 + 64, &ahead);
                 if (step <= last) finish_columns<kMode>(p, t, r, first, q, lane, bias, c0, v, now);
             }
-            if (kMode == kFewDown) {
-                // the tokens whose last expert this was: their sum over the
-                // experts, k ascending, whoever came last
-                const int tid = threadIdx.x - 128;
-                if (tid == 0) s->completed = 0;
-                __threadfence();
-                named_barrier(1, kReadWarps * 32);
-                for (int j = tid; j < r.rows; j += kReadWarps * 32) {
-                    const int tok = t.list[first + j] / p.K;
-                    int experts = 0;
-                    for (int k = 0; k < p.K; ++k) experts += t.expert[tok * p.K + k] >= 0;
-                    const uint32_t before = atomicAdd(&p.done[(r.f0 / kM) * p.T + tok], 1u);
-                    if (before + 1 == static_cast<uint32_t>(experts)) {
-                        __threadfence();
-                        t.expert[p.T * p.K + atomicAdd(&s->completed, 1)] = static_cast<int16_t>(tok);
-                    }
+            if (kMode == kFewDown) sum_tokens(r, first, 1, 0);
+        }
+    }
+    if (split > 1) {
+        // the pieces' sums are added in their order, every split-th 32 columns
+        // by each CTA
+        cluster_sync();
+        if (warp >= 4 && worker < tiles) {
+            const int q = warp & 3, turn = (warp - 4) / 4;
+            const Tile r = tile_at<NT, kStep>(worker, t, p.E, feature_tiles, tile_features);
+            const int first = t.first[r.e] + r.row0;
+            const float bias = kMode == kInputGrad ? 0.0f : bias_of(p, r, q, lane);
+            for (int step = piece + split * turn; step * 32 < r.width; step += 2 * split) {
+                Ahead ahead;
+                ask_ahead<kMode>(p, t, r, first, q, lane, step * 32, &ahead);
+                float v[32] = {};
+                for (int from = 0; from < split; ++from) {
+                    const uint32_t base = map_to_rank(smem_addr(stages), from) + (step * 32 * kM + q * 32 + lane) * 4;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] += load_cluster(base + j * kM * 4);
                 }
-                named_barrier(1, kReadWarps * 32);
-                const int m = s->completed;
-                const int feature = r.f0 + tid % kM;
-                for (int i = tid / kM; i < m; i += kReadWarps * 32 / kM) {
-                    const int tok = t.expert[p.T * p.K + i];
-                    if (feature >= p.F || !EP_IN(tok, p.T)) continue;
-                    float sum = 0.0f;
-                    for (int k = 0; k < p.K; ++k) {
-                        const int entry = tok * p.K + k;
-                        if (t.expert[entry] >= 0)
-                            sum = fmaf(p.topk_weights[entry], __ldcg(p.part + static_cast<int64_t>(entry) * p.F + feature),
-                                       sum);
-                    }
-                    const int64_t at = static_cast<int64_t>(tok) * p.F + feature;
-                    if (p.residual) sum += __bfloat162float(p.residual[at]);
-                    p.out[at] = __float2bfloat16(sum);
-                }
-                named_barrier(1, kReadWarps * 32);
+                finish_columns<kMode>(p, t, r, first, q, lane, bias, step * 32, v, ahead);
             }
+            if (kMode == kFewDown) sum_tokens(r, first, split, piece);
         }
     }
     if (p.wait_late) pdl_wait();
     __syncthreads();
-    if (kCtas == 2) cluster_sync();   // neither CTA of a pair ends while the other may still reach it
+    // no CTA of a cluster ends while another may still reach it
+    if (kCtas == 2 || split > 1) cluster_sync();
     if (warp == 2) tmem_free<kCtas>(tmem, S::kColumns);
 }
 
@@ -385,19 +443,25 @@ template <int NT, int kCtas>
 size_t smem_bytes(int E, int entries) {
     using S = Shape<NT, kCtas>;
     return 1024 + S::kStages * S::kStageBytes + sizeof(Barriers) + static_cast<size_t>(E) * 12 +
-           (entries > 0 ? static_cast<size_t>(entries) * 4 + EP_FEW_MAX_TOKENS * 2 : 0);
+           (entries > 0 ? static_cast<size_t>(entries) * 4 + EP_FEW_MAX_TOKENS * 3 : 0);
 }
 
-// tiles_bound: at least as many tiles as there can be, for the grid.
+// tiles_bound: at least as many tiles as there can be, for the grid.  With
+// fewer than half as many tiles as SMs a cluster of up to 8 CTAs shares each
+// tile's sum, 8 stages or more each: one CTA reads no more than about a
+// seventieth of what the memory gives (one row, [7168, 7168]: 56 tiles).
 template <int kMode, int NT, int kCtas>
-cudaError_t launch(const MmaArgs& a, int tiles_bound, cudaStream_t stream) {
+cudaError_t launch(MmaArgs a, int tiles_bound, cudaStream_t stream) {
     const size_t smem = smem_bytes<NT, kCtas>(a.E, a.T * a.K);
     const auto kernel = experts_mma_kernel<kMode, NT, kCtas>;
     static std::atomic<bool> ready[kMaxDevices];
     const cudaError_t e = allow_all_smem(reinterpret_cast<const void*>(kernel), ready);
     if (e != cudaSuccess) return e;
-    const int workers = std::max(1, std::min(device_info().num_sms / kCtas, tiles_bound));
-    return launch_experts(kernel, dim3(workers * kCtas), dim3(kThreads), smem, stream, kCtas, a);
+    const int sms = device_info().num_sms, k_blocks = (a.depth + kDepth - 1) / kDepth;
+    a.split = 1;
+    while (kCtas == 1 && a.split < 8 && tiles_bound * a.split * 2 <= sms && k_blocks >= 16 * a.split) a.split *= 2;
+    const int cluster = kCtas * a.split, workers = std::max(1, std::min(sms / cluster, tiles_bound));
+    return launch_experts(kernel, dim3(workers * cluster), dim3(kThreads), smem, stream, cluster, a);
 }
 
 // Pairs of CTAs halve the row operand's copies into shared memory, whose

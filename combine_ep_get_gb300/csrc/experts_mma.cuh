@@ -52,6 +52,7 @@ struct MmaArgs {
     int done_words;
     __nv_bfloat16* out;           // [T][F]
     int32_t* status;
+    int split;                    // CTAs of a cluster that share a tile's sum, each a piece of k (1: none)
     int wait_late;                // the inputs are complete: wait for the kernel before only at the end
 };
 
@@ -82,6 +83,7 @@ struct Table {
     int* count;       // [E]
     int16_t* list;    // few tokens: entries t * K + k, expert by expert
     int16_t* expert;  // few tokens: expert of each entry, -1 for none; behind them, tokens just completed
+    uint8_t* named;   // few tokens: experts of each token
 };
 
 // A tile: expert, its rows [row0, row0 + rows) within the expert, features from f0.

@@ -124,6 +124,13 @@ def test_product_row_counts(counts, act):
     run_product(counts, 136, 200, act, bias=True, res=True, save=True, seed=sum(counts))
 
 
+@pytest.mark.parametrize("counts", [[1], [3, 0, 40], [100], [300, 5]])
+@pytest.mark.parametrize("K,N,act", [(2048, 136, "swiglu"), (1032, 200, "gelu"), (7168, 72, "none")])
+def test_product_long_sums_of_few_tiles(counts, K, N, act):
+    """A tile's sum shared by the CTAs of a cluster (2, 4 or 8 of them)."""
+    run_product(counts, K, N, act, bias=True, rw=True, res=True, save=True, gap=1, seed=K + N)
+
+
 def test_product_many_experts():
     rng = np.random.Generator(np.random.PCG64(5))
     counts = rng.integers(0, 9, size=2048).tolist()
@@ -301,6 +308,11 @@ def test_backward_larger():
     run_backward([700, 0, 1300, 5, 2000, 129], 1024, 704, "swiglu", True, seed=10)
 
 
+@pytest.mark.parametrize("counts", [[1], [3, 0, 40], [300]])
+def test_backward_long_sums_of_few_tiles(counts):
+    run_backward(counts, 72, 2056, "silu", True, seed=sum(counts))
+
+
 @pytest.mark.parametrize("want", [("dx",), ("dw",), ("dbias",), ("d_row_weight",), ("dx", "dbias")])
 def test_backward_parts(want):
     run_backward([33, 0, 70], 80, 96, "gelu", True, want=want, seed=12)
@@ -454,7 +466,7 @@ def test_few_activations(act):
 @pytest.mark.parametrize("T,K,E,H,I", [
     (1, 1, 1, 8, 8), (1, 8, 16, 256, 128), (2, 4, 7, 72, 200), (16, 8, 64, 512, 256), (17, 2, 3, 264, 1000),
     (128, 8, 32, 256, 192), (256, 16, 24, 128, 64), (256, 1, 2, 136, 72), (33, 16, 2048, 64, 64),
-    (64, 4, 256, 1024, 384), (256, 16, 2048, 64, 64),
+    (64, 4, 256, 1024, 384), (256, 16, 2048, 64, 64), (1, 1, 3, 2048, 1032), (3, 2, 2, 4096, 2048), (90, 1, 1, 1024, 1032),
 ])
 def test_few_sizes(T, K, E, H, I):
     run_few(T, K, E, H, I, seed=T + K + E)
