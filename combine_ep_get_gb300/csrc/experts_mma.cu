@@ -136,48 +136,59 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
             if (!ok && e != -1 && kMode == kFewUp && blockIdx.x == 0) atomicOr(p.status, EP_ERR_INVALID_INDEX);
             t.expert[i] = ok ? static_cast<int16_t>(e) : static_cast<int16_t>(-1);
         }
-        // how many of each expert's lie in each warp's share of the entries
-        // (counted where the stages will be), then where each share's begin
-        constexpr int kWarps = kThreads / 32;
-        const int entries = p.T * p.K, share = (entries + kThreads - 1) / kThreads * 32;
-        uint32_t* const at = reinterpret_cast<uint32_t*>(stages);   // [kWarps][E]
-        for (int i = threadIdx.x; i < kWarps * p.E; i += kThreads) at[i] = 0;
+        const int entries = p.T * p.K;
         if (kMode == kFewUp && blockIdx.x == 0)
             for (int i = threadIdx.x; i < p.done_words; i += kThreads) p.done[i] = 0;
+        // Few entries: one warp puts them in place, 32 at a time.  More: every
+        // warp its share of them, after counting how many of each expert's
+        // lie in the shares before it (counted where the stages will be).
+        // 1544 entries: 53 -> 34 us a call; 8 entries by shares: 117 -> 120 us.
+        const bool shared = entries > 256;
+        const int share = (entries + kThreads - 1) / kThreads * 32;
+        const int begin = shared ? min(entries, warp * share) : 0;
+        const int end = shared ? min(entries, begin + share) : warp == 0 ? entries : 0;
+        uint32_t* const at = reinterpret_cast<uint32_t*>(stages);   // [warps][E]
+        if (shared)
+            for (int i = threadIdx.x; i < kThreads / 32 * p.E; i += kThreads) at[i] = 0;
+        for (int e = threadIdx.x; e < p.E; e += kThreads) t.count[e] = 0;
         __syncthreads();
-        const int begin = warp * share, end = min(entries, begin + share);
-        for (int i = begin + lane; i < end; i += 32)
+        for (int i = threadIdx.x; i < entries; i += kThreads)
+            if (t.expert[i] >= 0) atomicAdd(&t.count[t.expert[i]], 1);
+        for (int i = begin + lane; shared && i < end; i += 32)
             if (t.expert[i] >= 0) atomicAdd(&at[warp * p.E + t.expert[i]], 1u);
-        for (int tok = threadIdx.x; tok < p.T; tok += kThreads) {
-            int n = 0;
-            for (int k = 0; k < p.K; ++k) n += t.expert[tok * p.K + k] >= 0;
-            t.named[tok] = static_cast<uint8_t>(n);
-        }
-        __syncthreads();
-        for (int e = threadIdx.x; e < p.E; e += kThreads) {
-            uint32_t sum = 0;
-            for (int w = 0; w < kWarps; ++w) {
-                const uint32_t n = at[w * p.E + e];
-                at[w * p.E + e] = sum;
-                sum += n;
-            }
-            t.count[e] = static_cast<int>(sum);
-        }
         __syncthreads();
         scan_experts<kThreads>(p.E, t.first, s->warp_sum, [&](int e) { return t.count[e]; });
         scan_experts<kThreads>(p.E, t.tile_end, s->warp_sum, [&](int e) { return (t.count[e] + NT - 1) / NT; });
-        for (int e = threadIdx.x; e < p.E; e += kThreads) t.first[e] -= t.count[e];   // ends to beginnings
-        __syncthreads();
-        for (int i0 = begin; i0 < end; i0 += 32) {
+        // first[e] is where expert e's entries end; filled from the last one
+        // down it becomes where they begin
+        if (shared) {
+            for (int e = threadIdx.x; e < p.E; e += kThreads) {
+                uint32_t end_at = t.first[e];
+                for (int w = kThreads / 32 - 1; w >= 0; --w) {
+                    const uint32_t n = at[w * p.E + e];
+                    at[w * p.E + e] = end_at;
+                    end_at -= n;
+                }
+                t.first[e] = static_cast<int>(end_at);
+            }
+            __syncthreads();
+        }
+        uint32_t* const ends = shared ? at + warp * p.E : reinterpret_cast<uint32_t*>(t.first);
+        for (int i0 = begin + (end - begin - 1) / 32 * 32; i0 >= begin && begin < end; i0 -= 32) {
             const int i = i0 + lane, e = i < end ? t.expert[i] : -1;
-            const unsigned same = __match_any_sync(0xffffffffu, e), before = same & ((1u << lane) - 1);
-            uint32_t* const mine = at + warp * p.E + e;
-            if (e >= 0) t.list[t.first[e] + *mine + __popc(before)] = static_cast<int16_t>(i);
+            const unsigned same = __match_any_sync(0xffffffffu, e);
+            if (e >= 0) t.list[ends[e] - __popc(same >> lane)] = static_cast<int16_t>(i);
             __syncwarp();
-            if (e >= 0 && before == 0) *mine += __popc(same);
+            if (e >= 0 && (same >> lane) == 1u) ends[e] -= __popc(same);
             __syncwarp();
         }
-        fence_proxy_async_smem();   // before the stages are loaded
+        if (kMode == kFewDown && (shared || warp != 0))
+            for (int tok = shared ? threadIdx.x : threadIdx.x - 32; tok < p.T; tok += shared ? kThreads : kThreads - 32) {
+                int n = 0;
+                for (int k = 0; k < p.K; ++k) n += t.expert[tok * p.K + k] >= 0;
+                t.named[tok] = static_cast<uint8_t>(n);
+            }
+        if (shared) fence_proxy_async_smem();   // before the stages are loaded
     } else {
         for (int e = threadIdx.x; e < p.E; e += kThreads) {
             int64_t first;
@@ -227,20 +238,41 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
             }
         }
         named_barrier(1, kReadWarps * 32);
-        const int m = s->completed, feature = r.f0 + tid % kM;
-        for (int i = tid / kM; i < m; i += kReadWarps * 32 / kM) {
+        // a warp a token, four features a lane, all its experts' rows at once
+        const int m = s->completed, feature = r.f0 + lane * 4;
+        for (int i = tid / 32; i < m; i += kReadWarps) {
             const int tok = t.expert[p.T * p.K + i];
             if (feature >= p.F || !EP_IN(tok, p.T)) continue;
-            float sum = 0.0f;
-            for (int k = 0; k < p.K; ++k) {
-                const int entry = tok * p.K + k;
-                if (t.expert[entry] >= 0)
-                    sum = fmaf(p.topk_weights[entry], __ldcg(p.part + static_cast<int64_t>(entry) * p.F + feature),
-                               sum);
-            }
             const int64_t at = static_cast<int64_t>(tok) * p.F + feature;
-            if (p.residual) sum += __bfloat162float(p.residual[at]);
-            p.out[at] = __float2bfloat16(sum);
+            uint2 res = make_uint2(0u, 0u);
+            if (p.residual) res = *reinterpret_cast<const uint2*>(p.residual + at);
+            float4 part[EP_FEW_MAX_TOPK];
+            float weight[EP_FEW_MAX_TOPK];
+#pragma unroll
+            for (int k = 0; k < EP_FEW_MAX_TOPK; ++k) {
+                const int entry = tok * p.K + k;
+                const bool there = k < p.K && t.expert[entry] >= 0;
+                part[k] = there ? __ldcg(reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(entry) * p.F +
+                                                                          feature))
+                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                weight[k] = there ? p.topk_weights[entry] : 0.0f;
+            }
+            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < EP_FEW_MAX_TOPK; ++k) {
+                sum.x = fmaf(weight[k], part[k].x, sum.x);
+                sum.y = fmaf(weight[k], part[k].y, sum.y);
+                sum.z = fmaf(weight[k], part[k].z, sum.z);
+                sum.w = fmaf(weight[k], part[k].w, sum.w);
+            }
+            if (p.residual) {
+                const float2 lo = unpack2(res.x), hi = unpack2(res.y);
+                sum.x += lo.x;
+                sum.y += lo.y;
+                sum.z += hi.x;
+                sum.w += hi.y;
+            }
+            *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack2(sum.x, sum.y), pack2(sum.z, sum.w));
         }
         named_barrier(1, kReadWarps * 32);
     };
@@ -448,8 +480,9 @@ size_t smem_bytes(int E, int entries) {
 
 // tiles_bound: at least as many tiles as there can be, for the grid.  With
 // fewer than half as many tiles as SMs a cluster of up to 8 CTAs shares each
-// tile's sum, 8 stages or more each: one CTA reads no more than about a
-// seventieth of what the memory gives (one row, [7168, 7168]: 56 tiles).
+// tile's sum, 16 stages or more each: one CTA reads no more than about a
+// seventieth of what the memory gives.  (A cluster and the addition cost about
+// 2 us, what 10 stages take: 20 stages on two CTAs 14 -> 18 us.)
 template <int kMode, int NT, int kCtas>
 cudaError_t launch(MmaArgs a, int tiles_bound, cudaStream_t stream) {
     const size_t smem = smem_bytes<NT, kCtas>(a.E, a.T * a.K);
@@ -459,7 +492,7 @@ cudaError_t launch(MmaArgs a, int tiles_bound, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const int sms = device_info().num_sms, k_blocks = (a.depth + kDepth - 1) / kDepth;
     a.split = 1;
-    while (kCtas == 1 && a.split < 8 && tiles_bound * a.split * 2 <= sms && k_blocks >= 16 * a.split) a.split *= 2;
+    while (kCtas == 1 && a.split < 8 && tiles_bound * a.split * 2 <= sms && k_blocks >= 32 * a.split) a.split *= 2;
     const int cluster = kCtas * a.split, workers = std::max(1, std::min(sms / cluster, tiles_bound));
     return launch_experts(kernel, dim3(workers * cluster), dim3(kThreads), smem, stream, cluster, a);
 }
