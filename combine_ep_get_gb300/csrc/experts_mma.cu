@@ -80,7 +80,7 @@ bool encode_map(CUtensorMap* map, bool fp8, int rank, const void* base, const ui
 
 namespace {
 
-template <int kMode, int NT, int kCtas>
+template <int kMode, int NT, int kCtas, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_constant__ MmaArgs p) {
     using S = Shape<NT, kCtas>;
     constexpr bool kFew = kMode == kFewUp || kMode == kFewDown;
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
     const int cta_features = p.gate_half ? kM / 2 : kM, tile_features = cta_features * kCtas;
     const int feature_tiles = (p.F + tile_features - 1) / tile_features;
     // a cluster's CTAs each take a piece of the sum (few tiles, long sums)
-    const int split = kCtas == 1 ? p.split : 1, piece = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int split = kSplit ? p.split : 1, piece = kSplit ? static_cast<int>(cluster_ctarank()) : 0;
     const int k_blocks = (p.depth + kDepth - 1) / kDepth, k_each = (k_blocks + split - 1) / split;
     const int kb_begin = piece * k_each, kb_end = min(k_blocks, kb_begin + k_each);
     const int worker = blockIdx.x / (kCtas * split), workers = gridDim.x / (kCtas * split);
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
             if (kMode == kFewDown ? *reinterpret_cast<volatile int*>(&s->gave_up) != 0 : !ready) break;
             tcgen05_after_sync();
             const int last = (r.width - 1) / 32;   // 32-column step
-            if (split > 1) {   // the only tile: this piece's sums, [column][feature], where the stages were
+            if (kSplit) {   // the only tile: this piece's sums, [column][feature], where the stages were
                 for (int step = turn; step <= last; step += 2) {
                     float v[32];
                     tmem_load32(acc + step * 32, v);
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
             if (kMode == kFewDown) sum_tokens(r, first, 1, 0);
         }
     }
-    if (split > 1) {
+    if (kSplit) {
         // the pieces' sums are added in their order, every split-th 32 columns
         // by each CTA
         cluster_sync();
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
     if (p.wait_late) pdl_wait();
     __syncthreads();
     // no CTA of a cluster ends while another may still reach it
-    if (kCtas == 2 || split > 1) cluster_sync();
+    if (kCtas == 2 || kSplit) cluster_sync();
     if (warp == 2) tmem_free<kCtas>(tmem, S::kColumns);
 }
 
@@ -483,17 +483,21 @@ size_t smem_bytes(int E, int entries) {
 // tile's sum, 16 stages or more each: one CTA reads no more than about a
 // seventieth of what the memory gives.  (A cluster and the addition cost about
 // 2 us, what 10 stages take: 20 stages on two CTAs 14 -> 18 us.)
-template <int kMode, int NT, int kCtas>
+template <int kMode, int NT, int kCtas, bool kSplit = false>
 cudaError_t launch(MmaArgs a, int tiles_bound, cudaStream_t stream) {
+    const int sms = device_info().num_sms;
+    if constexpr (kCtas == 1 && !kSplit) {
+        const int k_blocks = (a.depth + kDepth - 1) / kDepth;
+        a.split = 1;
+        while (a.split < 8 && tiles_bound * a.split * 2 <= sms && k_blocks >= 32 * a.split) a.split *= 2;
+        if (a.split > 1) return launch<kMode, NT, 1, true>(a, tiles_bound, stream);
+    }
     const size_t smem = smem_bytes<NT, kCtas>(a.E, a.T * a.K);
-    const auto kernel = experts_mma_kernel<kMode, NT, kCtas>;
+    const auto kernel = experts_mma_kernel<kMode, NT, kCtas, kSplit>;
     static std::atomic<bool> ready[kMaxDevices];
     const cudaError_t e = allow_all_smem(reinterpret_cast<const void*>(kernel), ready);
     if (e != cudaSuccess) return e;
-    const int sms = device_info().num_sms, k_blocks = (a.depth + kDepth - 1) / kDepth;
-    a.split = 1;
-    while (kCtas == 1 && a.split < 8 && tiles_bound * a.split * 2 <= sms && k_blocks >= 32 * a.split) a.split *= 2;
-    const int cluster = kCtas * a.split, workers = std::max(1, std::min(sms / cluster, tiles_bound));
+    const int cluster = kCtas * (kSplit ? a.split : 1), workers = std::max(1, std::min(sms / cluster, tiles_bound));
     return launch_experts(kernel, dim3(workers * cluster), dim3(kThreads), smem, stream, cluster, a);
 }
 

@@ -41,14 +41,15 @@ def run(B, lib, call):
     return int(st.item())
 
 
-@pytest.mark.parametrize("fp8,rows,n", [(False, 60, 128), (False, 2100, 2048), (True, 300, 256)])
-def test_product_wait_runs_out_then_the_stream_works(failing, fp8, rows, n):
-    """One CTA a tile, a pair of CTAs a tile, FP8."""
+@pytest.mark.parametrize("fp8,rows,n,k", [(False, 60, 128, 256), (False, 2100, 2048, 256), (False, 20, 64, 4096),
+                                          (True, 300, 256, 256)])
+def test_product_wait_runs_out_then_the_stream_works(failing, fp8, rows, n, k):
+    """One CTA a tile, a pair of CTAs a tile, a cluster that shares a sum, FP8."""
     from gpu_path import B
     from test_gpu_experts import blocks, gen, normal, to_fp8
     g = gen(rows)
     off, cnt, total = blocks([rows, rows // 2])
-    x, w = normal(g, total, 256), normal(g, 2, n, 256, std=1 / 16)
+    x, w = normal(g, total, k), normal(g, 2, n, k, std=k ** -0.5)
     kw, x64, w64 = {}, x.double(), w.double()
     if fp8:
         x, xs = to_fp8(x, 1)
