@@ -140,16 +140,29 @@ inline FewWorkspace few_workspace(int T, int K, int H, int I) {
 }
 
 // The activation of a pre-activation z (the gated one takes gate and up).
-// silu by the hardware's exponential and division: off by about 2^-21 of the
-// result plus |z| 2^-24 of it, far below the bf16 that it is rounded to; the
-// exact forms' branches cost the FP8 product's epilogue more than its stores.
-__device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+// 2^x and 1/x as the hardware gives them, to 2^-22 of the result and one unit in
+// the last place, subnormals as zero: far below the bf16 that activations are
+// rounded to.  The exact forms' branches and scalings cost the epilogues and
+// the activation's backward pass more than their memory.
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float reciprocal_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2E = 1.4426950408889634f;
+__device__ __forceinline__ float sigmoid(float z) { return reciprocal_approx(1.0f + exp2_approx(-kLog2E * z)); }
+__device__ __forceinline__ float silu(float z) { return z * sigmoid(z); }
 // The normal distribution function: erf by Abramowitz and Stegun, Handbook of
 // Mathematical Functions, 7.1.26 (off by at most 1.5e-7, the size of fp32's
 // own error in 1 + erf), whose exponential the density takes too.
 __device__ __forceinline__ float normal_cdf(float z, float* density) {
-    const float e = __expf(-0.5f * z * z);   // exp(-x^2), x = |z| / sqrt(2)
-    const float t = __fdividef(1.0f, fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.0f));
+    const float e = exp2_approx(-0.5f * kLog2E * z * z);   // exp(-x^2), x = |z| / sqrt(2)
+    const float t = reciprocal_approx(fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.0f));
     const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
                                 0.254829592f);
     const float upper = 0.5f * poly * e;     // 1 - Phi(|z|)

@@ -403,6 +403,33 @@ def test_gradients_against_differences(act):
         assert abs(float((grad.double() * v).sum()) - diff) <= float((bound[i] * v.abs()).sum()) + 1e-5
 
 
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements of y, z, dy and dz: the last expert's rows are right."""
+    from gpu_path import B
+    g = gen(33)
+    rows, tail, K, N = 310_000, 77, 64, 7168
+    off = torch.tensor([0, rows - tail, rows], dtype=torch.int32, device="cuda")
+    cnt = torch.tensor([rows - tail, tail], dtype=torch.int32, device="cuda")
+    assert rows * N > 1 << 31
+    x, w = normal(g, rows, K), normal(g, 2, N, K, std=K ** -0.5)
+    y, z = (torch.empty((rows, N), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    st = status()
+    B.ep_expert_gemm(x, w, off, cnt, y, st, activation=B.EP_ACT_SILU, z=z)
+    last = slice(rows - tail, rows)
+    yy, by, zz, bz = ref.product_rows(x[last].double(), w[1].double(), None, "silu", None, None)
+    ref.check(y[last], yy, by)
+    ref.check(z[last], zz, bz)
+    ws = torch.empty(B.ep_expert_gemm_backward_workspace_bytes(rows, N, 2, B.EP_ACT_SILU), dtype=torch.uint8,
+                     device="cuda")
+    dx, dw, drw = torch.empty_like(x), torch.empty_like(w), torch.empty(rows, device="cuda")
+    B.ep_expert_gemm_backward(y, x, w, z, off, cnt, ws, st, dx=dx, dw=dw, d_row_weight=drw, activation=B.EP_ACT_SILU)
+    assert int(st.item()) == 0
+    R = ref.backward_rows(y[last].double(), x[last].double(), w[1].double(), z[last].double(), "silu", None)
+    ref.check(dx[last], *R["dx"])
+    ref.check(dw[1], *R["dw"])
+    ref.check(drw[last], *R["d_row_weight"])
+
+
 # ---------------------------------------------------------------- few tokens
 
 def run_few(T, K, E, H, I, act="swiglu", bias=False, res=False, mode="distinct", mask=0.0, seed=0, alias=False,
