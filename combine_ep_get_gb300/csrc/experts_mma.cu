@@ -521,7 +521,8 @@ cudaError_t launch_rows(const MmaArgs& a, cudaStream_t stream) {
 // rows of the next one, or padding with anything in it: two warps clear those
 // rows of both operands in shared memory before the MMAs read them.  32
 // experts x 1024 rows, dw [4096, 7168] each: 1.22 ms, 1.58 PFLOP/s (8 experts x
-// 2048 rows: tensor pipe 90% busy); one CTA a tile 1.50 ms.
+// 2048 rows: tensor pipe 90% busy); one CTA a tile 1.50 ms.  Few tiles and many
+// rows: a cluster's CTAs each take a piece of the rows (kSplit, as above).
 // ---------------------------------------------------------------------------
 
 constexpr int kGradK = 256;      // columns of a tile
@@ -534,7 +535,7 @@ struct GradArgs {
     const int32_t* expert_offset;
     const int32_t* counts;
     int32_t* status;
-    int wait_late;               // as in MmaArgs
+    int split, wait_late;        // as in MmaArgs
 };
 
 template <int kCtas>
@@ -546,7 +547,7 @@ struct GradShape {
     static constexpr int kColumns = 2 * kGradK;
 };
 
-template <int kCtas>
+template <int kCtas, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_constant__ GradArgs p) {
     using S = GradShape<kCtas>;
     extern __shared__ uint8_t smem_raw[];
@@ -559,7 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
     const int rank = kCtas == 2 ? static_cast<int>(cluster_ctarank()) : 0;
     const int n_tiles = (p.Nw + kM * kCtas - 1) / (kM * kCtas), k_tiles = (p.K + kGradK - 1) / kGradK;
     const int tiles = p.E * n_tiles * k_tiles;
-    const int worker = blockIdx.x / kCtas, workers = gridDim.x / kCtas;
+    const int split = kSplit ? p.split : 1, piece = kSplit ? static_cast<int>(cluster_ctarank()) : 0;
+    const int worker = blockIdx.x / (kCtas * split), workers = gridDim.x / (kCtas * split);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) {
@@ -593,12 +595,44 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
     const auto expert_of = [&](int g) { return g / (n_tiles * k_tiles); };
     const auto n0_of = [&](int g) { return g % (n_tiles * k_tiles) % n_tiles * (kM * kCtas); };
     const auto k0_of = [&](int g) { return g % (n_tiles * k_tiles) / n_tiles * kGradK; };
+    // The rows of an expert that this CTA (or pair) sums: [lo, hi).
+    const auto lo_of = [&](int cnt) {
+        return kSplit ? min(cnt, ((cnt + kDepth - 1) / kDepth + split - 1) / split * kDepth * piece) : 0;
+    };
+    const auto hi_of = [&](int cnt) {
+        return kSplit ? min(cnt, ((cnt + kDepth - 1) / kDepth + split - 1) / split * kDepth * (piece + 1)) : cnt;
+    };
     // Arrive on a barrier of the CTA that issues the MMAs.
     const auto arrive_issuer = [&](uint64_t* bar) {
         if (kCtas == 1)
             mbar_arrive(bar);
         else
             mbar_arrive_cluster(map_to_rank(smem_addr(bar), 0));
+    };
+
+    // 32 rows x 64 columns of dw through shared memory, by one warp: a warp
+    // storing 16 bytes of 32 rows at a time kept its loads waiting.  take(c, v):
+    // this lane's row, columns c .. c + 31 of the tile (v comes as zeros).
+    const auto store_box = [&](int c0, int row0, int k0, int e, auto take) {
+        uint8_t* const box = boxes + (warp - 4) * 4096;
+        if (lane == 0) bulk_wait_read<0>();   // the store before
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float v[32] = {};
+            take(c0 + 32 * h, v);
+#pragma unroll
+            for (int c = 0; c < 32; c += 8)
+                *reinterpret_cast<uint4*>(box + lane * 128 + ((4 * h + c / 8) ^ (lane & 7)) * 16) =
+                    make_uint4(pack2(v[c], v[c + 1]), pack2(v[c + 2], v[c + 3]), pack2(v[c + 4], v[c + 5]),
+                               pack2(v[c + 6], v[c + 7]));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_3d(&p.out, box, k0 + c0, row0, e);
+            bulk_commit();
+        }
     };
 
     if (warp == 0) {
@@ -614,7 +648,8 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
             };
             const int mine_a = a_boxes(rank), mine_b = b_boxes(rank);
             const int all = a_boxes(0) + b_boxes(0) + (kCtas == 2 ? a_boxes(1) + b_boxes(1) : 0);
-            for (int r = 0; r < cnt; r += kDepth, ++issued, ring.next()) {
+            const int hi = hi_of(cnt);
+            for (int r = lo_of(cnt); r < hi; r += kDepth, ++issued, ring.next()) {
                 ok = warp_wait(&s->empty[ring.stage], ring.parity ^ 1);
                 if (!ok) break;
                 const uint32_t bit = 1u << ring.stage;
@@ -663,12 +698,12 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
         uint32_t tail_bits = 0, full_bits = 0;
         bool ok = true;
         for (int g = worker; g < tiles && ok; g += workers) {
-            const int cnt = s_count[expert_of(g)];
-            if (cnt == 0) continue;
+            const int cnt = s_count[expert_of(g)], lo = lo_of(cnt), hi = hi_of(cnt);
+            if (lo >= hi) continue;
             const uint32_t d = tmem + accs.stage * kGradK;
             ok = warp_wait(&s->acc_empty[accs.stage], accs.parity ^ 1);
             tcgen05_after_sync();
-            for (int r = 0; r < cnt && ok; r += kDepth, ring.next()) {
+            for (int r = lo; r < hi && ok; r += kDepth, ring.next()) {
                 const bool tail = r + kDepth > cnt;
                 ok = warp_wait(tail ? &s->cleared[ring.stage] : &s->full[ring.stage],
                                ((tail ? tail_bits : full_bits) >> ring.stage) & 1);
@@ -680,9 +715,9 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
                     const uint64_t b = desc_at(desc_b, ring.stage * S::kStageBytes);
 #pragma unroll
                     for (int k = 0; k < kDepth / 16; ++k)
-                        mma<kCtas, false>(d, desc_at(a, k * 2048), desc_at(b, k * 2048), idesc, r > 0 || k > 0);
+                        mma<kCtas, false>(d, desc_at(a, k * 2048), desc_at(b, k * 2048), idesc, r > lo || k > 0);
                     mma_commit<kCtas>(&s->empty[ring.stage]);
-                    if (r + kDepth >= cnt) mma_commit<kCtas>(&s->acc_full[accs.stage]);
+                    if (r + kDepth >= hi) mma_commit<kCtas>(&s->acc_full[accs.stage]);
                 }
                 __syncwarp();
             }
@@ -698,9 +733,9 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
         int it = 0;
         uint32_t tail_bits = 0;
         for (int g = worker; g < tiles; g += workers) {
-            const int cnt = s_count[expert_of(g)], blocks = (cnt + kDepth - 1) / kDepth, valid = cnt % kDepth;
-            it += blocks;
-            if (valid == 0) continue;
+            const int cnt = s_count[expert_of(g)], lo = lo_of(cnt), hi = hi_of(cnt), valid = cnt % kDepth;
+            it += (hi - lo + kDepth - 1) / kDepth;
+            if (valid == 0 || lo >= hi || hi < cnt) continue;
             const int st = (it - 1) % S::kStages;
             if (!warp_wait(&s->tail_full[st], (tail_bits >> st) & 1)) {
                 atomicOr(p.status, EP_ERR_TIMEOUT);
@@ -723,8 +758,8 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
         for (int g = worker; g < tiles; g += workers) {
             const int e = expert_of(g), n0 = n0_of(g) + rank * kM, k0 = k0_of(g), cnt = s_count[e];
             const int row0 = n0 + q * 32;
-            const bool rows_here = row0 < p.Nw;   // the rows past Nw in a box are not stored
-            if (cnt > 0) {
+            const bool sums = lo_of(cnt) < hi_of(cnt);
+            if (sums) {
                 if (!warp_wait(&s->acc_full[accs.stage], accs.parity)) {
                     atomicOr(p.status, EP_ERR_TIMEOUT);
                     break;
@@ -732,63 +767,72 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
                 tcgen05_after_sync();
             }
             const uint32_t acc = tmem + accs.stage * kGradK + (static_cast<uint32_t>(q * 32) << 16);
-            const int width = rows_here ? min(kGradK, p.K - k0) : 0;
+            const int width = row0 < p.Nw ? min(kGradK, p.K - k0) : 0;   // the rows past Nw in a box are not stored
+            if (kSplit) {   // the only tile: this piece's sums, [column][row], where the stages were
+                for (int c0 = turn * 32; c0 < width; c0 += 64) {
+                    float v[32] = {};
+                    if (sums) tmem_load32(acc + c0, v);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        reinterpret_cast<float*>(stages)[(c0 + j) * kM + q * 32 + lane] = v[j];
+                }
+                continue;
+            }
             const auto release = [&] {   // the accumulator has been read
                 tcgen05_before_sync();
                 __syncwarp();
                 if (lane == 0) arrive_issuer(&s->acc_empty[accs.stage]);
             };
-            if (cnt > 0 && turn * 64 >= width) release();
+            if (sums && turn * 64 >= width) release();
             for (int c0 = turn * 64; c0 < width; c0 += 128) {
-                // 32 rows x 64 columns through shared memory: a warp storing
-                // 16 bytes of 32 rows at a time kept its loads waiting
-                uint8_t* const box = boxes + (warp - 4) * 4096;
-                if (lane == 0) bulk_wait_read<0>();   // the store before
-                __syncwarp();
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float v[32];
-                    if (cnt > 0) {
-                        tmem_load32(acc + c0 + 32 * h, v);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-                    }
-#pragma unroll
-                    for (int c = 0; c < 32; c += 8)
-                        *reinterpret_cast<uint4*>(box + lane * 128 + ((4 * h + c / 8) ^ (lane & 7)) * 16) =
-                            make_uint4(pack2(v[c], v[c + 1]), pack2(v[c + 2], v[c + 3]), pack2(v[c + 4], v[c + 5]),
-                                       pack2(v[c + 6], v[c + 7]));
-                }
-                if (cnt > 0 && c0 + 128 >= width) release();
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    tma_store_3d(&p.out, box, k0 + c0, row0, e);
-                    bulk_commit();
-                }
+                store_box(c0, row0, k0, e, [&](int c, float (&v)[32]) {
+                    if (sums) tmem_load32(acc + c, v);
+                    if (sums && c0 + 128 >= width && c > c0) release();
+                });
             }
-            if (cnt > 0) accs.next();
+            if (sums) accs.next();
         }
         if (lane == 0) bulk_wait_all<0>();
         __syncwarp();
     }
+    if (kSplit) {
+        cluster_sync();
+        if (warp >= 4 && worker < tiles) {
+            const int q = warp & 3, turn = (warp - 4) / 4;
+            const int n0 = n0_of(worker), k0 = k0_of(worker), row0 = n0 + q * 32;
+            const int width = row0 < p.Nw ? min(kGradK, p.K - k0) : 0;
+            for (int step = piece + split * turn; step * 64 < width; step += 2 * split)
+                store_box(step * 64, row0, k0, expert_of(worker), [&](int c, float (&v)[32]) {
+                    if (c < width)
+                        for (int from = 0; from < split; ++from) {
+                            const uint32_t base =
+                                map_to_rank(smem_addr(stages), from) + (c * kM + q * 32 + lane) * 4;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] += load_cluster(base + j * kM * 4);
+                        }
+                });
+            if (lane == 0) bulk_wait_all<0>();
+            __syncwarp();
+        }
+    }
     if (p.wait_late) pdl_wait();
     __syncthreads();
-    if (kCtas == 2) cluster_sync();   // neither CTA of a pair ends while the other may still reach it
+    // no CTA of a cluster ends while another may still reach it
+    if (kCtas == 2 || kSplit) cluster_sync();
     if (warp == 2) tmem_free<kCtas>(tmem, S::kColumns);
 }
 
-template <int kCtas>
+template <int kCtas, bool kSplit = false>
 cudaError_t launch_grad(const GradArgs& a, int64_t tiles, cudaStream_t stream) {
     using S = GradShape<kCtas>;
-    const auto kernel = weight_grad_kernel<kCtas>;
+    const auto kernel = weight_grad_kernel<kCtas, kSplit>;
     const size_t smem = 1024 + S::kStages * S::kStageBytes + S::kOutBytes + sizeof(Barriers) + 8 * static_cast<size_t>(a.E);
     static std::atomic<bool> ready[kMaxDevices];
     const cudaError_t e = allow_all_smem(reinterpret_cast<const void*>(kernel), ready);
     if (e != cudaSuccess) return e;
-    const int workers = static_cast<int>(std::min<int64_t>(device_info().num_sms / kCtas, tiles));
-    return launch_experts(kernel, dim3(std::max(1, workers) * kCtas), dim3(kThreads), smem, stream, kCtas, a);
+    const int cluster = kCtas * (kSplit ? a.split : 1);
+    const int workers = static_cast<int>(std::min<int64_t>(device_info().num_sms / cluster, tiles));
+    return launch_experts(kernel, dim3(std::max(1, workers) * cluster), dim3(kThreads), smem, stream, cluster, a);
 }
 
 }  // namespace
@@ -840,7 +884,11 @@ cudaError_t launch_weight_grad(const ExpertBackwardParams& p, const __nv_bfloat1
     if (tiles(kM) > INT32_MAX) return cudaErrorInvalidValue;
     // pairs, as for the rows' products, unless they would leave SMs idle
     if (tiles(2 * kM) * 2 > device_info().num_sms) return launch_grad<2>(a, tiles(2 * kM), stream);
-    return launch_grad<1>(a, tiles(kM), stream);
+    // few tiles: pieces of 8 stages of rows or more
+    const int64_t blocks = p.rows / p.E / kDepth;
+    a.split = 1;
+    while (a.split < 8 && tiles(kM) * a.split * 2 <= device_info().num_sms && blocks >= 16 * a.split) a.split *= 2;
+    return a.split > 1 ? launch_grad<1, true>(a, tiles(kM), stream) : launch_grad<1>(a, tiles(kM), stream);
 }
 
 cudaError_t launch_few_tokens(const FewTokensParams& p, cudaStream_t stream) {

@@ -313,6 +313,13 @@ def test_backward_long_sums_of_few_tiles(counts):
     run_backward(counts, 72, 2056, "silu", True, seed=sum(counts))
 
 
+@pytest.mark.parametrize("counts", [[4200], [3000, 0, 129], [8192], [1030, 2000]])
+@pytest.mark.parametrize("K,N", [(72, 200), (520, 264)])
+def test_backward_many_rows_of_few_tiles(counts, K, N):
+    """A weight gradient's rows shared by the CTAs of a cluster; some of them without any."""
+    run_backward(counts, K, N, "gelu", True, gap=3, seed=sum(counts))
+
+
 @pytest.mark.parametrize("want", [("dx",), ("dw",), ("dbias",), ("d_row_weight",), ("dx", "dbias")])
 def test_backward_parts(want):
     run_backward([33, 0, 70], 80, 96, "gelu", True, want=want, seed=12)

@@ -69,7 +69,7 @@ def test_product_wait_runs_out_then_the_stream_works(failing, fp8, rows, n, k):
         ref.check(y[d], want, bound)
 
 
-@pytest.mark.parametrize("rows,k,n", [(60, 64, 64), (400, 2048, 1024)])
+@pytest.mark.parametrize("rows,k,n", [(60, 64, 64), (400, 2048, 1024), (2200, 64, 64)])
 def test_backward_wait_runs_out_then_the_stream_works(failing, rows, k, n):
     from gpu_path import B
     from test_gpu_experts import blocks, gen, normal
