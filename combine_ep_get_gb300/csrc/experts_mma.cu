@@ -502,16 +502,16 @@ cudaError_t launch(MmaArgs a, int tiles_bound, cudaStream_t stream) {
 }
 
 // Pairs of CTAs halve the row operand's copies into shared memory, whose
-// bandwidth (copies in, operands out) bounds one CTA's 128 x 256 tile; a call
-// that has no more tiles than pairs takes single CTAs, twice as many.
+// bandwidth (copies in, operands out) bounds one CTA's 128 x 256 tile.  A call
+// that has no more tiles than pairs takes single CTAs, twice as many, of half
+// as many rows: more of them, and room for six stages instead of four.
 template <int kMode>
 cudaError_t launch_rows(const MmaArgs& a, cudaStream_t stream) {
-    constexpr int NT = 256;
+    constexpr int kPairRows = 256, kRows = 128;
     const int per = a.gate_half ? kM / 2 : kM;
-    const int64_t row_tiles = a.rows / NT + a.E;
-    const int pairs = bound_tiles(row_tiles, (a.F + 2 * per - 1) / (2 * per));
-    if (pairs * 2 > device_info().num_sms) return launch<kMode, NT, 2>(a, pairs, stream);
-    return launch<kMode, NT, 1>(a, bound_tiles(row_tiles, (a.F + per - 1) / per), stream);
+    const int pairs = bound_tiles(a.rows / kPairRows + a.E, (a.F + 2 * per - 1) / (2 * per));
+    if (pairs * 2 > device_info().num_sms) return launch<kMode, kPairRows, 2>(a, pairs, stream);
+    return launch<kMode, kRows, 1>(a, bound_tiles(a.rows / kRows + a.E, (a.F + per - 1) / per), stream);
 }
 
 // ---------------------------------------------------------------------------
