@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
                         if (kCtas == 1)
                             mbar_arrive(&s->acc_empty[accs.stage]);
                         else
-                            mbar_arrive_cluster(map_to_rank(smem_addr(&s->acc_empty[accs.stage]), 0));
+                            mbar_arrive_cluster_relaxed(map_to_rank(smem_addr(&s->acc_empty[accs.stage]), 0));
                     }
                 }
                 const Ahead now = ahead;
@@ -602,13 +602,6 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
     const auto hi_of = [&](int cnt) {
         return kSplit ? min(cnt, ((cnt + kDepth - 1) / kDepth + split - 1) / split * kDepth * (piece + 1)) : cnt;
     };
-    // Arrive on a barrier of the CTA that issues the MMAs.
-    const auto arrive_issuer = [&](uint64_t* bar) {
-        if (kCtas == 1)
-            mbar_arrive(bar);
-        else
-            mbar_arrive_cluster(map_to_rank(smem_addr(bar), 0));
-    };
 
     // 32 rows x 64 columns of dw through shared memory, by one warp: a warp
     // storing 16 bytes of 32 rows at a time kept its loads waiting.  take(c, v):
@@ -750,7 +743,12 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
                     *reinterpret_cast<uint4*>(base + box * 8192 + i * 16) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) arrive_issuer(&s->cleared[st]);
+            if (lane == 0) {
+                if (kCtas == 1)
+                    mbar_arrive(&s->cleared[st]);
+                else
+                    mbar_arrive_cluster(map_to_rank(smem_addr(&s->cleared[st]), 0));
+            }
         }
     } else if (warp >= 4) {
         const int q = warp & 3, turn = (warp - 4) / 4;
@@ -781,7 +779,12 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
             const auto release = [&] {   // the accumulator has been read
                 tcgen05_before_sync();
                 __syncwarp();
-                if (lane == 0) arrive_issuer(&s->acc_empty[accs.stage]);
+                if (lane == 0) {
+                    if (kCtas == 1)
+                        mbar_arrive(&s->acc_empty[accs.stage]);
+                    else
+                        mbar_arrive_cluster_relaxed(map_to_rank(smem_addr(&s->acc_empty[accs.stage]), 0));
+                }
             };
             if (sums && turn * 64 >= width) release();
             for (int c0 = turn * 64; c0 < width; c0 += 128) {
