@@ -21,8 +21,8 @@
 // What bounds it.  Below about 290 rows an expert the weights' bytes do: 256
 // experts x 128 rows, [4096, 7168] weights each, 15.6 GB in 2.27-2.32 ms = 6.7-6.9
 // TB/s.  Above, the tensor cores: 4096 x 7168 x 7168 with bias, GELU and
-// residual 229 us, tensor pipe 86% busy (input gradient, nothing in its
-// epilogue: 94%); seconds of it run at the power limit, 1.60 PFLOP/s where a
+// residual 225-229 us, tensor pipe 86% busy (input gradient, nothing in its
+// epilogue: 94%); seconds of it run at the power limit, 1.63 PFLOP/s where a
 // library product of the same sizes without epilogue reaches 1.73.  With one
 // CTA a tile shared memory bounds it (a stage of 64 terms: 48 KB in, 48 KB
 // out, 768 cycles at 128 B each; measured ~800): pairs halve each CTA's share
@@ -34,7 +34,8 @@
 // down product fp32 rows for each (token, slot); whichever tile completes a
 // token's last expert sums the token's rows, k ascending, so the order of the
 // sum does not depend on timing.  Bound by the weights: one token, 8 experts
-// of 88 MB, 705 MB in 115 us = 6.1 TB/s; 128 tokens, 22 GB in 3.14 ms = 7.0 TB/s.
+// of 88 MB, 705 MB in 114-118 us = 6.0-6.2 TB/s; 128 tokens, 22 GB in 3.11-3.2 ms =
+// 6.9-7.1 TB/s.
 #include "experts_mma.cuh"
 
 namespace epg {
