@@ -58,19 +58,24 @@ struct Fp8Shared {
     int warp_sum[kFp8Warps];
 };
 
-// The epilogue of 16 columns of a row: 16 features from f, or, gated, 8 from f
-// (8 gate columns, then 8 up ones).
-__device__ __forceinline__ void finish_row(const MmaArgs& p, int e, int64_t d, int f, float (&v)[16]) {
-    const bool gated = p.gate_half != 0;
-    const int Fw = gated ? 2 * p.F : p.F;
+// The epilogue of a row's 64 columns in a warp: 64 features from f, or, gated,
+// 32 from f (8 gate columns, then 8 up ones, four times).  F is a multiple of
+// 128, so all of them exist or none.  The bias is read before the first store
+// and the residual 32 features at a time before theirs: it may be y itself, so
+// a load after a store would wait for it.
+template <bool kGated>
+__device__ __forceinline__ void finish_row(const MmaArgs& p, int e, int64_t d, int f, float (&v)[kSumColumns]) {
+    const int Fw = kGated ? 2 * p.F : p.F;
+    const float w = p.row_weight ? p.row_weight[d] : 1.0f;
+    // columns 8 i .. 8 i + 7 are these rows of W
+    const auto wrow = [&](int i) { return kGated ? (i % 2) * p.gate_half + f + i / 2 * 8 : f + i * 8; };
+    if (p.bias) {
+        const float* const bias = p.bias + static_cast<int64_t>(e) * Fw;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int wrow = gated ? h * p.gate_half + f : f + 8 * h;
-        float* const u = v + 8 * h;
-        if (!gated && f + 8 * h >= p.F) break;
-        if (p.bias) {
-            const float4* const b = reinterpret_cast<const float4*>(p.bias + static_cast<int64_t>(e) * Fw + wrow);
+        for (int i = 0; i < kSumColumns / 8; ++i) {
+            const float4* const b = reinterpret_cast<const float4*>(bias + wrow(i));
             const float4 b0 = b[0], b1 = b[1];
+            float* const u = v + 8 * i;
             u[0] += b0.x;
             u[1] += b0.y;
             u[2] += b0.z;
@@ -80,30 +85,45 @@ __device__ __forceinline__ void finish_row(const MmaArgs& p, int e, int64_t d, i
             u[6] += b1.z;
             u[7] += b1.w;
         }
-        if (p.z)
-            st_v4(p.z + d * Fw + wrow,
-                  make_uint4(pack2(u[0], u[1]), pack2(u[2], u[3]), pack2(u[4], u[5]), pack2(u[6], u[7])));
     }
-    const float w = p.row_weight ? p.row_weight[d] : 1.0f;
+    if (p.z)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (gated ? h > 0 : f + 8 * h >= p.F) break;
-        float* const u = v + 8 * h;
-        __nv_bfloat16* const out = p.y + d * p.F + f + 8 * h;
-        float a[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = (gated ? silu(u[i]) * v[8 + i] : activate(u[i], p.act)) * w;
-        if (p.residual) {
-            const uint4 r = *reinterpret_cast<const uint4*>(p.residual + d * p.F + f + 8 * h);
-            const uint32_t words[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 b = unpack2(words[i]);
-                a[2 * i] += b.x;
-                a[2 * i + 1] += b.y;
-            }
+        for (int i = 0; i < kSumColumns / 8; ++i) {
+            const float* const u = v + 8 * i;
+            st_v4(p.z + d * Fw + wrow(i),
+                  make_uint4(pack2(u[0], u[1]), pack2(u[2], u[3]), pack2(u[4], u[5]), pack2(u[6], u[7])));
         }
-        st_v4(out, make_uint4(pack2(a[0], a[1]), pack2(a[2], a[3]), pack2(a[4], a[5]), pack2(a[6], a[7])));
+    constexpr int kOut = kGated ? kSumColumns / 2 : kSumColumns;
+    if (kGated) {
+#pragma unroll
+        for (int i = 0; i < kOut; ++i) v[i] = silu(v[i / 8 * 16 + i % 8]) * v[i / 8 * 16 + 8 + i % 8];
+    } else {
+        activate_all(v, p.act);
+    }
+    __nv_bfloat16* const out = p.y + d * p.F + f;
+#pragma unroll
+    for (int c0 = 0; c0 < kOut; c0 += 32) {
+        uint4 r[4];
+        if (p.residual)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] = *reinterpret_cast<const uint4*>(p.residual + d * p.F + f + c0 + 8 * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float* const a = v + c0 + 8 * i;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a[j] *= w;
+            if (p.residual) {
+                const uint32_t words[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 s = unpack2(words[j]);
+                    a[2 * j] += s.x;
+                    a[2 * j + 1] += s.y;
+                }
+            }
+            st_v4(out + c0 + 8 * i,
+                  make_uint4(pack2(a[0], a[1]), pack2(a[2], a[3]), pack2(a[4], a[5]), pack2(a[6], a[7])));
+        }
     }
 }
 
@@ -291,15 +311,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
             }
             if (!ok) break;
             const int64_t d = static_cast<int64_t>(t.first[r.e]) + r.row0 + row;
-            if (row < r.rows && EP_IN(d, p.rows))
-#pragma unroll
-                for (int c = 0; c < kSumColumns / 16; ++c) {
-                    const int f = r.f0 + (group * kSumColumns + c * 16) / (kGated ? 2 : 1);
-                    float v[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = sum[c * 16 + i];
-                    if (f < p.F) finish_row(p, r.e, d, f, v);
-                }
+            const int f = r.f0 + group * kSumColumns / (kGated ? 2 : 1);
+            if (row < r.rows && f < p.F && EP_IN(d, p.rows)) finish_row<kGated>(p, r.e, d, f, sum);
             __syncwarp();
         }
         if (!ok) atomicOr(p.status, EP_ERR_TIMEOUT);
