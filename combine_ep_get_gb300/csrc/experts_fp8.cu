@@ -97,8 +97,6 @@ __device__ __forceinline__ void finish_row(const MmaArgs& p, int e, int64_t d, i
     if (kGated) {
 #pragma unroll
         for (int i = 0; i < kOut; ++i) v[i] = silu(v[i / 8 * 16 + i % 8]) * v[i / 8 * 16 + 8 + i % 8];
-    } else {
-        activate_all(v, p.act);
     }
     __nv_bfloat16* const out = p.y + d * p.F + f;
 #pragma unroll
@@ -107,6 +105,7 @@ __device__ __forceinline__ void finish_row(const MmaArgs& p, int e, int64_t d, i
         if (p.residual)
 #pragma unroll
             for (int i = 0; i < 4; ++i) r[i] = *reinterpret_cast<const uint4*>(p.residual + d * p.F + f + c0 + 8 * i);
+        if (!kGated) activate_all(*reinterpret_cast<float(*)[32]>(v + c0), p.act);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float* const a = v + c0 + 8 * i;
