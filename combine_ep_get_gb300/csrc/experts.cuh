@@ -59,7 +59,7 @@ struct FewTokensParams {
     const float* bias_down;      // [E][H] or null
     const __nv_bfloat16* residual;   // [T][H] or null
     int T, H, I, Nw, K, E, act;
-    __nv_bfloat16* h;            // workspace [T * K][I]
+    __nv_bfloat16* h;            // workspace [T * K][I], expert by expert
     float* part;                 // workspace [T * K][H]
     uint32_t* done;              // workspace [H / 128, rounded up][T]
     __nv_bfloat16* out;          // [T][H]

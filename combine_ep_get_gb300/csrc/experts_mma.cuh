@@ -15,6 +15,8 @@ constexpr int kThreads = 128 + kReadWarps * 32;
 constexpr int kM = 128;          // features of a tile
 constexpr int kDepth = 64;       // terms of the sum in a stage (128 bytes of bf16)
 constexpr int kABytes = kM * kDepth * 2;
+constexpr int kFewBoxRows = 8;   // few tokens, down: rows of a box (143 tokens over 10 experts, 896 and 5208
+                                 // features: boxes of 4 rows 82 us, of 8 rows 74; one token alike)
 constexpr int kGroupTiles = 8;   // row tiles whose features are walked together, for the L2 (dense 8192 x
                                  // 7168 x 7168 under the power limit: 4 538, 8 526, 16 536, 32 569 us)
 
@@ -162,7 +164,7 @@ __device__ __forceinline__ float bias_of(const MmaArgs& p, const Tile& r, int q,
 // (gated: 32 from 8).
 template <int kMode>
 struct Columns {
-    static constexpr bool kFew = kMode == kFewUp || kMode == kFewDown;
+    static constexpr bool kByEntry = kMode == kFewDown;   // rows of [T * K] by (token, slot), not by the list
     const MmaArgs& p;
     const Table& t;
     int first, left, column0;   // first: of the 32; left: columns there are
@@ -173,26 +175,18 @@ struct Columns {
         column0 = p.gate_half ? ((lane & 8) ? 1 : 0) + 2 * (lane & 1) : (lane & 1);
     }
     __device__ __forceinline__ int64_t row_of(int c) const {   // of column c of the 32
-        return kFew ? static_cast<int64_t>(t.list[first + c]) : static_cast<int64_t>(first) + c;
+        return kByEntry ? static_cast<int64_t>(t.list[first + c]) : static_cast<int64_t>(first) + c;
     }
     __device__ __forceinline__ bool has(int c) const { return c < left && EP_IN(row_of(c), p.rows); }
     // A lane's words of rows of `pitch` elements, from feature f; none if !ok.
     template <int kStep, class F>
     __device__ __forceinline__ void words(__nv_bfloat16* base, int pitch, int f, bool ok, F use) const {
-        if (kFew) {
+        __nv_bfloat16* at = base + row_of(column0) * pitch + f;
+        const int64_t next = static_cast<int64_t>(kStep) * pitch;
+        const int here = ok ? left - column0 : 0;
 #pragma unroll
-            for (int i = 0; i < 32 / kStep; ++i)
-                if (ok && has(column0 + i * kStep))
-                    use(i, reinterpret_cast<uint32_t*>(base + row_of(column0 + i * kStep) * pitch + f));
-        } else {
-            __nv_bfloat16* at = base + row_of(column0) * pitch + f;
-            const int64_t next = static_cast<int64_t>(kStep) * pitch;
-            const int here = ok ? left - column0 : 0;
-#pragma unroll
-            for (int i = 0; i < 32 / kStep; ++i, at += next)
-                if (i * kStep < here && EP_IN(row_of(column0 + i * kStep), p.rows))
-                    use(i, reinterpret_cast<uint32_t*>(at));
-        }
+        for (int i = 0; i < 32 / kStep; ++i, at += next)
+            if (i * kStep < here && EP_IN(row_of(column0 + i * kStep), p.rows)) use(i, reinterpret_cast<uint32_t*>(at));
     }
 };
 
