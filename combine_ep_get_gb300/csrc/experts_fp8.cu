@@ -17,12 +17,12 @@
 //
 // What bounds it: with 512 rows an expert the summing warps (a block of 128
 // terms takes them ~700 of the ~1000 cycles, the MMAs 512): 64 experts x 512
-// rows, [4096, 7168] weights, 0.93 ms = 2.1 PFLOP/s (1.05 ms after seconds of it,
-// under the power limit).  Tried and slower: pairs of CTAs on 256 rows (278
+// rows, [4096, 7168] weights, 0.85 ms = 2.25 PFLOP/s (0.96-1.0 ms after seconds of
+// it, under the power limit).  Tried and slower: pairs of CTAs on 256 rows (278
 // against 240 us on 16 experts x 512 rows; shared memory is freed, the summing
 // warps have as much to do and the pair waits for both), two-wide fp32
 // multiply-adds (their packing costs what they save).  With 32 rows an expert the weights bound it:
-// 1.95 GB in 0.291-0.297 ms = 6.6 TB/s.
+// 1.95 GB in 0.289-0.291 ms = 6.7 TB/s.
 #include "experts_mma.cuh"
 
 namespace epg {
