@@ -29,10 +29,13 @@
 // of the rows (1.58 -> 1.87 PFLOP/s, 4096 x 7168 x 7168 alone).
 //
 // Few tokens: the same walk over the experts that some token names, with the
-// tokens' rows gathered by index.  Each CTA sorts topk_idx itself.  The up
+// tokens' rows gathered by index, by 16-byte copies of two warps (gathers of four
+// rows by tensor map take up to 16 instructions a stage of 64 rows, ~90 cycles
+// each: 143 tokens over 10 experts 72 us, by copies 60; 6 tokens 17.4 against
+// 18.4).  Each CTA sorts topk_idx itself.  The up
 // product leaves h, rounded to bf16 for the down product's tensor cores and
 // expert by expert, so that its loads are boxes of rows and not gathers (143
-// tokens over 10 experts, 896 and 5208 features: 100 -> 72 us), the down
+// tokens over 10 experts, 896 and 5208 features: 100 -> 72 us at that step), the down
 // product fp32 rows for each (token, slot); whichever tile completes a
 // token's last expert sums the token's rows, k ascending, so the order of the
 // sum does not depend on timing.  Bound by the weights: one token, 8 experts
@@ -87,9 +90,8 @@ template <int kMode, int NT, int kCtas, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_constant__ MmaArgs p) {
     using S = Shape<NT, kCtas>;
     constexpr bool kFew = kMode == kFewUp || kMode == kFewDown;
-    // Rows of a load: 4 gathered ones where the rows are tokens anywhere in x, else a box of neighbours.
-    constexpr bool kGather = kMode == kFewUp;
-    constexpr int kBoxRows = kGather ? 4 : kFew ? kFewBoxRows : S::kBoxRows;
+    constexpr bool kGather = kMode == kFewUp;   // rows are tokens anywhere in x: warps 2 and 3 copy them
+    constexpr int kBoxRows = kFew ? kFewBoxRows : S::kBoxRows;
     constexpr int kStep = 16 * kCtas;   // an MMA's rows come in steps of
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stages = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(&s->full[i], 1);
+            mbar_init(&s->full[i], kGather ? 1 + kGatherWarps : 1);
             mbar_init(&s->empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -124,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
         s->gave_up = 0;
         fence_mbar_init();
         prefetch_map(&p.a);
-        prefetch_map(&p.b);
+        if (!kGather) prefetch_map(&p.b);
     }
     if (warp == 2) tmem_alloc<kCtas>(&s->tmem, S::kColumns);
     // The down product's kernel may start, and route, once every CTA of the
@@ -183,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
         for (int i0 = begin + (end - begin - 1) / 32 * 32; i0 >= begin && begin < end; i0 -= 32) {
             const int i = i0 + lane, e = i < end ? t.expert[i] : -1;
             const unsigned same = __match_any_sync(0xffffffffu, e);
-            if (e >= 0) t.list[ends[e] - __popc(same >> lane)] = static_cast<int16_t>(i);
+            if (e >= 0) t.list[ends[e] - __popc(same >> lane)] = static_cast<int16_t>(kGather ? i / p.K : i);
             __syncwarp();
             if (e >= 0 && (same >> lane) == 1u) ends[e] -= __popc(same);
             __syncwarp();
@@ -291,16 +293,11 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
             const Tile r = tile_at<NT, kStep>(g, t, p.E, feature_tiles, tile_features);
             const int share = r.width / kCtas;   // the row operand's rows of each CTA
             const int first = t.first[r.e] + r.row0 + rank * share;
-            // few tokens, up: lane i gathers the tokens of entries 4 i .. 4 i + 3 (past the last one, the last)
-            int row[4] = {};
-            if (kGather && 4 * lane < r.rows)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) row[j] = t.list[first + min(4 * lane + j, r.rows - 1)] / p.K;
             const auto boxes_of = [&](int who) {
                 return (max(0, min(share, r.rows - who * share)) + kBoxRows - 1) / kBoxRows;
             };
             const int boxes = boxes_of(rank);
-            const uint32_t bytes = kCtas * kABytes + (boxes_of(0) + (kCtas == 2 ? boxes_of(1) : 0)) *
+            const uint32_t bytes = kGather ? kABytes : kCtas * kABytes + (boxes_of(0) + (kCtas == 2 ? boxes_of(1) : 0)) *
                                                          (kBoxRows * kDepth * 2);
             const int f0 = r.f0 + rank * cta_features;
             const auto load_weights = [&](int stage, int kb) {
@@ -325,10 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
                 uint8_t* const sb = stages + stage * S::kStageBytes + kABytes;
                 uint32_t bar = smem_addr(&s->full[stage]);
                 if (kCtas == 2) bar = map_to_rank(bar, 0);
-                if (kGather) {
-                    if (lane < boxes)
-                        tma_gather4(sb + lane * 4 * kDepth * 2, &p.b, bar, kb * kDepth, row[0], row[1], row[2], row[3]);
-                } else if (elect_one()) {
+                if (elect_one()) {
                     for (int i = 0; i < boxes; ++i)
                         tma_load_2d<kCtas>(sb + i * kBoxRows * kDepth * 2, &p.b, bar, kb * kDepth, first + i * kBoxRows);
                 }
@@ -347,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
                     if (!ok) break;
                     load_weights(ring.stage, kb);
                 }
-                load_rows(ring.stage, kb);
+                if (!kGather) load_rows(ring.stage, kb);
             }
         }
         if (!ok) atomicOr(p.status, EP_ERR_TIMEOUT);
@@ -390,6 +384,66 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
             if (elect_one()) mma_commit<kCtas>(&s->drain);
             __syncwarp();
             warp_wait(&s->drain, 0);
+        }
+    } else if (kGather && (warp == 2 || warp == 3)) {
+        // The tokens' rows, 16 bytes a lane, 8 rows at a time, into the places
+        // the swizzle gives them.  A stage's copies are waited for when the
+        // kLag next ones are on their way (1: 128 tokens of all experts 3.17 ->
+        // 3.39 ms; 2, 4 and 5: 6 tokens alike, 143 tokens 61.0, 59.8, 59.6 us, 154
+        // tokens 48.0, 48.6, 49.3 against 60.3 and 47.6).
+        constexpr int kLag = 3, kCopies = NT / 8;
+        static_assert(kLag < S::kStages, "the stage waited for is never the one to be filled");
+        Ring<S::kStages> ring, landed;
+        const int tid = threadIdx.x - 64, chunk = tid & 7, row0 = tid >> 3;
+        const uint32_t place = kABytes + row0 * 128 + ((chunk ^ row0) << 4);
+        int in_flight = 0;
+        bool ok = true;
+        const auto hand_over = [&] {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && !(kTestDropFirstLoad && worker == 0 && landed.stage == 0 && landed.parity == 0))
+                mbar_arrive(&s->full[landed.stage]);
+            landed.next();
+            --in_flight;
+        };
+        for (int g = worker; g < tiles && ok; g += workers) {
+            const Tile r = tile_at<NT, kStep>(g, t, p.E, feature_tiles, tile_features);
+            const int first = t.first[r.e] + r.row0;
+            int tok[kCopies];
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                tok[i] = -1;
+                if (i * 8 + row0 < r.rows) tok[i] = t.list[first + i * 8 + row0];
+                if (tok[i] >= 0 && !EP_IN(tok[i], p.T)) tok[i] = -1;
+            }
+            for (int kb = kb_begin; kb < kb_end; ++kb, ring.next()) {
+                ok = warp_wait(&s->empty[ring.stage], ring.parity ^ 1);
+                if (!ok) break;
+                const uint32_t sb = smem_addr(stages + ring.stage * S::kStageBytes) + place;
+                const int column = kb * kDepth + chunk * 8;
+                const bool inside = column < p.depth;   // else zeros
+                const __nv_bfloat16* const from = p.x + (inside ? column : 0);
+#pragma unroll
+                for (int i = 0; i < kCopies; ++i) {
+                    if (tok[i] >= 0)
+                        copy16_async(sb + i * 1024, from + static_cast<int64_t>(tok[i]) * p.depth, inside);
+                }
+                copies_commit();
+                if (++in_flight > kLag) {
+                    copies_wait<kLag>();
+                    hand_over();
+                }
+            }
+        }
+        if (!ok) atomicOr(p.status, EP_ERR_TIMEOUT);
+        while (in_flight > 0) {
+            if (in_flight == 3)
+                copies_wait<2>();
+            else if (in_flight == 2)
+                copies_wait<1>();
+            else
+                copies_wait<0>();
+            hand_over();
         }
     } else if (warp >= 4) {
         const int q = warp & 3, turn = (warp - 4) / 4;
@@ -900,14 +954,14 @@ cudaError_t launch_few_tokens(const FewTokensParams& p, cudaStream_t stream) {
     constexpr int NT = 64;
     MmaArgs up{};
     const bool gated = p.act == EP_ACT_SWIGLU;
-    if (!(gated ? gated_map(&up.a, p.w_up, p.E, p.I, p.H) : weight_map(&up.a, p.w_up, p.E, p.Nw, p.H, kM)) ||
-        !row_map(&up.b, p.x, p.T, p.H, 1))
+    if (!(gated ? gated_map(&up.a, p.w_up, p.E, p.I, p.H) : weight_map(&up.a, p.w_up, p.E, p.Nw, p.H, kM)))
         return cudaErrorInvalidValue;
     up.depth = p.H;
     up.F = p.I;
     up.gate_half = gated ? p.I : 0;
     up.E = p.E;
     up.act = p.act;
+    up.x = p.x;
     up.topk_idx = p.topk_idx;
     up.topk_weights = p.topk_weights;
     up.T = p.T;

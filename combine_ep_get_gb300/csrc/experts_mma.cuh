@@ -29,6 +29,7 @@ constexpr bool kTestDropFirstLoad = true;
 constexpr bool kTestDropFirstLoad = false;
 #endif
 
+constexpr int kGatherWarps = 2;  // few tokens, up: warps 2 and 3
 enum Mode { kProduct, kInputGrad, kFewUp, kFewDown };
 
 struct MmaArgs {
@@ -46,6 +47,7 @@ struct MmaArgs {
     __nv_bfloat16* y;             // rows of F
     __nv_bfloat16* z;             // rows of F or 2 F
     // few tokens
+    const __nv_bfloat16* x;       // up: [T][depth]
     const int64_t* topk_idx;
     const float* topk_weights;
     int T, K;
@@ -83,7 +85,7 @@ struct Table {
     int* tile_end;    // [E]
     int* first;       // [E] first row, or first entry of the list
     int* count;       // [E]
-    int16_t* list;    // few tokens: entries t * K + k, expert by expert
+    int16_t* list;    // few tokens: entries t * K + k (up: their tokens t), expert by expert
     int16_t* expert;  // few tokens: expert of each entry, -1 for none; behind them, tokens just completed
     uint8_t* named;   // few tokens: experts of each token
 };

@@ -116,12 +116,15 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* s
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(m),
                  "r"(smem_addr(src)), "r"(x), "r"(y), "r"(z) : "memory");
 }
-// Four rows of a map whose box is one row high, by their indices.
-__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* m, uint32_t bar, int x, int r0, int r1,
-                                            int r2, int r3) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::
-            "r"(smem_addr(dst)), "l"(m), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3) : "memory");
+// 16 bytes from global to shared memory in the thread's current group of
+// copies, zeros if not `there` (the address is then not read).
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {   // until at most kLeft groups are in flight
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
 template <int kCtas>
