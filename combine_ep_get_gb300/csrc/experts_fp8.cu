@@ -58,6 +58,40 @@ struct Fp8Shared {
     int warp_sum[kFp8Warps];
 };
 
+// 16 neighbouring bf16 features of a row, a whole 32-byte sector: in one access
+// where y, z and the residual start on 32 bytes, else in two (a lane is a row, so
+// an access touches 32 lines whatever its width.  Two: 40405 rows, 256 -> 3200,
+// residual 288 against 239 us, 8192 rows, 512 -> 2 x 2048, z 60 against 41,
+// 32768 rows, 7168 -> 2 x 2048 861 against 826).
+struct Words8 {
+    uint32_t w[8];
+};
+__device__ __forceinline__ void store16(__nv_bfloat16* at, const Words8& v, bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(v.w[0]), "r"(v.w[1]),
+                     "r"(v.w[2]), "r"(v.w[3]), "r"(v.w[4]), "r"(v.w[5]), "r"(v.w[6]), "r"(v.w[7]) : "memory");
+    } else {
+        st_v4(at, make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]));
+        st_v4(at + 8, make_uint4(v.w[4], v.w[5], v.w[6], v.w[7]));
+    }
+}
+__device__ __forceinline__ Words8 load16(const __nv_bfloat16* at, bool wide) {
+    Words8 v;
+    if (wide) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];" : "=r"(v.w[0]), "=r"(v.w[1]),
+                     "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]), "=r"(v.w[7]) : "l"(at)
+                     : "memory");
+    } else {
+        const uint4 a = reinterpret_cast<const uint4*>(at)[0], b = reinterpret_cast<const uint4*>(at)[1];
+        v = {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+    }
+    return v;
+}
+__device__ __forceinline__ Words8 pack16(const float* a, const float* b) {
+    return {{pack2(a[0], a[1]), pack2(a[2], a[3]), pack2(a[4], a[5]), pack2(a[6], a[7]), pack2(b[0], b[1]),
+             pack2(b[2], b[3]), pack2(b[4], b[5]), pack2(b[6], b[7])}};
+}
+
 // The epilogue of a row's 64 columns in a warp: 64 features from f, or, gated,
 // 32 from f (8 gate columns, then 8 up ones, four times).  F is a multiple of
 // 128, so all of them exist or none.  The bias is read before the first store
@@ -66,6 +100,8 @@ struct Fp8Shared {
 template <bool kGated>
 __device__ __forceinline__ void finish_row(const MmaArgs& p, int e, int64_t d, int f, float (&v)[kSumColumns]) {
     const int Fw = kGated ? 2 * p.F : p.F;
+    const bool wide = ((reinterpret_cast<uintptr_t>(p.y) | reinterpret_cast<uintptr_t>(p.z) |
+                        reinterpret_cast<uintptr_t>(p.residual)) & 31) == 0;
     const float w = p.row_weight ? p.row_weight[d] : 1.0f;
     // columns 8 i .. 8 i + 7 are these rows of W
     const auto wrow = [&](int i) { return kGated ? (i % 2) * p.gate_half + f + i / 2 * 8 : f + i * 8; };
@@ -88,10 +124,10 @@ __device__ __forceinline__ void finish_row(const MmaArgs& p, int e, int64_t d, i
     }
     if (p.z)
 #pragma unroll
-        for (int i = 0; i < kSumColumns / 8; ++i) {
-            const float* const u = v + 8 * i;
-            st_v4(p.z + d * Fw + wrow(i),
-                  make_uint4(pack2(u[0], u[1]), pack2(u[2], u[3]), pack2(u[4], u[5]), pack2(u[6], u[7])));
+        for (int i = 0; i < kSumColumns / 16; ++i) {
+            // columns 8 a .. 8 a + 7 and 8 b .. 8 b + 7 are neighbours in W
+            const int a = kGated ? i / 2 * 4 + i % 2 : 2 * i, b = kGated ? a + 2 : a + 1;
+            store16(p.z + d * Fw + wrow(a), pack16(v + 8 * a, v + 8 * b), wide);
         }
     constexpr int kOut = kGated ? kSumColumns / 2 : kSumColumns;
     if (kGated) {
@@ -101,27 +137,24 @@ __device__ __forceinline__ void finish_row(const MmaArgs& p, int e, int64_t d, i
     __nv_bfloat16* const out = p.y + d * p.F + f;
 #pragma unroll
     for (int c0 = 0; c0 < kOut; c0 += 32) {
-        uint4 r[4];
+        Words8 r[2];
         if (p.residual)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) r[i] = *reinterpret_cast<const uint4*>(p.residual + d * p.F + f + c0 + 8 * i);
+            for (int i = 0; i < 2; ++i) r[i] = load16(p.residual + d * p.F + f + c0 + 16 * i, wide);
         if (!kGated) activate_all(*reinterpret_cast<float(*)[32]>(v + c0), p.act);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float* const a = v + c0 + 8 * i;
+        for (int i = 0; i < 2; ++i) {
+            float* const a = v + c0 + 16 * i;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a[j] *= w;
-            if (p.residual) {
-                const uint32_t words[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+            for (int j = 0; j < 16; ++j) a[j] *= w;
+            if (p.residual)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 s = unpack2(words[j]);
+                for (int j = 0; j < 8; ++j) {
+                    const float2 s = unpack2(r[i].w[j]);
                     a[2 * j] += s.x;
                     a[2 * j + 1] += s.y;
                 }
-            }
-            st_v4(out + c0 + 8 * i,
-                  make_uint4(pack2(a[0], a[1]), pack2(a[2], a[3]), pack2(a[4], a[5]), pack2(a[6], a[7])));
+            store16(out + c0 + 16 * i, pack16(a, a + 8), wide);
         }
     }
 }

@@ -162,6 +162,33 @@ def test_product_fp8_many_experts():
     run_product(rng.integers(0, 4, size=2048).tolist(), 128, 128, "swiglu", fp8=True, seed=7)
 
 
+@pytest.mark.parametrize("N,act", [(384, "gelu"), (256, "swiglu")])
+@pytest.mark.parametrize("at", [(8, 0, 0), (0, 8, 0), (0, 0, 8), (8, 8, 8)])
+def test_product_fp8_arrays_on_16_bytes(N, act, at):
+    """y, z and the residual need 16-byte alignment alone; on 32 bytes they give the same bits."""
+    from gpu_path import B
+    g = gen(N)
+    off, cnt, rows = blocks([5, 0, 140], gap=1)
+    Nw = 2 * N if act == "swiglu" else N
+    x, xs = to_fp8(normal(g, rows, 256), 1)
+    w, ws = to_fp8(normal(g, 3, Nw, 256, std=1.0 / 16), 128)
+    res = normal(g, rows, N)
+
+    def put(shape, shift):
+        n = shape[0] * shape[1]
+        return torch.full((n + 16,), -7.0, dtype=torch.bfloat16, device="cuda")[shift:shift + n].view(shape)
+
+    def run(ay, az, ar):
+        y, z, r, st = put((rows, N), ay), put((rows, Nw), az), put((rows, N), ar), status()
+        r.copy_(res)
+        B.ep_expert_gemm(x, w, off, cnt, y, st, activation=ACTS[act], residual=r, z=z, x_sf=xs, w_sf=ws)
+        assert int(st.item()) == 0
+        return y, z
+
+    for got, want in zip(run(*at), run(0, 0, 0)):
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
 @pytest.mark.parametrize("act", list(ACTS))
 def test_nan_and_infinity_follow_the_activation(act):
     """NaN rows give NaN; +inf pre-activations give what the formula gives."""
