@@ -17,7 +17,7 @@
 //
 // What bounds it: with 512 rows an expert the summing warps (a block of 128
 // terms takes them ~700 of the ~1000 cycles, the MMAs 512): 64 experts x 512
-// rows, [4096, 7168] weights, 0.85 ms = 2.25 PFLOP/s (0.96-1.0 ms after seconds of
+// rows, [4096, 7168] weights, 0.83 ms = 2.33 PFLOP/s (0.95-1.0 ms after seconds of
 // it, under the power limit).  Tried and slower: pairs of CTAs on 256 rows (278
 // against 240 us on 16 experts x 512 rows; shared memory is freed, the summing
 // warps have as much to do and the pair waits for both), two-wide fp32
