@@ -735,7 +735,7 @@ ep_status_t check_experts(int64_t num_rows, int K, int N, int E, int act, const 
                           const int32_t* counts, const int32_t* d_status) {
     if (!d_status || num_rows < 0 || K < 1 || N < 1 || E < 1) return EP_RET(EP_ERR_INVALID_ARG);
     if (act < EP_ACT_NONE || act > EP_ACT_SWIGLU) return EP_RET(EP_ERR_INVALID_ARG);
-    if (E > EP_MAX_EXPERTS || num_rows > INT32_MAX || K > epg::kMaxExpertDim || N > epg::kMaxExpertDim)
+    if (E > EP_MAX_EXPERTS || num_rows > EP_MAX_EXPERT_ROWS || K > epg::kMaxExpertDim || N > epg::kMaxExpertDim)
         return EP_RET(EP_ERR_UNSUPPORTED);
     if (K % 8 != 0 || N % 8 != 0 || !ok_ptr(offset) || !ok_ptr(counts)) return EP_RET(EP_ERR_INVALID_ARG);
     return EP_OK;

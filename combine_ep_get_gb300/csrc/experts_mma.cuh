@@ -116,7 +116,7 @@ __device__ __forceinline__ Tile tile_at(int g, const Table& t, int E, int featur
     const int f = local / in_group, row_tile = group * kGroupTiles + local % in_group;
     // an expert's tiles share its rows evenly, unless the rounding to an MMA's
     // step would leave the last one without any
-    const int even = ((cnt + n - 1) / n + kStep - 1) / kStep * kStep;
+    const int even = ((cnt - 1) / n + kStep) / kStep * kStep;   // ceil(cnt / n), without cnt + n: it may pass 2^31
     const int per = (n - 1) * even < cnt ? even : NT;
     r.row0 = row_tile * per;
     r.rows = min(per, cnt - r.row0);

@@ -360,6 +360,10 @@ ep_status_t ep_combine_expanded(const void* y, int64_t num_y_rows, const float* 
 #define EP_ACT_SILU   3
 #define EP_ACT_SWIGLU 4
 
+/* Most rows of ep_expert_gemm and its backward call: row numbers are 32-bit
+ * and reach past the last row, by less than 2^16. */
+#define EP_MAX_EXPERT_ROWS 2147418112LL   /* 2^31 - 2^16 */
+
 /*
  * Experts' matrix product, bias, activation, row weight and residual in its
  * epilogue.  For every expert e and row d of its block,
@@ -393,8 +397,8 @@ ep_status_t ep_combine_expanded(const void* y, int64_t num_y_rows, const float* 
  * y             bf16 [num_rows, n_dim].
  * z             bf16 [num_rows, n_w] or NULL: z[d] rounded, for
  *               ep_expert_gemm_backward.
- * Limits: num_experts <= EP_MAX_EXPERTS, num_rows <= 2^31 - 1, k_dim and
- * n_dim <= 2^20 (beyond: EP_ERR_UNSUPPORTED).
+ * Limits: num_experts <= EP_MAX_EXPERTS, num_rows <= EP_MAX_EXPERT_ROWS, k_dim
+ * and n_dim <= 2^20 (beyond: EP_ERR_UNSUPPORTED).
  */
 ep_status_t ep_expert_gemm(const void* x, const float* x_sf, int sf_col_major, const void* w,
                            const float* w_sf, int in_dtype, const float* bias, int activation,
