@@ -836,6 +836,7 @@ ep_status_t ep_expert_gemm_backward(const void* dy, const void* x, const void* w
     p.dz = reinterpret_cast<__nv_bfloat16*>(ws + b.off_dz);
     p.bias_part = reinterpret_cast<float*>(ws + b.off_part);
     p.weight_part = reinterpret_cast<float*>(ws + b.off_weight);
+    p.blocks_fit = reinterpret_cast<int*>(ws + b.off_fit);
     p.status = d_status;
     return epg::launch_expert_backward(p, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
                ? EP_OK

@@ -46,6 +46,7 @@ struct ExpertBackwardParams {
     __nv_bfloat16* dz;           // workspace [rows][Nw]
     float* bias_part;            // workspace [row tiles][Nw]: sums of dz over a tile's rows
     float* weight_part;          // workspace [strips][rows]: sums of dy * a over a strip's columns
+    int* blocks_fit;             // workspace: expert_blocks' answer, for the kernel that adds the partial sums
     int32_t* status;
 };
 
@@ -114,7 +115,7 @@ cudaError_t launch_experts(void (*kernel)(KArgs...), dim3 grid, dim3 block, size
 constexpr int kBackwardTileRows = 32;   // rows of one partial column sum of dz
 constexpr int kBackwardStrip = 256;     // columns of one partial row sum
 struct BackwardWorkspace {
-    size_t off_dz, off_part, off_weight, total;
+    size_t off_dz, off_part, off_weight, off_fit, total;
 };
 inline BackwardWorkspace backward_workspace(int64_t rows, int N, int Nw, int E) {
     const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
@@ -123,7 +124,8 @@ inline BackwardWorkspace backward_workspace(int64_t rows, int N, int Nw, int E) 
     b.off_dz = 0;
     b.off_part = up(static_cast<size_t>(rows) * Nw * 2);
     b.off_weight = b.off_part + up(tiles * Nw * 4);
-    b.total = b.off_weight + up((static_cast<size_t>(N) + kBackwardStrip - 1) / kBackwardStrip * rows * 4) + 256;
+    b.off_fit = b.off_weight + up((static_cast<size_t>(N) + kBackwardStrip - 1) / kBackwardStrip * rows * 4);
+    b.total = b.off_fit + 256;
     return b;
 }
 struct FewWorkspace {
@@ -215,6 +217,36 @@ __device__ __forceinline__ int expert_rows(const int32_t* offset, const int32_t*
         return static_cast<int>(rows - o);
     }
     return static_cast<int>(c);
+}
+
+// The experts' blocks into shared memory, by all threads of a block of
+// kThreads.  Blocks whose rows add up to more than there are overlap, and may
+// have more row tiles than the workspace and the grids are sized for (rows /
+// tile + E): they are flagged and count as empty; the answer is then false.
+template <int kThreads>
+__device__ __forceinline__ bool expert_blocks(const int32_t* offset, const int32_t* counts, int E, int64_t rows,
+                                              int* first, int* count, int64_t* warp_rows, int32_t* status) {
+    int64_t mine = 0;
+    for (int e = threadIdx.x; e < E; e += kThreads) {
+        int64_t at;
+        const int n = expert_rows(offset, counts, e, rows, &at, status);
+        first[e] = static_cast<int>(at);
+        count[e] = n;
+        mine += n;
+    }
+    // EP_MAX_EXPERTS / kThreads blocks of less than 2^31 rows: 16 bits and the rest
+    const int64_t low = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(mine) & 0xffffu);
+    const int64_t high = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(mine >> 16));
+    if ((threadIdx.x & 31) == 0) warp_rows[threadIdx.x / 32] = (high << 16) + low;
+    __syncthreads();
+    int64_t all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) all += warp_rows[w];
+    if (all <= rows) return true;
+    for (int e = threadIdx.x; e < E; e += kThreads) count[e] = 0;
+    if (threadIdx.x == 0) atomicOr(status, EP_ERR_CAPACITY);
+    __syncthreads();
+    return false;
 }
 
 // Inclusive scan of f(e) over the experts into out[e], by all threads of a

@@ -50,16 +50,14 @@ struct Tables {
 };
 
 __device__ __forceinline__ Tables row_tables(const ExpertBackwardParams& p, int* smem, int* warp_sum) {
+    __shared__ int64_t warp_rows[kThreads / 32];
     Tables t;
     t.tile_end = smem;
     t.first = smem + p.E;
     t.count = t.first + p.E;
-    for (int e = threadIdx.x; e < p.E; e += kThreads) {
-        int64_t first;
-        t.count[e] = expert_rows(p.expert_offset, p.counts, e, p.rows, &first, p.status);
-        t.first[e] = static_cast<int>(first);
-    }
-    __syncthreads();
+    const bool fit =
+        expert_blocks<kThreads>(p.expert_offset, p.counts, p.E, p.rows, t.first, t.count, warp_rows, p.status);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.blocks_fit = fit;
     scan_experts<kThreads>(p.E, t.tile_end, warp_sum,
                            [&](int e) { return (t.count[e] + kBackwardTileRows - 1) / kBackwardTileRows; });
     return t;
@@ -189,10 +187,11 @@ __global__ void __launch_bounds__(kThreads) backward_sums_kernel(const __grid_co
     pdl_wait();
     pdl_launch_dependents();
     const int column_blocks = (p.Nw + columns - 1) / columns;
+    const bool fit = p.rows == 0 || *p.blocks_fit;   // (without rows there was no pass before)
     int64_t first;
     if (static_cast<int>(blockIdx.x) >= bias_blocks) {
         const int block = blockIdx.x - bias_blocks, e = block / row_blocks;
-        const int cnt = expert_rows(p.expert_offset, p.counts, e, p.rows, &first, p.status);
+        const int cnt = fit ? expert_rows(p.expert_offset, p.counts, e, p.rows, &first, p.status) : 0;
         const int strips = (p.N + kBackwardStrip - 1) / kBackwardStrip;
         for (int r = block % row_blocks * kThreads + threadIdx.x; r < cnt; r += row_blocks * kThreads) {
             float v = 0.0f;
@@ -213,8 +212,8 @@ __global__ void __launch_bounds__(kThreads) backward_sums_kernel(const __grid_co
     __syncthreads();
     before = 0;
     for (int w = 0; w < kThreads / 32; ++w) before += warp_sum[w];
-    const int tiles = (expert_rows(p.expert_offset, p.counts, e, p.rows, &first, p.status) + kBackwardTileRows - 1) /
-                      kBackwardTileRows;
+    const int rows = fit ? expert_rows(p.expert_offset, p.counts, e, p.rows, &first, p.status) : 0;
+    const int tiles = (rows + kBackwardTileRows - 1) / kBackwardTileRows;
     float v = 0.0f;
     if (n < p.Nw)
 #pragma unroll 8

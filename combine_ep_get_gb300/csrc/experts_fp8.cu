@@ -54,6 +54,7 @@ struct Fp8Shared {
     // a block's row scales times the two weight scales of the tile: of its
     // first and last 128 features, or of its gate and up features
     float scales[kAccs][2][kRows];
+    int64_t warp_rows[kFp8Warps];
     uint32_t tmem;
     int warp_sum[kFp8Warps];
 };
@@ -191,12 +192,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
     if (warp == 2) tmem_alloc<1>(&s->tmem, kAccs * kFeatures);
     pdl_wait();
     pdl_launch_dependents();
-    for (int e = threadIdx.x; e < p.E; e += kFp8Threads) {
-        int64_t first;
-        t.count[e] = expert_rows(p.expert_offset, p.counts, e, p.rows, &first, p.status);
-        t.first[e] = static_cast<int>(first);
-    }
-    __syncthreads();
+    expert_blocks<kFp8Threads>(p.expert_offset, p.counts, p.E, p.rows, t.first, t.count, s->warp_rows, p.status);
     scan_experts<kFp8Threads>(p.E, t.tile_end, s->warp_sum, [&](int e) { return (t.count[e] + kRows - 1) / kRows; });
     tcgen05_before_sync();
     __syncthreads();

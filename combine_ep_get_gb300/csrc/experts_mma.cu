@@ -198,12 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
             }
         if (shared) fence_proxy_async_smem();   // before the stages are loaded
     } else {
-        for (int e = threadIdx.x; e < p.E; e += kThreads) {
-            int64_t first;
-            t.count[e] = expert_rows(p.expert_offset, p.counts, e, p.rows, &first, p.status);
-            t.first[e] = static_cast<int>(first);
-        }
-        __syncthreads();
+        expert_blocks<kThreads>(p.expert_offset, p.counts, p.E, p.rows, t.first, t.count, s->warp_rows, p.status);
         scan_experts<kThreads>(p.E, t.tile_end, s->warp_sum, [&](int e) { return (t.count[e] + NT - 1) / NT; });
     }
     tcgen05_before_sync();
@@ -638,11 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
     if (warp == 2) tmem_alloc<kCtas>(&s->tmem, S::kColumns);
     if (!p.wait_late) pdl_wait();
     pdl_launch_dependents();
-    for (int e = threadIdx.x; e < p.E; e += kThreads) {
-        int64_t first;
-        s_count[e] = expert_rows(p.expert_offset, p.counts, e, p.rows, &first, p.status);
-        s_first[e] = static_cast<int>(first);
-    }
+    expert_blocks<kThreads>(p.expert_offset, p.counts, p.E, p.rows, s_first, s_count, s->warp_rows, p.status);
     tcgen05_before_sync();
     __syncthreads();
     if (kCtas == 2) cluster_sync();   // the pair's barriers are there for either

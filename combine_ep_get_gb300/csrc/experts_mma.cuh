@@ -74,6 +74,7 @@ struct Barriers {
     uint64_t full[12], empty[12], acc_full[2], acc_empty[2], drain;
     uint64_t tail_full[6], cleared[6];   // weight gradient: an expert's last stage
     uint32_t tmem;
+    int64_t warp_rows[kThreads / 32];
     int total_tiles;
     int warp_sum[kThreads / 32];
     int gave_up;                  // a wait of the epilogue ran out

@@ -393,7 +393,9 @@ ep_status_t ep_combine_expanded(const void* y, int64_t num_y_rows, const float* 
  *               int32 [num_experts + 1] and [num_experts], as ep_get_layout
  *               writes them (any offsets of disjoint blocks will do: one
  *               expert of num_rows rows is a dense product).  Rows at or
- *               beyond num_rows are skipped and set EP_ERR_CAPACITY.
+ *               beyond num_rows are skipped and set EP_ERR_CAPACITY.  Blocks
+ *               whose rows then add up to more than num_rows overlap: they
+ *               set EP_ERR_CAPACITY and count as empty.
  * y             bf16 [num_rows, n_dim].
  * z             bf16 [num_rows, n_w] or NULL: z[d] rounded, for
  *               ep_expert_gemm_backward.
