@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 3) activation_backward_kernel(const 
                 for (int i = 0; i < 8; ++i) sums[row_lane][vec * 8 + i] = sum[half][i];
                 __syncthreads();
                 for (int c = threadIdx.x; c < kBackwardStrip; c += kThreads)
-                    if (strip * kBackwardStrip + c < p.N) {
+                    if (strip * kBackwardStrip + c < p.N && EP_IN(tile, p.rows / kBackwardTileRows + p.E)) {
                         float v = 0.0f;
                         for (int i = 0; i < kRowLanes; ++i) v += sums[i][c];
                         p.bias_part[static_cast<int64_t>(tile) * p.Nw + half * p.N + strip * kBackwardStrip + c] = v;
@@ -217,14 +217,16 @@ __global__ void __launch_bounds__(kThreads) backward_sums_kernel(const __grid_co
     float v = 0.0f;
     if (n < p.Nw)
 #pragma unroll 8
-        for (int i = part; i < tiles; i += parts) v += p.bias_part[static_cast<int64_t>(before + i) * p.Nw + n];
+        for (int i = part; i < tiles; i += parts)
+            if (EP_IN(before + i, p.rows / kBackwardTileRows + p.E))
+                v += p.bias_part[static_cast<int64_t>(before + i) * p.Nw + n];
     if (parts > 1) {
         sums[threadIdx.x] = v;
         __syncthreads();
         if (part > 0) return;
         for (int i = 1; i < parts; ++i) v += sums[i * columns + c];
     }
-    if (n < p.Nw) p.dbias[static_cast<int64_t>(e) * p.Nw + n] = v;
+    if (n < p.Nw && EP_IN(e, p.E)) p.dbias[static_cast<int64_t>(e) * p.Nw + n] = v;
 }
 
 }  // namespace

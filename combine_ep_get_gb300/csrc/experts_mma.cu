@@ -234,6 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
         for (int j = tid; j < r.rows; j += kReadWarps * 32) {
             if (j / 32 % of != which) continue;
             const int tok = t.list[first + j] / p.K;
+            if (!EP_IN((r.f0 / kM) * p.T + tok, p.done_words)) continue;
             const uint32_t before = atomicAdd(&p.done[(r.f0 / kM) * p.T + tok], 1u);
             if (before + 1 == t.named[tok]) {
                 __threadfence();
@@ -669,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
+        if (lane == 0 && EP_IN(e, p.E) && EP_IN(row0, p.Nw) && EP_IN(k0 + c0, p.K)) {
             tma_store_3d(&p.out, box, k0 + c0, row0, e);
             bulk_commit();
         }
