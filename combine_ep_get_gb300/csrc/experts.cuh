@@ -90,6 +90,19 @@ inline cudaError_t allow_all_smem(const void* kernel, std::atomic<bool>* done) {
     return e;
 }
 
+// Reads before the wait.  Three of the experts' kernels read before their
+// griddepcontrol.wait: the few-token layer's down kernel (topk_idx, w_down) and
+// both products of the gradients where another kernel of the call stands
+// between them and dz's (dz, x, w, the blocks).  All of it was complete before
+// that kernel, whose threads wait before they let the next one start (or, for
+// the second product, before they let the first one start): what a wait has
+// seen end is in L2.  There the early reads go, by tensor maps or __ldcg, never
+// through an L1 that an earlier launch may have filled.  What the kernel just
+// before writes (h, the sums) is read after the wait or not at all, and every
+// kernel waits before it ends, so a kernel that waits for the last one of a
+// call waits for all of them.  (With every wait at the start: gradients of
+// 5005 rows over 40 experts 90.9 -> 97.8 us, one token's layer 116.6 -> 120.4.)
+
 // launch_pdl with clusters of `cluster` CTAs.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_experts(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
@@ -203,9 +216,11 @@ __device__ __forceinline__ void activate_all(float (&v)[N], int act) {
 }
 
 // Rows of expert e that lie inside the arrays; the rest is skipped and flagged.
+// kEarly: a read that may come before the wait.
+template <bool kEarly = false>
 __device__ __forceinline__ int expert_rows(const int32_t* offset, const int32_t* counts, int e, int64_t rows,
                                            int64_t* first, int32_t* status) {
-    const int64_t o = offset[e], c = counts[e];
+    const int64_t o = kEarly ? __ldcg(offset + e) : offset[e], c = kEarly ? __ldcg(counts + e) : counts[e];
     *first = o;
     if (c <= 0) return 0;
     if (o < 0 || o >= rows) {
@@ -229,7 +244,7 @@ __device__ __forceinline__ bool expert_blocks(const int32_t* offset, const int32
     int64_t mine = 0;
     for (int e = threadIdx.x; e < E; e += kThreads) {
         int64_t at;
-        const int n = expert_rows(offset, counts, e, rows, &at, status);
+        const int n = expert_rows<true>(offset, counts, e, rows, &at, status);
         first[e] = static_cast<int>(at);
         count[e] = n;
         mine += n;

@@ -264,7 +264,8 @@ cudaError_t launch_expert_backward(const ExpertBackwardParams& given, cudaStream
     }
     // Both products need only dz.  A kernel between them and dz's has waited
     // for dz before it let them start, so they need not wait for it to end
-    // until they end themselves: each fills the SMs that the one before frees.
+    // until they end themselves ("Reads before the wait" in experts.cuh): each
+    // fills the SMs that the one before frees.
     bool late = p.dbias || p.d_row_weight;
     if (p.dx) {
         const cudaError_t e = launch_input_grad(p, dz, late, stream);

@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
     }
     if (warp == 2) tmem_alloc<kCtas>(&s->tmem, S::kColumns);
     // The down product's kernel may start, and route, once every CTA of the
-    // up product's has seen its own inputs complete.
+    // up product's has seen its own inputs complete ("Reads before the wait").
     if (kMode != kFewDown) {
         if (!p.wait_late) pdl_wait();
         pdl_launch_dependents();
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
     if (kFew) {
         // entries by expert, in the order of (token, slot)
         for (int i = threadIdx.x; i < p.T * p.K; i += kThreads) {
-            const int64_t e = p.topk_idx[i];
+            const int64_t e = __ldcg(reinterpret_cast<const long long*>(p.topk_idx) + i);   // (may come before the wait)
             const bool ok = e >= 0 && e < p.E;
             if (!ok && e != -1 && kMode == kFewUp && blockIdx.x == 0) atomicOr(p.status, EP_ERR_INVALID_INDEX);
             t.expert[i] = ok ? static_cast<int16_t>(e) : static_cast<int16_t>(-1);

@@ -57,7 +57,7 @@ struct MmaArgs {
     __nv_bfloat16* out;           // [T][F]
     int32_t* status;
     int split;                    // CTAs of a cluster that share a tile's sum, each a piece of k (1: none)
-    int wait_late;                // the inputs are complete: wait for the kernel before only at the end
+    int wait_late;                // the inputs are complete: wait only at the end ("Reads before the wait")
 };
 
 template <int NT, int kCtas>
