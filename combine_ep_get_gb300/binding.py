@@ -417,11 +417,18 @@ def ep_expert_gemm_backward_workspace_bytes(num_rows, n_dim, num_experts, activa
 def ep_expert_gemm_backward(dy, x, w, z, expert_offset, num_tokens_per_expert, workspace, d_status, dx=None, dw=None,
                             dbias=None, d_row_weight=None, activation=EP_ACT_NONE, row_weight=None, stream=None):
     """Gradients of ep_expert_gemm (bf16) for its rows, weights, bias and row
-    weights, each where its output is given (see the C header).  The
+    weights, each where its output is given (see the C header).  x may be None
+    without dw, w without dx, z without an activation and d_row_weight.  The
     residual's gradient is dy itself."""
     bf16, f32 = torch.bfloat16, torch.float32
     rows, n_dim = dy.shape
-    E, n_w, k_dim = (w if w is not None else dw).shape
+    like_w = w if w is not None else dw
+    if like_w is not None:
+        E, n_w, k_dim = like_w.shape
+    else:   # no product can be wanted: x and w are not read, k_dim is any width
+        E, n_w = num_tokens_per_expert.numel(), 2 * n_dim if activation == EP_ACT_SWIGLU else n_dim
+        like_x = x if x is not None else dx
+        k_dim = like_x.shape[1] if like_x is not None else 8
     assert n_w == (2 * n_dim if activation == EP_ACT_SWIGLU else n_dim)
     first, count = _blocks(expert_offset, num_tokens_per_expert, E)
     assert workspace.is_contiguous()
