@@ -132,15 +132,17 @@ def _ptr(t):
 
 # The current stream's handle without a Stream object around it, which costs a
 # call more than all of its checks; torch.cuda.current_stream() where a torch
-# has no such shortcut.
+# has no such shortcut.  The device without torch.cuda's check that CUDA is up:
+# a call has tensors on it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _stream(stream):
     if stream is not None:
         return stream.cuda_stream
-    if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+    if _raw_stream is not None and _current_device is not None:
+        return _raw_stream(_current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -362,18 +364,34 @@ def ep_combine_hierarchical(y, topk_idx, topk_weights, num_experts, num_ranks, r
 
 def _take(t, dtype, shape, name):
     """Address of a contiguous tensor of this type and shape (the library
-    takes no strides); None stays None."""
+    takes no strides) on the GPU (or pinned, which kernels reach too); None
+    stays None."""
     if t is None:
         return None
-    assert t.dtype is dtype and t.shape == shape and t.is_contiguous(), \
-        "%s: a contiguous %s tensor of shape %s is wanted" % (name, dtype, tuple(shape))
+    assert t.dtype is dtype and t.shape == shape and t.is_contiguous() and (t.is_cuda or t.is_pinned()), \
+        "%s: a contiguous %s tensor of shape %s on the GPU is wanted" % (name, dtype, tuple(shape))
     return t.data_ptr()
+
+
+def _take_any(t, name):
+    """Address of a contiguous tensor of any shape on the GPU."""
+    assert t.is_contiguous() and (t.is_cuda or t.is_pinned()), "%s: a contiguous tensor on the GPU is wanted" % name
+    return t.data_ptr()
+
+
+def _word(d_status):
+    """Address of the status word; None stays None (the library answers invalid_arg)."""
+    if d_status is None:
+        return None
+    assert d_status.dtype is torch.int32 and (d_status.is_cuda or d_status.is_pinned()), \
+        "d_status: an int32 word on the GPU is wanted"
+    return d_status.data_ptr()
 
 
 def _blocks(expert_offset, num_tokens_per_expert, E):
     """Addresses of the experts' blocks (offsets may go on past the last expert's)."""
-    assert expert_offset.dtype is torch.int32 and expert_offset.numel() >= E and expert_offset.is_contiguous()
-    return expert_offset.data_ptr(), _take(num_tokens_per_expert, torch.int32, (E,), "num_tokens_per_expert")
+    assert expert_offset.dtype is torch.int32 and expert_offset.numel() >= E
+    return _take_any(expert_offset, "expert_offset"), _take(num_tokens_per_expert, torch.int32, (E,), "num_tokens_per_expert")
 
 
 def ep_expert_gemm(x, w, expert_offset, num_tokens_per_expert, y, d_status, bias=None, activation=EP_ACT_NONE,
@@ -397,15 +415,15 @@ def ep_expert_gemm(x, w, expert_offset, num_tokens_per_expert, y, d_status, bias
     if fp8:
         assert kind in (torch.float8_e4m3fn, torch.uint8)
         stride = (rows + 3) // 4 * 4 if sf_col_major else rows
-        assert x_sf.dtype is f32 and x_sf.numel() >= stride * (k_dim // 128) and x_sf.is_contiguous()
-        scales, scale_weights = x_sf.data_ptr(), _take(w_sf, f32, (E, n_w // 128, k_dim // 128), "w_sf")
+        assert x_sf.dtype is f32 and x_sf.numel() >= stride * (k_dim // 128)
+        scales, scale_weights = _take_any(x_sf, "x_sf"), _take(w_sf, f32, (E, n_w // 128, k_dim // 128), "w_sf")
     first, count = _blocks(expert_offset, num_tokens_per_expert, E)
     code = _lib.ep_expert_gemm(_take(x, kind, (rows, k_dim), "x"), scales, 1 if sf_col_major else 0,
                                _take(w, kind, (E, n_w, k_dim), "w"), scale_weights, EP_FP8_E4M3 if fp8 else EP_BF16,
                                _take(bias, f32, (E, n_w), "bias"), activation,
                                _take(row_weight, f32, (rows,), "row_weight"),
                                _take(residual, bf16, (rows, n_dim), "residual"), rows, k_dim, n_dim, E, first, count,
-                               _take(y, bf16, (rows, n_dim), "y"), _take(z, bf16, (rows, n_w), "z"), _ptr(d_status),
+                               _take(y, bf16, (rows, n_dim), "y"), _take(z, bf16, (rows, n_w), "z"), _word(d_status),
                                _stream(stream))
     return _check(code, "ep_expert_gemm")
 
@@ -431,13 +449,12 @@ def ep_expert_gemm_backward(dy, x, w, z, expert_offset, num_tokens_per_expert, w
         k_dim = like_x.shape[1] if like_x is not None else 8
     assert n_w == (2 * n_dim if activation == EP_ACT_SWIGLU else n_dim)
     first, count = _blocks(expert_offset, num_tokens_per_expert, E)
-    assert workspace.is_contiguous()
     code = _lib.ep_expert_gemm_backward(
         _take(dy, bf16, (rows, n_dim), "dy"), _take(x, bf16, (rows, k_dim), "x"), _take(w, bf16, (E, n_w, k_dim), "w"),
         _take(z, bf16, (rows, n_w), "z"), activation, _take(row_weight, f32, (rows,), "row_weight"), rows, k_dim, n_dim,
         E, first, count, _take(dx, bf16, (rows, k_dim), "dx"), _take(dw, bf16, (E, n_w, k_dim), "dw"),
-        _take(dbias, f32, (E, n_w), "dbias"), _take(d_row_weight, f32, (rows,), "d_row_weight"), _ptr(workspace),
-        workspace.nbytes, _ptr(d_status), _stream(stream))
+        _take(dbias, f32, (E, n_w), "dbias"), _take(d_row_weight, f32, (rows,), "d_row_weight"),
+        _take_any(workspace, "workspace"), workspace.nbytes, _word(d_status), _stream(stream))
     return _check(code, "ep_expert_gemm_backward")
 
 
@@ -456,11 +473,11 @@ def ep_moe_few_tokens(x, topk_idx, topk_weights, w_up, w_down, workspace, out, d
     E, n_w, _ = w_up.shape
     inner = w_down.shape[2]
     assert n_w == (2 * inner if activation == EP_ACT_SWIGLU else inner)
-    assert workspace.is_contiguous()
     code = _lib.ep_moe_few_tokens(
         _take(x, bf16, (T, H), "x"), _take(topk_idx, torch.int64, (T, K), "topk_idx"),
         _take(topk_weights, f32, (T, K), "topk_weights"), _take(w_up, bf16, (E, n_w, H), "w_up"),
         _take(bias_up, f32, (E, n_w), "bias_up"), activation, _take(w_down, bf16, (E, H, inner), "w_down"),
         _take(bias_down, f32, (E, H), "bias_down"), _take(residual, bf16, (T, H), "residual"), T, H, inner, K, E,
-        _ptr(workspace), workspace.nbytes, _take(out, bf16, (T, H), "out"), _ptr(d_status), _stream(stream))
+        _take_any(workspace, "workspace"), workspace.nbytes, _take(out, bf16, (T, H), "out"), _word(d_status),
+        _stream(stream))
     return _check(code, "ep_moe_few_tokens")
