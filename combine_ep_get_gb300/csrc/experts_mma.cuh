@@ -75,7 +75,6 @@ struct Barriers {
     uint64_t tail_full[6], cleared[6];   // weight gradient: an expert's last stage
     uint32_t tmem;
     int64_t warp_rows[kThreads / 32];
-    int total_tiles;
     int warp_sum[kThreads / 32];
     int gave_up;                  // a wait of the epilogue ran out
     int completed;                // few tokens, down: tokens whose last expert this tile was

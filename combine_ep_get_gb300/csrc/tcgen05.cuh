@@ -10,8 +10,8 @@
 
 namespace epg {
 
-// Shared-memory address of the same offset in the pair's rank 0: bit 24 of a
-// shared::cluster address of one's own memory is the CTA's parity in a pair.
+// The CTA's rank in its cluster, and the address of the same shared-memory
+// offset in the CTA of another rank.
 __device__ __forceinline__ uint32_t cluster_ctarank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
