@@ -242,6 +242,12 @@ __device__ __forceinline__ int expert_rows(const int32_t* offset, const int32_t*
     return static_cast<int>(c);
 }
 
+// Sum over a warp of values below 2^42 each: 16 bits and the rest.
+__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
+    const int64_t low = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(v) & 0xffffu);
+    return (static_cast<int64_t>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(v >> 16))) << 16) + low;
+}
+
 // The experts' blocks into shared memory, by all threads of a block of
 // kThreads.  Blocks whose rows add up to more than there are overlap, and may
 // have more row tiles than the workspace and the grids are sized for (rows /
@@ -257,15 +263,12 @@ __device__ __forceinline__ bool expert_blocks(const int32_t* offset, const int32
         count[e] = n;
         mine += n;
     }
-    // EP_MAX_EXPERTS / kThreads blocks of less than 2^31 rows: 16 bits and the rest
-    const int64_t low = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(mine) & 0xffffu);
-    const int64_t high = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(mine >> 16));
-    if ((threadIdx.x & 31) == 0) warp_rows[threadIdx.x / 32] = (high << 16) + low;
+    // (few instructions: a short call's time is fetching them)
+    const int64_t warps_sum = warp_sum64(mine);
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) warp_rows[threadIdx.x / 32] = warps_sum;
     __syncthreads();
-    int64_t all = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) all += warp_rows[w];
-    if (all <= rows) return true;
+    if (warp_sum64(lane < kThreads / 32 ? warp_rows[lane] : 0) <= rows) return true;
     for (int e = threadIdx.x; e < E; e += kThreads) count[e] = 0;
     if (threadIdx.x == 0) atomicOr(status, EP_ERR_CAPACITY);
     __syncthreads();
