@@ -19,7 +19,8 @@ ALIGNMENT = 16      # rows of an expert's block start at a multiple of this
 
 
 class MoeLayer:
-    """Weights of E experts: w_up [E, 2 inner, H] (gate rows first), w_down [E, H, inner], bf16."""
+    """Weights of E experts: w_up [E, 2 inner, H] (gate rows first), w_down [E, H, inner], bf16.
+    A layer keeps its workspaces from call to call: its calls go to one stream at a time."""
 
     def __init__(self, w_up, w_down, ranks=1):
         self.w_up, self.w_down, self.ranks = w_up, w_down, ranks
