@@ -17,8 +17,12 @@
 //
 // What bounds it: with 512 rows an expert the summing warps (a block of 128
 // terms takes them ~700 of the ~1000 cycles, the MMAs 512): 64 experts x 512
-// rows, [4096, 7168] weights, 0.83 ms = 2.33 PFLOP/s (0.95-1.0 ms after seconds of
-// it, under the power limit).  Tried and slower: pairs of CTAs on 256 rows (278
+// rows, [4096, 7168] weights, 0.83 ms = 2.33 PFLOP/s (0.92-0.97 ms = 2.0-2.1 PFLOP/s
+// after seconds of it, under the power limit).  All 19 warps are launched with 96
+// registers: 64 sums spill a little (48-80 bytes), and a warp waits for each of
+// its four reads of tensor memory before it multiplies.  Not tried: registers
+// moved from the three issuing warps to these, the next read asked for ahead.
+// Tried and slower: pairs of CTAs on 256 rows (278
 // against 240 us on 16 experts x 512 rows; shared memory is freed, the summing
 // warps have as much to do and the pair waits for both), two-wide fp32
 // multiply-adds (their packing costs what they save).  With 32 rows an expert the weights bound it:

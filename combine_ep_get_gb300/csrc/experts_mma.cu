@@ -22,7 +22,7 @@
 // experts x 128 rows, [4096, 7168] weights each, 15.6 GB in 2.27-2.32 ms = 6.7-6.9
 // TB/s.  Above, the tensor cores: 4096 x 7168 x 7168 with bias, GELU and
 // residual 225-229 us, tensor pipe 86% busy (input gradient, nothing in its
-// epilogue: 94%); seconds of it run at the power limit, 1.63 PFLOP/s where a
+// epilogue: 92-93%); seconds of it run at the power limit, 1.63 PFLOP/s where a
 // library product of the same sizes without epilogue reaches 1.73.  With one
 // CTA a tile shared memory bounds it (a stage of 64 terms: 48 KB in, 48 KB
 // out, 768 cycles at 128 B each; measured ~800): pairs halve each CTA's share
@@ -33,8 +33,9 @@
 // rows by tensor map take up to 16 instructions a stage of 64 rows, ~90 cycles
 // each: 143 tokens over 10 experts 72 us, by copies 60; 6 tokens 17.4 against
 // 18.4).  Each CTA sorts topk_idx itself.  The up
-// product leaves h, rounded to bf16 for the down product's tensor cores and
-// expert by expert, so that its loads are boxes of rows and not gathers (143
+// product leaves h, rounded to bf16 for the down product's tensor cores (one
+// token, SWIGLU: the output is off by 2.3e-3 of its norm, 1.6e-3 of it its own
+// rounding) and expert by expert, so that its loads are boxes of rows and not gathers (143
 // tokens over 10 experts, 896 and 5208 features: 100 -> 72 us at that step), the down
 // product fp32 rows for each (token, slot); whichever tile completes a
 // token's last expert sums the token's rows, k ascending, so the order of the
@@ -571,9 +572,13 @@ cudaError_t launch_rows(const MmaArgs& a, cudaStream_t stream) {
 // Both operands are read as they lie, rows of the sum outermost (MN-major
 // descriptors), 128 n x 256 k a tile.  The last stage of an expert may hold
 // rows of the next one, or padding with anything in it: two warps clear those
-// rows of both operands in shared memory before the MMAs read them.  32
+// rows of both operands in shared memory before the MMAs read them.  The tensor
+// cores' fp32 additions truncate, which shows where one accumulator takes very
+// many rows: dw is off by 1.7e-3 of its norm (its rounding to bf16) up to 2^17
+// rows an expert, 2.0e-3 at 2^20, 5.2e-3 at 2^22, 1.9e-2 at 2^24 (a cluster of 8 on
+// the sum: 2.9e-3).  32
 // experts x 1024 rows, dw [4096, 7168] each: 1.22 ms, 1.58 PFLOP/s (8 experts x
-// 2048 rows: tensor pipe 90% busy); one CTA a tile 1.50 ms.  Few tiles and many
+// 2048 rows: tensor pipe 89% busy); one CTA a tile 1.50 ms.  Few tiles and many
 // rows: a cluster's CTAs each take a piece of the rows (kSplit, as above).
 // ---------------------------------------------------------------------------
 
