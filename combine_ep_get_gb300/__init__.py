@@ -18,6 +18,9 @@ _BINDING_NAMES = (
     "ep_expert_gemm", "ep_expert_gemm_backward", "ep_expert_gemm_backward_workspace_bytes",
     "ep_moe_few_tokens", "ep_moe_few_tokens_workspace_bytes", "EP_ACT_NONE", "EP_ACT_RELU", "EP_ACT_GELU",
     "EP_ACT_SILU", "EP_ACT_SWIGLU", "EP_FEW_MAX_TOKENS", "EP_FEW_MAX_TOPK",
+    "ep_route", "ep_balance_loss", "ep_balance_loss_workspace_bytes", "ep_route_backward", "EP_SCORE_SOFTMAX",
+    "EP_SCORE_SIGMOID", "EP_FP16", "EP_FP32", "ep_expert_gemm_w4", "ep_moe_few_tokens_w4",
+    "ep_moe_few_tokens_w4_workspace_bytes", "EP_W4_INT", "EP_W4_FP",
 )
 
 

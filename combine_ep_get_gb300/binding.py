@@ -32,6 +32,8 @@ EP_ERR_CUDA = 32
 EP_ERR_OUT_OF_BOUNDS = 64
 EP_BF16 = 0
 EP_FP8_E4M3 = 1
+EP_FP16 = 2
+EP_FP32 = 3
 EP_ACT_NONE = 0
 EP_ACT_RELU = 1
 EP_ACT_GELU = 2
@@ -39,6 +41,10 @@ EP_ACT_SILU = 3
 EP_ACT_SWIGLU = 4
 EP_FEW_MAX_TOKENS = 256
 EP_FEW_MAX_TOPK = 16
+EP_SCORE_SOFTMAX = 0
+EP_SCORE_SIGMOID = 1
+EP_W4_INT = 0
+EP_W4_FP = 1
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
@@ -112,6 +118,25 @@ _lib.ep_moe_few_tokens_workspace_bytes.argtypes = [_i, _i, _i, _i, _i]
 _lib.ep_moe_few_tokens.restype = ctypes.c_int32
 _lib.ep_moe_few_tokens.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp,
                                    ctypes.c_size_t, _vp, _vp, _vp]
+_f = ctypes.c_float
+_sz = ctypes.c_size_t
+_lib.ep_route.restype = ctypes.c_int32
+_lib.ep_route.argtypes = [_vp, _i, _i64, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _vp]
+_lib.ep_balance_loss_workspace_bytes.restype = _sz
+_lib.ep_balance_loss_workspace_bytes.argtypes = [_i, _i, _i]
+_lib.ep_balance_loss.restype = ctypes.c_int32
+_lib.ep_balance_loss.argtypes = [_vp, _i, _i64, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _vp, _sz, _vp, _vp]
+_lib.ep_route_backward.restype = ctypes.c_int32
+_lib.ep_route_backward.argtypes = [_vp, _i, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _vp, _i64,
+                                   _vp, _vp]
+_lib.ep_expert_gemm_w4.restype = ctypes.c_int32
+_lib.ep_expert_gemm_w4.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp, _vp, _i64, _i, _i, _i, _vp, _vp, _vp,
+                                   _vp, _vp]
+_lib.ep_moe_few_tokens_w4_workspace_bytes.restype = _sz
+_lib.ep_moe_few_tokens_w4_workspace_bytes.argtypes = [_i, _i, _i, _i, _i]
+_lib.ep_moe_few_tokens_w4.restype = ctypes.c_int32
+_lib.ep_moe_few_tokens_w4.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _vp, _vp, _vp, _i, _vp, _i, _i, _vp, _i,
+                                      _i, _i, _i, _i, _vp, _sz, _vp, _vp, _vp]
 
 
 def library():
@@ -481,3 +506,155 @@ def ep_moe_few_tokens(x, topk_idx, topk_weights, w_up, w_down, workspace, out, d
         _take_any(workspace, "workspace"), workspace.nbytes, _take(out, bf16, (T, H), "out"), _word(d_status),
         _stream(stream))
     return _check(code, "ep_moe_few_tokens")
+
+
+_ROW_TYPES = {torch.bfloat16: EP_BF16, torch.float16: EP_FP16, torch.float32: EP_FP32}
+
+
+def _rows_of(t, shape, name):
+    """Address, type and row stride of a matrix whose rows are contiguous (columns of a wider one will do)."""
+    assert t.dtype in _ROW_TYPES and t.shape == shape and (t.is_cuda or t.is_pinned()), \
+        "%s: a %s tensor of bf16, fp16 or fp32 on the GPU is wanted" % (name, tuple(shape))
+    rows, cols = shape
+    assert cols <= 1 or rows == 0 or t.stride(1) == 1, "%s: rows must be contiguous" % name
+    stride = t.stride(0) if rows > 1 else cols
+    assert stride >= cols, "%s: rows must not overlap" % name
+    return t.data_ptr(), _ROW_TYPES[t.dtype], stride
+
+
+def _mask(token_mask, T):
+    """Address of a token mask: bool or uint8, one byte a token."""
+    if token_mask is None:
+        return None
+    assert token_mask.dtype in (torch.bool, torch.uint8), "token_mask: bool or uint8 is wanted"
+    return _take(token_mask, token_mask.dtype, (T,), "token_mask")
+
+
+def _sequences(seq_offset):
+    """Address of sequences' offsets and how many sequences there are; None: one of all tokens."""
+    if seq_offset is None:
+        return None, 1
+    return _take(seq_offset, torch.int32, (seq_offset.numel(),), "seq_offset"), seq_offset.numel() - 1
+
+
+def ep_route(logits, topk_idx, topk_weights, d_status, score=EP_SCORE_SOFTMAX, bias=None, token_mask=None, num_groups=1,
+             topk_groups=None, normalize=True, scale=1.0, stream=None):
+    """Each token's top-k experts and their weights from the router's logits
+    (see the C header): logits [T, E] bf16, fp16 or fp32, its rows contiguous;
+    topk_idx int64 and topk_weights fp32 [T, K] are written.  What
+    ep_get_layout, the dispatch and the few-token layers take."""
+    T, E = logits.shape
+    K = topk_idx.shape[1]
+    address, kind, stride = _rows_of(logits, (T, E), "logits")
+    code = _lib.ep_route(address, kind, stride, _take(bias, torch.float32, (E,), "bias"), _mask(token_mask, T), T, E, K,
+                         score, num_groups, num_groups if topk_groups is None else topk_groups, 1 if normalize else 0,
+                         scale, _take(topk_idx, torch.int64, (T, K), "topk_idx"),
+                         _take(topk_weights, torch.float32, (T, K), "topk_weights"), _word(d_status), _stream(stream))
+    return _check(code, "ep_route")
+
+
+def ep_balance_loss_workspace_bytes(num_tokens, num_experts, num_sequences=1) -> int:
+    return int(_lib.ep_balance_loss_workspace_bytes(num_tokens, num_experts, num_sequences))
+
+
+def ep_balance_loss(logits, topk_idx, workspace, loss, load, d_status, score=EP_SCORE_SOFTMAX, token_mask=None,
+                    seq_offset=None, coeff=1.0, num_tokens_per_expert=None, stream=None):
+    """Balance loss of the router (see the C header), over all tokens or the
+    mean over the sequences that seq_offset (int32 [S + 1]) cuts: loss fp32 [1],
+    load fp32 [S, E] (its derivative by the normalised scores, for
+    ep_route_backward) and num_tokens_per_expert int32 [S, E] are written."""
+    f32 = torch.float32
+    T, E = logits.shape
+    K = topk_idx.shape[1]
+    address, kind, stride = _rows_of(logits, (T, E), "logits")
+    offsets, S = _sequences(seq_offset)
+    code = _lib.ep_balance_loss(address, kind, stride, _take(topk_idx, torch.int64, (T, K), "topk_idx"),
+                                _mask(token_mask, T), offsets, T, E, K, S, score, coeff, _take(loss, f32, (1,), "loss"),
+                                _take(load, f32, (S, E), "load"),
+                                _take(num_tokens_per_expert, torch.int32, (S, E), "num_tokens_per_expert"),
+                                _take_any(workspace, "workspace"), workspace.nbytes, _word(d_status), _stream(stream))
+    return _check(code, "ep_balance_loss")
+
+
+def ep_route_backward(logits, topk_idx, d_logits, d_status, d_topk_weights=None, load=None, d_loss=None,
+                      score=EP_SCORE_SOFTMAX, token_mask=None, seq_offset=None, normalize=True, scale=1.0, stream=None):
+    """Gradient of the router's logits through the top-k weights
+    (d_topk_weights fp32 [T, K]) and through the balance loss (load from
+    ep_balance_loss, d_loss fp32 [1]), each where it is given (see the C
+    header).  d_logits [T, E] of the logits' type is written."""
+    f32 = torch.float32
+    T, E = logits.shape
+    K = topk_idx.shape[1]
+    address, kind, stride = _rows_of(logits, (T, E), "logits")
+    out, out_kind, out_stride = _rows_of(d_logits, (T, E), "d_logits")
+    assert out_kind == kind, "d_logits: the logits' type is wanted"
+    offsets, S = _sequences(seq_offset)
+    code = _lib.ep_route_backward(address, kind, stride, _take(topk_idx, torch.int64, (T, K), "topk_idx"),
+                                  _mask(token_mask, T), _take(d_topk_weights, f32, (T, K), "d_topk_weights"),
+                                  _take(load, f32, (S, E), "load"), _take(d_loss, f32, (1,), "d_loss"), offsets, T, E, K,
+                                  S, score, 1 if normalize else 0, scale, out, out_stride, _word(d_status),
+                                  _stream(stream))
+    return _check(code, "ep_route_backward")
+
+
+def _weights4(w, sf, zero, depth, name):
+    """Addresses of 4-bit weights, their scales and zero points, the scales' type and the group."""
+    E, n_w, half = w.shape
+    assert half * 2 == depth and sf.dtype in (torch.bfloat16, torch.float32), "%s: codes [E, n_w, k / 2] are wanted" % name
+    groups = sf.shape[1]
+    assert groups > 0 and depth % groups == 0, "%s: scales [E, k / group, n_w] are wanted" % name
+    shape = (E, groups, n_w)
+    return (_take(w, torch.uint8, (E, n_w, half), name), _take(sf, sf.dtype, shape, name + "'s scales"),
+            _take(zero, sf.dtype, shape, name + "'s zero points"), EP_FP32 if sf.dtype is torch.float32 else EP_BF16,
+            depth // groups)
+
+
+def ep_expert_gemm_w4(x, w, w_sf, expert_offset, num_tokens_per_expert, y, d_status, w_zero=None, w_format=EP_W4_INT,
+                      bias=None, activation=EP_ACT_NONE, row_weight=None, residual=None, stream=None):
+    """ep_expert_gemm with 4-bit weights for the rows of a decode step (see the C
+    header): x [rows, k] bf16, w uint8 [E, n_w, k / 2] (two codes a byte, the
+    even k's in the low half), w_sf and w_zero [E, k / group, n_w] bf16 or
+    fp32, group 32, 64 or 128."""
+    bf16, f32 = torch.bfloat16, torch.float32
+    rows, k_dim = x.shape
+    E, n_w, _ = w.shape
+    gated = activation == EP_ACT_SWIGLU
+    assert not gated or n_w % 2 == 0
+    n_dim = n_w // 2 if gated else n_w
+    codes, sf, zero, sf_kind, group = _weights4(w, w_sf, w_zero, k_dim, "w")
+    first, count = _blocks(expert_offset, num_tokens_per_expert, E)
+    code = _lib.ep_expert_gemm_w4(_take(x, bf16, (rows, k_dim), "x"), codes, sf, zero, sf_kind, w_format, group,
+                                  _take(bias, f32, (E, n_w), "bias"), activation,
+                                  _take(row_weight, f32, (rows,), "row_weight"),
+                                  _take(residual, bf16, (rows, n_dim), "residual"), rows, k_dim, n_dim, E, first, count,
+                                  _take(y, bf16, (rows, n_dim), "y"), _word(d_status), _stream(stream))
+    return _check(code, "ep_expert_gemm_w4")
+
+
+def ep_moe_few_tokens_w4_workspace_bytes(num_tokens, num_topk, hidden, inner, num_experts) -> int:
+    return int(_lib.ep_moe_few_tokens_w4_workspace_bytes(num_tokens, num_topk, hidden, inner, num_experts))
+
+
+def ep_moe_few_tokens_w4(x, topk_idx, topk_weights, w_up, up_sf, w_down, down_sf, workspace, out, d_status, up_zero=None,
+                         down_zero=None, w_format=EP_W4_INT, bias_up=None, bias_down=None, residual=None,
+                         activation=EP_ACT_SWIGLU, stream=None):
+    """ep_moe_few_tokens with 4-bit weights (see the C header): w_up uint8
+    [E, n_w, H / 2], w_down uint8 [E, H, inner / 2], scales and zero points
+    [E, H / group, n_w] and [E, inner / group, H], bf16 or fp32."""
+    bf16, f32 = torch.bfloat16, torch.float32
+    T, H = x.shape
+    K = topk_idx.shape[1]
+    E, n_w, _ = w_up.shape
+    inner = w_down.shape[2] * 2
+    assert n_w == (2 * inner if activation == EP_ACT_SWIGLU else inner) and w_down.shape[:2] == (E, H)
+    assert up_sf.dtype is down_sf.dtype, "both scales are of one type"
+    up, sf_up, zero_up, sf_kind, up_group = _weights4(w_up, up_sf, up_zero, H, "w_up")
+    down, sf_down, zero_down, _, down_group = _weights4(w_down, down_sf, down_zero, inner, "w_down")
+    code = _lib.ep_moe_few_tokens_w4(
+        _take(x, bf16, (T, H), "x"), _take(topk_idx, torch.int64, (T, K), "topk_idx"),
+        _take(topk_weights, f32, (T, K), "topk_weights"), up, sf_up, zero_up, up_group,
+        _take(bias_up, f32, (E, n_w), "bias_up"), activation, down, sf_down, zero_down, down_group,
+        _take(bias_down, f32, (E, H), "bias_down"), sf_kind, w_format, _take(residual, bf16, (T, H), "residual"), T, H,
+        inner, K, E, _take_any(workspace, "workspace"), workspace.nbytes, _take(out, bf16, (T, H), "out"),
+        _word(d_status), _stream(stream))
+    return _check(code, "ep_moe_few_tokens_w4")

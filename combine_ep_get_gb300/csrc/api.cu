@@ -14,6 +14,8 @@
 
 #include "ep_internal.cuh"
 #include "experts.cuh"
+#include "experts_w4.cuh"
+#include "route.cuh"
 
 namespace epg {
 
@@ -893,6 +895,268 @@ ep_status_t ep_moe_few_tokens(const void* x, const int64_t* topk_idx, const floa
     p.status = d_status;
     return epg::launch_few_tokens(p, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? EP_OK
                                                                                            : EP_RET(EP_ERR_CUDA);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks shared by the router's calls.
+ep_status_t check_router(const void* logits, int dtype, int64_t row_stride, const int64_t* topk_idx, int T, int E, int K,
+                         int score, const int32_t* d_status) {
+    if (!d_status || T < 0 || E < 1 || K < 1 || K > E) return EP_RET(EP_ERR_INVALID_ARG);
+    if (dtype != EP_BF16 && dtype != EP_FP16 && dtype != EP_FP32) return EP_RET(EP_ERR_INVALID_ARG);
+    if (score != EP_SCORE_SOFTMAX && score != EP_SCORE_SIGMOID) return EP_RET(EP_ERR_INVALID_ARG);
+    if (E > EP_MAX_EXPERTS || K > EP_MAX_TOPK || static_cast<int64_t>(T) * E > INT32_MAX ||
+        static_cast<int64_t>(T) * K > INT32_MAX)
+        return EP_RET(EP_ERR_UNSUPPORTED);
+    const uintptr_t item = dtype == EP_FP32 ? 4 : 2;
+    if (row_stride < E || (T > 0 && (!logits || reinterpret_cast<uintptr_t>(logits) % item != 0)))
+        return EP_RET(EP_ERR_INVALID_ARG);
+    if (row_stride > (INT64_MAX / 8) / (T > 0 ? T : 1)) return EP_RET(EP_ERR_UNSUPPORTED);
+    if (T > 0 && !ok_ptr(topk_idx)) return EP_RET(EP_ERR_INVALID_ARG);
+    return EP_OK;
+}
+
+// Sequences of the loss: how many, and where they are.
+ep_status_t check_sequences(const int32_t* seq_offset, int S, int E) {
+    if (S < 1 || (!seq_offset && S != 1) || !aligned16(seq_offset)) return EP_RET(EP_ERR_INVALID_ARG);
+    if (static_cast<int64_t>(S) * E > INT32_MAX) return EP_RET(EP_ERR_UNSUPPORTED);
+    return EP_OK;
+}
+
+// 4-bit weights of n_w features: pointers, types and groups.
+ep_status_t check_w4(const void* w, const void* sf, const void* zero, int sf_dtype, int format, int group, int depth) {
+    if (sf_dtype != EP_BF16 && sf_dtype != EP_FP32) return EP_RET(EP_ERR_INVALID_ARG);
+    if (format != EP_W4_INT && (format != EP_W4_FP || zero)) return EP_RET(EP_ERR_INVALID_ARG);
+    if ((group != 32 && group != 64 && group != 128) || depth % group != 0) return EP_RET(EP_ERR_INVALID_ARG);
+    return ok_ptr(w) && ok_ptr(sf) && aligned16(zero) ? EP_OK : EP_RET(EP_ERR_INVALID_ARG);
+}
+
+epg::Weights4 weights4(const void* w, const void* sf, const void* zero, int sf_dtype, int format, int group) {
+    return {static_cast<const uint8_t*>(w), sf, zero, sf_dtype == EP_FP32 ? 1 : 0, format, group};
+}
+
+}  // namespace
+
+extern "C" {
+
+ep_status_t ep_route(const void* logits, int logits_dtype, int64_t row_stride, const float* bias,
+                     const uint8_t* token_mask, int T, int E, int K, int score, int num_groups, int topk_groups,
+                     int normalize, float scale, int64_t* topk_idx, float* topk_weights, int32_t* d_status,
+                     void* cuda_stream) {
+    EP_DEBUG("ep_route: T=%d E=%d K=%d dtype=%d stride=%lld score=%d groups=%d/%d%s%s%s", T, E, K, logits_dtype,
+             static_cast<long long>(row_stride), score, topk_groups, num_groups, bias ? " bias" : "",
+             token_mask ? " mask" : "", normalize ? " normalize" : "");
+    const ep_status_t s = check_router(logits, logits_dtype, row_stride, topk_idx, T, E, K, score, d_status);
+    if (s != EP_OK) return s;
+    if (num_groups < 1 || E % num_groups != 0 || topk_groups < 1 || topk_groups > num_groups)
+        return EP_RET(EP_ERR_INVALID_ARG);
+    if (num_groups > EP_MAX_GROUPS) return EP_RET(EP_ERR_UNSUPPORTED);
+    if (static_cast<int64_t>(topk_groups) * (E / num_groups) < K) return EP_RET(EP_ERR_INVALID_ARG);
+    if (!aligned16(bias) || (T > 0 && !ok_ptr(topk_weights))) return EP_RET(EP_ERR_INVALID_ARG);
+    if (T == 0) return EP_OK;
+    epg::RouteParams p{};
+    p.logits = logits;
+    p.dtype = logits_dtype;
+    p.row_stride = row_stride;
+    p.bias = bias;
+    p.token_mask = token_mask;
+    p.T = T;
+    p.E = E;
+    p.K = K;
+    p.score = score;
+    p.num_groups = num_groups;
+    p.topk_groups = topk_groups;
+    p.normalize = normalize ? 1 : 0;
+    p.scale = scale;
+    p.topk_idx = topk_idx;
+    p.topk_weights = topk_weights;
+    p.status = d_status;
+    return epg::launch_route(p, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? EP_OK : EP_RET(EP_ERR_CUDA);
+}
+
+size_t ep_balance_loss_workspace_bytes(int num_tokens, int num_experts, int num_sequences) {
+    if (num_tokens < 0 || num_experts < 1 || num_sequences < 1) return 16;
+    return epg::balance_workspace(num_tokens, num_experts, num_sequences).total;
+}
+
+ep_status_t ep_balance_loss(const void* logits, int logits_dtype, int64_t row_stride, const int64_t* topk_idx,
+                            const uint8_t* token_mask, const int32_t* seq_offset, int T, int E, int K, int S, int score,
+                            float coeff, float* loss, float* load, int32_t* num_tokens_per_expert, void* workspace,
+                            size_t ws_bytes, int32_t* d_status, void* cuda_stream) {
+    EP_DEBUG("ep_balance_loss: T=%d E=%d K=%d S=%d dtype=%d stride=%lld score=%d%s%s", T, E, K, S, logits_dtype,
+             static_cast<long long>(row_stride), score, token_mask ? " mask" : "", seq_offset ? " sequences" : "");
+    ep_status_t s = check_router(logits, logits_dtype, row_stride, topk_idx, T, E, K, score, d_status);
+    if (s != EP_OK) return s;
+    s = check_sequences(seq_offset, S, E);
+    if (s != EP_OK) return s;
+    if (!ok_ptr(loss) || !ok_ptr(load) || !aligned16(num_tokens_per_expert)) return EP_RET(EP_ERR_INVALID_ARG);
+    const epg::BalanceWorkspace b = epg::balance_workspace(T, E, S);
+    if (!ok_ptr(workspace) || ws_bytes < b.total) return EP_RET(EP_ERR_INVALID_ARG);
+    epg::BalanceParams p{};
+    p.logits = logits;
+    p.dtype = logits_dtype;
+    p.row_stride = row_stride;
+    p.topk_idx = topk_idx;
+    p.token_mask = token_mask;
+    p.seq_offset = seq_offset;
+    p.T = T;
+    p.E = E;
+    p.K = K;
+    p.S = S;
+    p.score = score;
+    p.coeff = coeff;
+    p.loss = loss;
+    p.load = load;
+    p.counts = num_tokens_per_expert;
+    char* ws = static_cast<char*>(workspace);
+    p.part_sum = reinterpret_cast<float*>(ws + b.off_sum);
+    p.part_count = reinterpret_cast<int32_t*>(ws + b.off_count);
+    p.part_tokens = reinterpret_cast<int32_t*>(ws + b.off_tokens);
+    p.part_loss = reinterpret_cast<float*>(ws + b.off_loss);
+    p.arrived = reinterpret_cast<uint32_t*>(ws + b.off_arrived);
+    p.tile_tokens = b.tile_tokens;
+    p.tiles = b.tiles;
+    p.status = d_status;
+    return epg::launch_balance_loss(p, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? EP_OK
+                                                                                             : EP_RET(EP_ERR_CUDA);
+}
+
+ep_status_t ep_route_backward(const void* logits, int logits_dtype, int64_t row_stride, const int64_t* topk_idx,
+                              const uint8_t* token_mask, const float* d_topk_weights, const float* load,
+                              const float* d_loss, const int32_t* seq_offset, int T, int E, int K, int S, int score,
+                              int normalize, float scale, void* d_logits, int64_t d_row_stride, int32_t* d_status,
+                              void* cuda_stream) {
+    EP_DEBUG("ep_route_backward: T=%d E=%d K=%d S=%d dtype=%d stride=%lld score=%d%s%s%s", T, E, K, S, logits_dtype,
+             static_cast<long long>(row_stride), score, d_topk_weights ? " weights" : "", load ? " loss" : "",
+             token_mask ? " mask" : "");
+    ep_status_t s = check_router(logits, logits_dtype, row_stride, topk_idx, T, E, K, score, d_status);
+    if (s != EP_OK) return s;
+    if (load) {
+        s = check_sequences(seq_offset, S, E);
+        if (s != EP_OK) return s;
+    }
+    const uintptr_t item = logits_dtype == EP_FP32 ? 4 : 2;
+    if (d_row_stride < E || reinterpret_cast<uintptr_t>(d_logits) % item != 0 || (T > 0 && !d_logits))
+        return EP_RET(EP_ERR_INVALID_ARG);
+    if (d_row_stride > (INT64_MAX / 8) / (T > 0 ? T : 1)) return EP_RET(EP_ERR_UNSUPPORTED);
+    if (!aligned16(d_topk_weights) || !aligned16(load) || !aligned16(d_loss) || !load != !d_loss)
+        return EP_RET(EP_ERR_INVALID_ARG);
+    if (T == 0) return EP_OK;
+    epg::RouteBackwardParams p{};
+    p.logits = logits;
+    p.dtype = logits_dtype;
+    p.row_stride = row_stride;
+    p.topk_idx = topk_idx;
+    p.token_mask = token_mask;
+    p.d_topk_weights = d_topk_weights;
+    p.load = load;
+    p.d_loss = d_loss;
+    p.seq_offset = load ? seq_offset : nullptr;
+    p.T = T;
+    p.E = E;
+    p.K = K;
+    p.S = load ? S : 1;
+    p.score = score;
+    p.normalize = normalize ? 1 : 0;
+    p.scale = scale;
+    p.d_logits = d_logits;
+    p.d_row_stride = d_row_stride;
+    p.status = d_status;
+    return epg::launch_route_backward(p, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? EP_OK
+                                                                                               : EP_RET(EP_ERR_CUDA);
+}
+
+ep_status_t ep_expert_gemm_w4(const void* x, const void* w, const void* w_sf, const void* w_zero, int sf_dtype,
+                              int w_format, int group, const float* bias, int activation, const float* row_weight,
+                              const void* residual, int64_t num_rows, int K, int N, int E,
+                              const int32_t* expert_offset, const int32_t* num_tokens_per_expert, void* y,
+                              int32_t* d_status, void* cuda_stream) {
+    EP_DEBUG("ep_expert_gemm_w4: rows=%lld K=%d N=%d E=%d format=%d group=%d sf=%d act=%d%s%s%s%s",
+             static_cast<long long>(num_rows), K, N, E, w_format, group, sf_dtype, activation, w_zero ? " zero" : "",
+             bias ? " bias" : "", row_weight ? " row_weight" : "", residual ? " residual" : "");
+    ep_status_t s = check_experts(num_rows, K, N, E, activation, expert_offset, num_tokens_per_expert, d_status);
+    if (s != EP_OK) return s;
+    s = check_w4(w, w_sf, w_zero, sf_dtype, w_format, group, K);
+    if (s != EP_OK) return s;
+    if (!aligned16(bias) || !aligned16(row_weight) || !aligned16(residual)) return EP_RET(EP_ERR_INVALID_ARG);
+    if (num_rows > 0 && (!ok_ptr(x) || !ok_ptr(y))) return EP_RET(EP_ERR_INVALID_ARG);
+    if (num_rows == 0) return EP_OK;
+    epg::ExpertGemmW4Params p{};
+    p.x = static_cast<const __nv_bfloat16*>(x);
+    p.w = weights4(w, w_sf, w_zero, sf_dtype, w_format, group);
+    p.bias = bias;
+    p.row_weight = row_weight;
+    p.residual = static_cast<const __nv_bfloat16*>(residual);
+    p.rows = num_rows;
+    p.K = K;
+    p.N = N;
+    p.Nw = activation == EP_ACT_SWIGLU ? 2 * N : N;
+    p.E = E;
+    p.act = activation;
+    p.expert_offset = expert_offset;
+    p.counts = num_tokens_per_expert;
+    p.y = static_cast<__nv_bfloat16*>(y);
+    p.status = d_status;
+    return epg::launch_expert_gemm_w4(p, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? EP_OK
+                                                                                               : EP_RET(EP_ERR_CUDA);
+}
+
+size_t ep_moe_few_tokens_w4_workspace_bytes(int num_tokens, int num_topk, int hidden, int inner, int num_experts) {
+    (void)num_experts;
+    if (num_tokens < 0 || num_topk < 1 || hidden < 1 || inner < 1) return 16;
+    return epg::few_w4_workspace(num_tokens, num_topk, hidden, inner).total;
+}
+
+ep_status_t ep_moe_few_tokens_w4(const void* x, const int64_t* topk_idx, const float* topk_weights, const void* w_up,
+                                 const void* up_sf, const void* up_zero, int up_group, const float* bias_up,
+                                 int activation, const void* w_down, const void* down_sf, const void* down_zero,
+                                 int down_group, const float* bias_down, int sf_dtype, int w_format,
+                                 const void* residual, int T, int H, int I, int K, int E, void* workspace,
+                                 size_t ws_bytes, void* out, int32_t* d_status, void* cuda_stream) {
+    EP_DEBUG("ep_moe_few_tokens_w4: T=%d H=%d I=%d K=%d E=%d format=%d groups=%d,%d sf=%d act=%d%s%s%s%s", T, H, I, K, E,
+             w_format, up_group, down_group, sf_dtype, activation, up_zero ? " zero" : "", bias_up ? " bias_up" : "",
+             bias_down ? " bias_down" : "", residual ? " residual" : "");
+    if (!d_status || T < 0 || H < 1 || I < 1 || K < 1 || E < 1) return EP_RET(EP_ERR_INVALID_ARG);
+    if (activation < EP_ACT_NONE || activation > EP_ACT_SWIGLU) return EP_RET(EP_ERR_INVALID_ARG);
+    if (T > EP_FEW_MAX_TOKENS || K > EP_FEW_MAX_TOPK || E > EP_MAX_EXPERTS || H > epg::kMaxExpertDim ||
+        I > epg::kMaxExpertDim)
+        return EP_RET(EP_ERR_UNSUPPORTED);
+    if (!up_zero != !down_zero) return EP_RET(EP_ERR_INVALID_ARG);
+    ep_status_t s = check_w4(w_up, up_sf, up_zero, sf_dtype, w_format, up_group, H);
+    if (s != EP_OK) return s;
+    s = check_w4(w_down, down_sf, down_zero, sf_dtype, w_format, down_group, I);
+    if (s != EP_OK) return s;
+    if (!aligned16(bias_up) || !aligned16(bias_down) || !aligned16(residual)) return EP_RET(EP_ERR_INVALID_ARG);
+    if (T > 0 && (!ok_ptr(x) || !ok_ptr(topk_idx) || !ok_ptr(topk_weights) || !ok_ptr(out)))
+        return EP_RET(EP_ERR_INVALID_ARG);
+    const epg::FewW4Workspace f = epg::few_w4_workspace(T, K, H, I);
+    if (!ok_ptr(workspace) || ws_bytes < f.total) return EP_RET(EP_ERR_INVALID_ARG);
+    if (T == 0) return EP_OK;
+    epg::FewTokensW4Params p{};
+    p.x = static_cast<const __nv_bfloat16*>(x);
+    p.topk_idx = topk_idx;
+    p.topk_weights = topk_weights;
+    p.up = weights4(w_up, up_sf, up_zero, sf_dtype, w_format, up_group);
+    p.bias_up = bias_up;
+    p.down = weights4(w_down, down_sf, down_zero, sf_dtype, w_format, down_group);
+    p.bias_down = bias_down;
+    p.residual = static_cast<const __nv_bfloat16*>(residual);
+    p.T = T;
+    p.H = H;
+    p.I = I;
+    p.Nw = activation == EP_ACT_SWIGLU ? 2 * I : I;
+    p.K = K;
+    p.E = E;
+    p.act = activation;
+    char* ws = static_cast<char*>(workspace);
+    p.h = reinterpret_cast<__nv_bfloat16*>(ws + f.off_h);
+    p.part = reinterpret_cast<float*>(ws + f.off_part);
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.status = d_status;
+    return epg::launch_few_tokens_w4(p, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? EP_OK
+                                                                                              : EP_RET(EP_ERR_CUDA);
 }
 
 const char* ep_status_string(int32_t status) {

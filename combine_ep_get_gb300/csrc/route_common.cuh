@@ -1,0 +1,84 @@
+// Device helpers of the router's kernels: a warp holds one token's row of
+// logits, expert j * 32 + lane in element j.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "route.cuh"
+
+namespace epg {
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+__device__ __forceinline__ void from_float(float* p, float v) { *p = v; }
+__device__ __forceinline__ void from_float(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void from_float(__half* p, float v) { *p = __float2half_rn(v); }
+
+constexpr float kInf = __builtin_huge_valf();
+
+// A row's logits; -inf behind the last expert.
+template <int kPer, typename L>
+__device__ __forceinline__ void load_row(const L* row, int E, int lane, float (&v)[kPer]) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int e = j * 32 + lane;
+        v[j] = e < E ? to_float(row[e]) : -kInf;
+    }
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// sigmoid(l) exp(-shift), shift <= 0: with the largest logit of a sum as shift
+// where that is far below zero, so that ratios of sigmoids stay exact where the
+// sigmoids themselves would be subnormal or zero.
+__device__ __forceinline__ float sigmoid_shifted(float l, float shift) {
+    const float e = expf(-fabsf(l));
+    const float top = l < 0.0f ? (shift == 0.0f ? e : expf(l - shift)) : 1.0f;
+    return top / (1.0f + e);
+}
+__device__ __forceinline__ float shift_of(float largest) { return largest < -16.0f ? largest : 0.0f; }
+
+// Sequence of token t: the last q with offset[q] <= t, -1 or S for tokens
+// before the first or behind the last one.
+__device__ __forceinline__ int sequence_of(const int32_t* offset, int S, int t) {
+    if (!offset) return 0;
+    int lo = -1, hi = S;     // offset[lo] <= t (or lo = -1), offset[hi + 1] > t (or hi = S)
+    while (lo < hi) {
+        const int mid = lo + (hi - lo + 1) / 2;
+        if (offset[mid] <= t)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+// Calls f with the type of the logits and the elements of a row in a lane.
+template <typename F>
+cudaError_t with_row_type(int dtype, int E, F f) {
+    const auto sized = [&](auto* type) {
+        if (E <= 32) return f(type, std::integral_constant<int, 1>());
+        if (E <= 64) return f(type, std::integral_constant<int, 2>());
+        if (E <= 128) return f(type, std::integral_constant<int, 4>());
+        if (E <= 256) return f(type, std::integral_constant<int, 8>());
+        if (E <= 512) return f(type, std::integral_constant<int, 16>());
+        if (E <= 1024) return f(type, std::integral_constant<int, 32>());
+        return f(type, std::integral_constant<int, 64>());
+    };
+    if (dtype == EP_FP32) return sized(static_cast<const float*>(nullptr));
+    if (dtype == EP_FP16) return sized(static_cast<const __half*>(nullptr));
+    return sized(static_cast<const __nv_bfloat16*>(nullptr));
+}
+
+}  // namespace epg

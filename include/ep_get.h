@@ -78,9 +78,12 @@ typedef int32_t ep_status_t;
  * -1 as "absent", like -1). */
 #define EP_ERR_OUT_OF_BOUNDS 64
 
-/* Payload types of the receive buffer. */
+/* Payload types of the receive buffer (EP_BF16, EP_FP8_E4M3), and types of the
+ * router's logits and of 4-bit weights' scales. */
 #define EP_BF16      0
 #define EP_FP8_E4M3  1
+#define EP_FP16      2
+#define EP_FP32      3
 
 /* Limits ("DeepEP V2 ElasticBuffer architecture", limits fragment), plus the
  * top-k width this library supports. */
@@ -490,6 +493,150 @@ ep_status_t ep_moe_few_tokens(const void* x, const int64_t* topk_idx, const floa
                               const float* bias_down, const void* residual, int num_tokens, int hidden,
                               int inner, int num_topk, int num_experts, void* workspace, size_t ws_bytes,
                               void* out, int32_t* d_status, void* cuda_stream);
+
+/*
+ * The router in front of the dispatch.  The pages take topk_idx and
+ * topk_weights as given; these calls make them from the router's logits, with
+ * the loss that balances the experts and the gradient of both.
+ *
+ * Scores of a token's logits l: SOFTMAX s = exp(l) / sum exp(l); SIGMOID
+ * s = 1 / (1 + exp(-l)).  Sums and exponentials are fp32.
+ */
+#define EP_SCORE_SOFTMAX 0
+#define EP_SCORE_SIGMOID 1
+#define EP_MAX_GROUPS    32
+
+/*
+ * Choice of the experts.  For every token t, with c = s + bias:
+ *   groups    with topk_groups < num_groups, experts fall into num_groups
+ *             groups of neighbours; the topk_groups groups with the largest
+ *             sum of their two largest c (of one, where there is one) stay;
+ *   topk_idx  the K experts of those with the largest c, the largest first;
+ *   topk_weights[t,k] = s of that expert, over the sum of the chosen ones' s
+ *             with `normalize`, times `scale`.
+ * Equal values go to the lower index.  The choice is that of c in 64 bits: where
+ * fp32 cannot tell neighbours apart, the token is chosen again in 64 (without a
+ * bias the choice goes by the logits, which order as the scores do).  An
+ * expert whose logit or c is -inf is closed: never chosen, and where too few
+ * are open the last slots hold -1 with weight 0.  NaN counts as the largest
+ * value, and shows in the weights.
+ *
+ * logits        [T, E] of logits_dtype EP_BF16, EP_FP16 or EP_FP32, row t at
+ *               t * row_stride elements (row_stride >= E: columns of a wider
+ *               matrix will do); aligned to its elements only.
+ * bias          fp32 [E] or NULL: moves the choice, not the weights.
+ * token_mask    uint8 [T] or NULL (any alignment): 0 = the token takes no part, its slots are
+ *               -1 with weight 0.
+ * num_groups    1, or a divisor of E up to EP_MAX_GROUPS; 1 <= topk_groups <= num_groups, with
+ *               topk_groups * E / num_groups >= K.
+ * topk_idx      int64 [T, K]; topk_weights fp32 [T, K].
+ * Limits: E <= EP_MAX_EXPERTS, K <= min(E, EP_MAX_TOPK), T * E and T * K below 2^31 (beyond: EP_ERR_UNSUPPORTED).
+ */
+ep_status_t ep_route(const void* logits, int logits_dtype, int64_t row_stride, const float* bias,
+                     const uint8_t* token_mask, int num_tokens, int num_experts, int num_topk, int score,
+                     int num_groups, int topk_groups, int normalize, float scale, int64_t* topk_idx,
+                     float* topk_weights, int32_t* d_status, void* cuda_stream);
+
+/* Bytes of device workspace ep_balance_loss needs (>= 16). */
+size_t ep_balance_loss_workspace_bytes(int num_tokens, int num_experts, int num_sequences);
+
+/*
+ * Balance loss, per-expert counts, and the loss's derivative by the scores.
+ * With p the scores over their sum, a sequence q of n tokens that take part,
+ * count[q,i] the slots of those tokens that name expert i:
+ *   load[q,i] = coeff * E * count[q,i] / (S * K * n^2)
+ *   loss      = sum over q, i of load[q,i] * (sum over q's tokens of p_i)
+ *             = coeff / S * sum over q, i of f[q,i] * P[q,i],
+ * f = E * count / (K * n), P the mean of p.  A sequence without tokens adds
+ * nothing; its load and counts are zero.  A token takes part unless it is
+ * masked, lies in no sequence or has only logits of -inf.  Sums are fp32, in an
+ * order that depends on the sizes alone.
+ *
+ * topk_idx      int64 [T, K]: the slots that count, -1 = none; entries outside
+ *               [-1, E) set EP_ERR_INVALID_INDEX and are skipped.
+ * seq_offset    int32 [S + 1]: sequence q is tokens seq_offset[q] .. up to
+ *               seq_offset[q+1]; NULL with S = 1: all tokens.  Offsets must
+ *               ascend from >= 0 to <= T; others set EP_ERR_INVALID_INDEX and
+ *               the results are of no use.
+ * loss          fp32 [1]; load fp32 [S, E]; num_tokens_per_expert int32 [S, E] or NULL.
+ * workspace     device scratch of ws_bytes >= ep_balance_loss_workspace_bytes(...); no
+ *               initialisation, garbage after.
+ * logits, token_mask, score and limits as ep_route; S * E below 2^31.
+ */
+ep_status_t ep_balance_loss(const void* logits, int logits_dtype, int64_t row_stride, const int64_t* topk_idx,
+                            const uint8_t* token_mask, const int32_t* seq_offset, int num_tokens, int num_experts,
+                            int num_topk, int num_sequences, int score, float coeff, float* loss, float* load,
+                            int32_t* num_tokens_per_expert, void* workspace, size_t ws_bytes, int32_t* d_status,
+                            void* cuda_stream);
+
+/*
+ * Gradient of the logits, through the weights (the choice and the bias have
+ * none) and through the loss:
+ *   d_logits[t] = sum over k of d_topk_weights[t,k] * d topk_weights[t,k] / d l
+ *               + *d_loss * sum over i of load[q,i] * d p_i / d l,  q = t's sequence.
+ * Every row is written: zero for masked tokens and those with only logits of -inf;
+ * tokens in no sequence have the first part alone.  An expert that two slots of a
+ * token name gets both slots' parts.
+ *
+ * logits .. scale  as in the forward calls; topk_idx as ep_route left it
+ *                  (entries outside [-1, E) set EP_ERR_INVALID_INDEX and are skipped).
+ * d_topk_weights   fp32 [T, K], or NULL: no first part.
+ * load, d_loss     fp32 [S, E] from ep_balance_loss and fp32 [1], or both
+ *                  NULL: no second part.  num_sequences, seq_offset as there.
+ * d_logits         [T, E] of logits_dtype, row t at t * d_row_stride elements; aligned
+ *                  to its elements only; may be logits itself.
+ */
+ep_status_t ep_route_backward(const void* logits, int logits_dtype, int64_t row_stride, const int64_t* topk_idx,
+                              const uint8_t* token_mask, const float* d_topk_weights, const float* load,
+                              const float* d_loss, const int32_t* seq_offset, int num_tokens, int num_experts,
+                              int num_topk, int num_sequences, int score, int normalize, float scale,
+                              void* d_logits, int64_t d_row_stride, int32_t* d_status, void* cuda_stream);
+
+/*
+ * Experts with 4-bit weights and group scales: W[e][f][k] =
+ *   EP_W4_INT  (u - zero) * scale, u = 0 .. 15, zero = 8 where there are no zero points
+ *   EP_W4_FP   scale * {0, 0.5, 1, 1.5, 2, 3, 4, 6}[u & 7], negative with u & 8 (E2M1)
+ * u = the code of (e, f, k): byte k / 2 of row (e, f), its low half for an even
+ * k.  scale and zero belong to `group` neighbouring k of one feature and lie
+ * group by group: element (e, k / group, f) of an array [E, k_dim / group, n_w].
+ */
+#define EP_W4_INT 0
+#define EP_W4_FP  1
+
+/*
+ * Experts' matrix product with 4-bit weights, for the rows of a decode step
+ * (few for each expert); one expert of one row is a matrix-vector product.
+ * Every argument but the weights as ep_expert_gemm, bf16 rows, accumulated in
+ * fp32; the weights' products are exact, scales are applied in fp32.
+ *
+ * w             uint8 [E, n_w, k_dim / 2].
+ * w_sf          scales [E, k_dim / group, n_w] of sf_dtype EP_BF16 or EP_FP32.
+ * w_zero        zero points, type and shape of w_sf, or NULL (EP_W4_INT only).
+ * group         32, 64 or 128, a divisor of k_dim; n_dim a multiple of 8.
+ */
+ep_status_t ep_expert_gemm_w4(const void* x, const void* w, const void* w_sf, const void* w_zero, int sf_dtype,
+                              int w_format, int group, const float* bias, int activation, const float* row_weight,
+                              const void* residual, int64_t num_rows, int k_dim, int n_dim, int num_experts,
+                              const int32_t* expert_offset, const int32_t* num_tokens_per_expert, void* y,
+                              int32_t* d_status, void* cuda_stream);
+
+/* Bytes of device workspace ep_moe_few_tokens_w4 needs (>= 16). */
+size_t ep_moe_few_tokens_w4_workspace_bytes(int num_tokens, int num_topk, int hidden, int inner, int num_experts);
+
+/*
+ * ep_moe_few_tokens with 4-bit weights: w_up [E, n_w, hidden / 2], w_down
+ * [E, hidden, inner / 2], scales and zero points [E, hidden / up_group, n_w]
+ * and [E, inner / down_group, hidden], both or neither with zero points.  Other
+ * arguments, results and limits as there; up_group must divide hidden and
+ * down_group inner.
+ */
+ep_status_t ep_moe_few_tokens_w4(const void* x, const int64_t* topk_idx, const float* topk_weights, const void* w_up,
+                                 const void* up_sf, const void* up_zero, int up_group, const float* bias_up,
+                                 int activation, const void* w_down, const void* down_sf, const void* down_zero,
+                                 int down_group, const float* bias_down, int sf_dtype, int w_format,
+                                 const void* residual, int num_tokens, int hidden, int inner, int num_topk,
+                                 int num_experts, void* workspace, size_t ws_bytes, void* out, int32_t* d_status,
+                                 void* cuda_stream);
 
 /*
  * Combined top-k weights ("DeepEP Symmetric Memory" section 9.2: combine
