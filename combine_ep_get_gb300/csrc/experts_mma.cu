@@ -69,8 +69,10 @@ EncodeFn encode_fn() {
 
 }  // namespace
 
-bool encode_map(CUtensorMap* map, bool fp8, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
-                const uint32_t* box) {
+namespace {
+
+bool encode(CUtensorMap* map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, int rank, const void* base,
+            const uint64_t* dims, const uint64_t* strides, const uint32_t* box) {
     const EncodeFn fn = encode_fn();
     if (!fn) return false;
     cuuint64_t d[5], s[5];
@@ -80,9 +82,21 @@ bool encode_map(CUtensorMap* map, bool fp8, int rank, const void* base, const ui
         b[i] = box[i];
         if (i + 1 < rank) s[i] = strides[i];
     }
-    return fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
-              const_cast<void*>(base), d, s, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    return fn(map, type, rank, const_cast<void*>(base), d, s, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+bool encode_map(CUtensorMap* map, bool fp8, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                const uint32_t* box) {
+    return encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                  CU_TENSOR_MAP_SWIZZLE_128B, rank, base, dims, strides, box);
+}
+bool encode_plain_map(CUtensorMap* map, bool fp32, int rank, const void* base, const uint64_t* dims,
+                      const uint64_t* strides, const uint32_t* box) {
+    return encode(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                  CU_TENSOR_MAP_SWIZZLE_NONE, rank, base, dims, strides, box);
 }
 
 namespace {

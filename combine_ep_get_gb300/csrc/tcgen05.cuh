@@ -121,6 +121,10 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* s
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
+// Arrives on `bar` when the thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
 __device__ __forceinline__ void copies_wait() {   // until at most kLeft groups are in flight
@@ -226,5 +230,8 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
 // dims and box from the innermost on; strides in bytes from the second.
 bool encode_map(CUtensorMap* map, bool fp8, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
                 const uint32_t* box);
+// The same for bf16 or fp32 elements whose boxes lie in shared memory as they are.
+bool encode_plain_map(CUtensorMap* map, bool fp32, int rank, const void* base, const uint64_t* dims,
+                      const uint64_t* strides, const uint32_t* box);
 
 }  // namespace epg
