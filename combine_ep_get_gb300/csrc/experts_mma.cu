@@ -93,6 +93,10 @@ bool encode_map(CUtensorMap* map, bool fp8, int rank, const void* base, const ui
     return encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                   CU_TENSOR_MAP_SWIZZLE_128B, rank, base, dims, strides, box);
 }
+bool encode_bytes_map(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                      const uint32_t* box) {
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_64B, rank, base, dims, strides, box);
+}
 bool encode_plain_map(CUtensorMap* map, bool fp32, int rank, const void* base, const uint64_t* dims,
                       const uint64_t* strides, const uint32_t* box) {
     return encode(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,

@@ -99,6 +99,11 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uin
             "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::
                 "r"(smem_addr(dst)), "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
 }
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z, int u) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::
+            "r"(smem_addr(dst)), "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(u) : "memory");
+}
 template <int kCtas>
 __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z, int u,
                                             int v) {
@@ -230,6 +235,9 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
 // dims and box from the innermost on; strides in bytes from the second.
 bool encode_map(CUtensorMap* map, bool fp8, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
                 const uint32_t* box);
+// The same for bytes, 64-byte swizzle.
+bool encode_bytes_map(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                      const uint32_t* box);
 // The same for bf16 or fp32 elements whose boxes lie in shared memory as they are.
 bool encode_plain_map(CUtensorMap* map, bool fp32, int rank, const void* base, const uint64_t* dims,
                       const uint64_t* strides, const uint32_t* box);

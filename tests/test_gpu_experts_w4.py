@@ -314,6 +314,24 @@ def test_calls_see_what_the_stream_wrote_before():
     assert all(torch.equal(alone[i], o) for i, o in got)
 
 
+def test_many_calls_in_flight():
+    """A long queue of calls, so that the down product's kernel starts on the SMs that the up product leaves free and
+    waits there with its first weights loaded: no wait runs out, and every call's answer is the same."""
+    T, H, I, E, K = 1, 7168, 2048, 12, 8
+    d = make_few(T, H, I, E, K, "swiglu")
+    d["idx"] = torch.arange(K, device="cuda")[None, :].contiguous()
+    from gpu_path import B
+    ws = torch.empty(B.ep_moe_few_tokens_w4_workspace_bytes(T, K, H, I, E), dtype=torch.uint8, device="cuda")
+    st, outs = status(), [torch.empty_like(d["x"]) for _ in range(40)]
+    want = run_few(d, "swiglu", "int").clone()
+    torch.cuda.synchronize()
+    for out in outs:
+        run_few(d, "swiglu", "int", ws, out, st=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    assert all(torch.equal(out, want) for out in outs)
+
+
 def test_rows_of_a_dispatch():
     """Router, layout, dispatch, both products, combine: the rows path against the few-token call."""
     from gpu_path import B
