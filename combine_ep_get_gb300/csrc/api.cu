@@ -907,7 +907,7 @@ ep_status_t check_router(const void* logits, int dtype, int64_t row_stride, cons
     if (!d_status || T < 0 || E < 1 || K < 1 || K > E) return EP_RET(EP_ERR_INVALID_ARG);
     if (dtype != EP_BF16 && dtype != EP_FP16 && dtype != EP_FP32) return EP_RET(EP_ERR_INVALID_ARG);
     if (score != EP_SCORE_SOFTMAX && score != EP_SCORE_SIGMOID) return EP_RET(EP_ERR_INVALID_ARG);
-    if (E > EP_MAX_EXPERTS || K > EP_MAX_TOPK || static_cast<int64_t>(T) * E > INT32_MAX ||
+    if (T > (1 << 30) || E > EP_MAX_EXPERTS || K > EP_MAX_TOPK || static_cast<int64_t>(T) * E > INT32_MAX ||
         static_cast<int64_t>(T) * K > INT32_MAX)
         return EP_RET(EP_ERR_UNSUPPORTED);
     const uintptr_t item = dtype == EP_FP32 ? 4 : 2;

@@ -9,6 +9,7 @@
 // ends; the second adds the pieces of each sequence in their order, 32 experts
 // a CTA, and its last CTA the sequences' parts.  Every sum runs in an order
 // that only the sizes decide.
+#include <algorithm>
 #include <type_traits>
 
 #include "route_common.cuh"
@@ -21,32 +22,40 @@ constexpr int kThreads = kBalanceWarps * 32;
 
 __device__ __forceinline__ int clamped(int v, int n) { return v < 0 ? 0 : v > n ? n : v; }
 
-// Scores of a row as parts of their sum, with the largest logit and (softmax)
-// the sum of exponentials; false for a row whose logits are all -inf.
+// Scores of a row as parts of their sum, for a sigmoid 1 - score too; false for a row whose logits are all -inf.
+// *base and *inverse: a softmax's q is 2^(log2(e) l - base) * inverse; a sigmoid's base is its shift.  Exponentials and reciprocals are the hardware's
+// (sigmoid_fast): exact ones took half of the kernels' instructions.
 template <int kPer>
-__device__ __forceinline__ bool normalised_scores(const float (&l)[kPer], int score, float (&q)[kPer], float& largest,
-                                                  float& sum) {
-    largest = -kInf;
-    bool any = false;      // (a NaN is something, and stays one)
+__device__ __forceinline__ bool normalised_scores(const float (&l)[kPer], int score, float (&q)[kPer], float (&rest)[kPer],
+                                                  float* base, float* inverse) {
+    float largest = l[0];
+    bool nan = l[0] != l[0];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
+    for (int j = 1; j < kPer; ++j) {
         largest = fmaxf(largest, l[j]);
-        any |= l[j] != -kInf;
+        nan |= l[j] != l[j];
     }
-    if (!__any_sync(0xffffffffu, any)) return false;
     largest = warp_max(largest);
-    sum = 0.0f;
+    // (a NaN is something, and stays one)
+    if (largest == -kInf && !__any_sync(0xffffffffu, nan)) return false;
+    float sum = 0.0f;
+    *base = score == EP_SCORE_SOFTMAX ? largest * kLog2E : shift_of(largest);
     if (score == EP_SCORE_SOFTMAX) {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) sum += q[j] = expf(l[j] - largest);
+        for (int j = 0; j < kPer; ++j) sum += q[j] = exp2_approx(fmaf(l[j], kLog2E, -*base));
+    } else if (*base == 0.0f) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) sum += q[j] = sigmoid_fast(l[j], &rest[j]);
     } else {
-        const float shift = shift_of(largest);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) sum += q[j] = sigmoid_shifted(l[j], shift);
+        for (int j = 0; j < kPer; ++j) {
+            sum += q[j] = sigmoid_shifted(l[j], *base);
+            rest[j] = sigmoid_shifted(-l[j], 0.0f);
+        }
     }
-    sum = warp_sum(sum);
+    *inverse = 1.0f / warp_sum(sum);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) q[j] /= sum;
+    for (int j = 0; j < kPer; ++j) q[j] *= *inverse;
     return true;
 }
 
@@ -60,7 +69,7 @@ __global__ void __launch_bounds__(kThreads) balance_sums_kernel(const BalancePar
     pdl_launch_dependents();
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.arrived = 0;
     const int begin = blockIdx.x * p.tile_tokens, end = min(p.T, begin + p.tile_tokens);
-    int q = p.seq_offset ? sequence_of(p.seq_offset, p.S, begin) : 0;
+    int q = warp_sequence_of(p.seq_offset, p.S, begin, lane);
     for (int at = begin; at < end;) {
         int stop = end;
         if (p.seq_offset) {
@@ -79,11 +88,21 @@ __global__ void __launch_bounds__(kThreads) balance_sums_kernel(const BalancePar
         int live = 0;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) sum[j] = 0.0f;
+        constexpr bool kAhead = kPer <= 16;      // the next row is asked for before this one's work
+        const L* const logits = static_cast<const L*>(p.logits);
+        float ahead[kPer];
+        if (kAhead && at + warp < stop) load_row(logits + (at + warp) * p.row_stride, p.E, lane, ahead);
         for (int t = at + warp; t < stop; t += kBalanceWarps) {
+            float l[kPer], s[kPer], rest[kPer], base, inverse;
+            if constexpr (kAhead) {
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) l[j] = ahead[j];
+                if (t + kBalanceWarps < stop) load_row(logits + (t + kBalanceWarps) * p.row_stride, p.E, lane, ahead);
+            } else {
+                load_row(logits + t * p.row_stride, p.E, lane, l);
+            }
             if (p.token_mask && p.token_mask[t] == 0) continue;
-            float l[kPer], s[kPer], largest, all;
-            load_row(static_cast<const L*>(p.logits) + t * p.row_stride, p.E, lane, l);
-            if (!normalised_scores(l, p.score, s, largest, all)) continue;
+            if (!normalised_scores(l, p.score, s, rest, &base, &inverse)) continue;
             ++live;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) sum[j] += s[j];
@@ -188,105 +207,123 @@ __global__ void __launch_bounds__(kParts * 32) balance_loss_kernel(const Balance
 
 template <typename L, int kPer>
 __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteBackwardParams p) {
-    extern __shared__ float smem[];      // [kBalanceWarps][E]: the chosen experts' parts of a row
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    float* const chosen = smem + warp * p.E;
     pdl_wait();
     pdl_launch_dependents();
     const bool softmax = p.score == EP_SCORE_SOFTMAX;
     const float d_loss = p.load ? *p.d_loss : 0.0f;
-    for (int e = lane; e < p.E; e += 32) chosen[e] = 0.0f;
-    __syncwarp();
-    for (int t = blockIdx.x * kBalanceWarps + warp; t < p.T; t += gridDim.x * kBalanceWarps) {
+    constexpr bool kAhead = kPer <= 16;      // the next row is asked for before this one's work
+    const int step = gridDim.x * kBalanceWarps, first = blockIdx.x * kBalanceWarps + warp;
+    const L* const logits = static_cast<const L*>(p.logits);
+    float ahead[kPer], load[kPer];
+    int load_of = -1;        // the sequence whose derivatives `load` holds
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) load[j] = 0.0f;
+    if (kAhead && first < p.T) load_row(logits + first * p.row_stride, p.E, lane, ahead);
+    for (int t = first; t < p.T; t += step) {
+        const L* const row = logits + t * p.row_stride;
         L* const out = static_cast<L*>(p.d_logits) + t * p.d_row_stride;
-        const L* const row = static_cast<const L*>(p.logits) + t * p.row_stride;
-        float l[kPer], s[kPer], d[kPer], largest = 0.0f, total = 1.0f;
-        bool live = !p.token_mask || p.token_mask[t] != 0;
-        if (live) {
+        float l[kPer], s[kPer], rest[kPer], d[kPer], base, inverse;
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) l[j] = ahead[j];
+            if (t < p.T - step) load_row(row + step * p.row_stride, p.E, lane, ahead);
+        } else {
             load_row(row, p.E, lane, l);
-            live = normalised_scores(l, p.score, s, largest, total);
         }
-        if (!live) {
+        // the token's slots, a lane each, with their experts' logits
+        int e = -1;
+        float g = 0.0f, v = -kInf;
+        if (p.d_topk_weights && lane < p.K) {
+            const int64_t at = static_cast<int64_t>(t) * p.K + lane, named = p.topk_idx[at];
+            if (named >= 0 && named < p.E) {
+                e = static_cast<int>(named);
+                g = p.d_topk_weights[at] * p.scale;
+                v = to_float(row[e]);
+            } else if (named != -1) {
+                atomicOr(p.status, EP_ERR_INVALID_INDEX);
+            }
+        }
+        if ((p.token_mask && p.token_mask[t] == 0) || !normalised_scores(l, p.score, s, rest, &base, &inverse)) {
 #pragma unroll
             for (int j = 0; j < kPer; ++j)
                 if (j * 32 + lane < p.E) from_float(out + j * 32 + lane, 0.0f);
             continue;
         }
         // through the loss
+        float mean = 0.0f;
+        const int q = p.load ? warp_sequence_of(p.seq_offset, p.S, t, lane) : -1;
+        const bool in_loss = q >= 0 && q < p.S;
+        if (in_loss) {
+            if (q != load_of) {
+                load_of = q;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) d[j] = 0.0f;
-        const int q = p.load ? sequence_of(p.seq_offset, p.S, t) : -1;
-        if (q >= 0 && q < p.S) {
-            float mean = 0.0f;
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                const int e = j * 32 + lane;
-                if (e < p.E) d[j] = p.load[static_cast<int64_t>(q) * p.E + e] * d_loss;
-                mean += d[j] * s[j];
+                for (int j = 0; j < kPer; ++j)
+                    load[j] = j * 32 + lane < p.E ? p.load[static_cast<int64_t>(q) * p.E + j * 32 + lane] * d_loss : 0.0f;
             }
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) mean += load[j] * s[j];
             mean = warp_sum(mean);
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) d[j] = s[j] * (d[j] - mean);
-        }
-        // through the weights, by the lane of each slot
-        float spread = 0.0f;      // softmax without normalisation: every expert's share of the chosen ones' sum
-        if (p.d_topk_weights) {
-            int e = -1;
-            float g = 0.0f, v = -kInf;
-            if (lane < p.K) {
-                const int64_t at = static_cast<int64_t>(t) * p.K + lane;
-                const int64_t named = p.topk_idx[at];
-                if (named >= 0 && named < p.E) {
-                    e = static_cast<int>(named);
-                    g = p.d_topk_weights[at] * p.scale;
-                    v = to_float(row[e]);
-                } else if (named != -1) {
-                    atomicOr(p.status, EP_ERR_INVALID_INDEX);
-                }
+            for (int j = 0; j < kPer; ++j) {
+                d[j] = s[j] * (load[j] - mean);
+                if (!softmax) d[j] *= rest[j];
             }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) d[j] = 0.0f;
+        }
+        // Through the weights: the slots' lanes know their experts' whole derivative, and store it after the row's.
+        float r = 0.0f;
+        if (p.d_topk_weights) {
             const float top = warp_max(v);
-            float r = 0.0f;
             if (p.normalize) {
-                const float u = v == -kInf ? 0.0f : softmax ? expf(v - top) : sigmoid_shifted(v, shift_of(top));
+                const float u = v == -kInf ? 0.0f : softmax ? exp2_approx((v - top) * kLog2E) : sigmoid_shifted(v, shift_of(top));
                 const float sum = warp_sum(u), part = u == 0.0f ? 0.0f : u / sum;
                 r = part * (g - warp_sum(part * g));
-            } else if (softmax) {
-                r = v == -kInf ? 0.0f : expf(v - largest) / total * g;
-                spread = warp_sum(r);
             } else if (v != -kInf) {
-                r = sigmoid_shifted(v, 0.0f) * g;
+                r = (softmax ? exp2_approx(fmaf(v, kLog2E, -base)) * inverse : sigmoid_shifted(v, 0.0f)) * g;
+            }
+            if (softmax && !p.normalize) {
+                // every expert loses its share of the chosen ones' sum
+                const float spread = warp_sum(r);
+                mean += spread;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) d[j] -= s[j] * spread;
             }
             if (!softmax && e >= 0) r *= sigmoid_shifted(-v, 0.0f);
-            // an expert that is named twice gets both parts, in the order of the slots
-            float sum = 0.0f;
-            bool first = true;
-            for (int k = 0; k < p.K; ++k) {
-                const int ek = __shfl_sync(0xffffffffu, e, k);
-                const float rk = __shfl_sync(0xffffffffu, r, k);
-                if (ek == e) {
-                    sum += rk;
-                    if (k < lane) first = false;
-                }
-            }
-            if (e >= 0 && first) chosen[e] = sum;
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                const int ej = j * 32 + lane;
-                if (ej < p.E) {
-                    const float c = chosen[ej];
-                    d[j] = softmax ? d[j] + c - s[j] * spread : sigmoid_shifted(-l[j], 0.0f) * d[j] + c;
-                    if (c != 0.0f || c != c) chosen[ej] = 0.0f;
-                }
-            }
-            __syncwarp();
-        } else if (!softmax) {
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) d[j] *= sigmoid_shifted(-l[j], 0.0f);
         }
 #pragma unroll
         for (int j = 0; j < kPer; ++j)
             if (j * 32 + lane < p.E) from_float(out + j * 32 + lane, d[j]);
+        if (p.d_topk_weights) {
+            // an expert that is named twice gets both parts, in the order of the slots, from the first one's lane
+            const unsigned same = __match_any_sync(0xffffffffu, e >= 0 ? e : -1 - lane);
+            if (__any_sync(0xffffffffu, same & (same - 1))) {
+                float sum = 0.0f;
+                for (int k = 0; k < p.K; ++k) {
+                    const float other = __shfl_sync(0xffffffffu, r, k);
+                    if (same >> k & 1) sum += other;
+                }
+                r = sum;
+            }
+            __syncwarp();     // after the row's stores
+            if (e >= 0 && (same & ((1u << lane) - 1)) == 0) {
+                float own = 0.0f;
+                if (v == -kInf) {
+                    own = 0.0f;
+                } else if (softmax) {
+                    const float s_e = exp2_approx(fmaf(v, kLog2E, -base)) * inverse;
+                    own = s_e * ((in_loss ? p.load[static_cast<int64_t>(q) * p.E + e] * d_loss : 0.0f) - mean);
+                } else if (in_loss) {
+                    float rest_e;
+                    const float s_e = (base == 0.0f ? sigmoid_fast(v, &rest_e) : sigmoid_shifted(v, base)) * inverse;
+                    if (base != 0.0f) rest_e = sigmoid_shifted(-v, 0.0f);
+                    own = s_e * (p.load[static_cast<int64_t>(q) * p.E + e] * d_loss - mean) * rest_e;
+                }
+                from_float(out + e, own + r);
+            }
+        }
     }
 }
 
@@ -313,14 +350,9 @@ cudaError_t launch_route_backward(const RouteBackwardParams& p, cudaStream_t str
     return with_row_type(p.dtype, p.E, [&](auto* type, auto per) {
         using L = std::remove_const_t<std::remove_pointer_t<decltype(type)>>;
         const auto kernel = route_backward_kernel<L, decltype(per)::value>;
-        const size_t smem = static_cast<size_t>(kBalanceWarps) * p.E * 4;
-        if (smem > 48 * 1024) {
-            const cudaError_t err =
-                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-            if (err != cudaSuccess) return err;
-        }
-        const int blocks = (p.T + kBalanceWarps - 1) / kBalanceWarps;
-        return launch_pdl(kernel, dim3(blocks), dim3(kThreads), smem, stream, p);
+        // (many tokens: warps that go on to another token have asked for its row)
+        const int blocks = std::min((p.T + kBalanceWarps - 1) / kBalanceWarps, device_info().num_sms * 8);
+        return launch_pdl(kernel, dim3(blocks), dim3(kThreads), 0, stream, p);
     });
 }
 

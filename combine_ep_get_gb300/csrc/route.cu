@@ -5,6 +5,13 @@
 // whose rounding may turn two neighbours round: where two of the values that
 // decide the choice lie closer than that rounding reaches and do not come
 // from the same logit and bias, the token is chosen once more by c in 64 bits.
+//
+// The choice.  The K-th largest of the lanes' largest values bounds the K-th
+// largest value from below, and few values reach it: they go to a list, whose
+// members find their places by comparing themselves with one another.  About
+// 200 instructions a token of 256 experts bound the kernel for many tokens; K
+// rounds of a warp's maximum over what is left took 400.
+#include <algorithm>
 #include <type_traits>
 
 #include "route_common.cuh"
@@ -14,16 +21,17 @@ namespace epg {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr uint32_t kClosed = 0x007fffffu;      // key of -inf; a closed expert's is this or less
 
 // Unsigned keys that order as the values do: NaN above all, then +inf, down to
-// -inf; 0 (below every value) is left for closed experts.
+// -inf.
 __device__ __forceinline__ uint32_t key_of(float v) {
-    const uint32_t b = __float_as_uint(v + 0.0f);    // -0 as +0
-    return v != v ? 0xffffffffu : (b & 0x80000000u ? ~b : b | 0x80000000u);
+    const uint32_t b = __float_as_uint(v + 0.0f);    // -0 as +0, any NaN as the positive one
+    return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ uint64_t key_of(double v) {
     const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
-    return v != v ? ~0ull : (b >> 63 ? ~b : b | (1ull << 63));
+    return v != v ? ~0ull : v == -kInf ? 0ull : (b >> 63 ? ~b : b | (1ull << 63));
 }
 __device__ __forceinline__ uint32_t key_max(uint32_t k) { return __reduce_max_sync(0xffffffffu, k); }
 __device__ __forceinline__ uint64_t key_max(uint64_t k) {
@@ -38,105 +46,217 @@ __device__ __forceinline__ float value_of(uint32_t k) {
 // How far c in fp32 may lie from c: the score is good to a few units of the last place, the sum to half a one.
 __device__ __forceinline__ float reach(float c) { return 5e-7f * fmaxf(1.0f, fabsf(c)); }
 
-template <typename L, int kPer, bool kByScore>
-struct Chooser {
-    const RouteParams& p;
-    const L* row;
-    int lane;
-    float l[kPer];
+// What a warp's choice needs in shared memory.
+struct Lists {
+    uint64_t found[32];
+    int16_t ranked[33];
+};
 
-    // The K largest keys, equal ones by the lower index: lane k gets the k-th expert, or -1.
-    // margin: the least distance between neighbours of the first K + 1 that are not the same inputs.
-    template <typename Key>
-    __device__ __forceinline__ int choose(Key (&key)[kPer], bool* close) {
-        int mine = -1;
-        Key before = 0;
-        int chosen_before = -1;
-        for (int k = 0; k <= p.K; ++k) {
-            if (k == p.K && !(kByScore && sizeof(Key) == 4)) break;
-            Key best = 0;
-            int at = 0x7fffffff;
+// The K largest keys, equal ones by the lower index, one round a slot: lane k gets the k-th expert, or -1.
+template <int kPer, typename Key>
+__device__ __forceinline__ int choose_in_rounds(Key (&key)[kPer], int K, Key closed, int lane) {
+    int mine = -1;
+    for (int k = 0; k < K; ++k) {
+        Key best = closed;
+        int at = 0x7fffffff;
 #pragma unroll
-            for (int j = 0; j < kPer; ++j)
-                if (key[j] > best) {
-                    best = key[j];
-                    at = j * 32 + lane;
-                }
-            const Key top = key_max(best);
-            if (top == 0) break;     // nothing is open any more
-            const int e = __reduce_min_sync(0xffffffffu, best == top ? at : 0x7fffffff);
-            if constexpr (kByScore && sizeof(Key) == 4) {
-                if (k > 0) {
-                    const float a = value_of(before), b = value_of(top);
-                    if (a - b <= reach(a) + reach(b) && before != 0xffffffffu && !same_inputs(chosen_before, e)) *close = true;
-                }
+        for (int j = 0; j < kPer; ++j)
+            if (key[j] > best) {
+                best = key[j];
+                at = j * 32 + lane;
             }
-            if (k == p.K) break;
+        const Key top = key_max(best);
+        if (top == closed) break;     // nothing is open any more
+        const int e = __reduce_min_sync(0xffffffffu, best == top ? at : 0x7fffffff);
 #pragma unroll
-            for (int j = 0; j < kPer; ++j)
-                if (e == j * 32 + lane) key[j] = 0;
-            if (lane == k) mine = e;
-            before = top;
-            chosen_before = e;
-        }
-        return mine;
+        for (int j = 0; j < kPer; ++j)
+            if (e == j * 32 + lane) key[j] = closed;
+        if (lane == k) mine = e;
     }
-    __device__ __forceinline__ bool same_inputs(int a, int b) const {
-        return to_float(row[a]) == to_float(row[b]) && (!p.bias || p.bias[a] == p.bias[b]);
-    }
+    return mine;
+}
 
-    // Closes the experts of all but the topk_groups best groups.  `c` is in shared memory by expert.
-    template <typename V>
-    __device__ __forceinline__ void keep_groups(V* c, bool* close) {
-        const int G = p.num_groups, size = p.E / G;
-        V score = 0;
-        bool open = false;
-        if (lane < G) {
-            V first = -kInf, second = -kInf;
-            for (int i = 0; i < size; ++i) {
-                const V v = c[lane * size + i];
-                if (v != v || v > first) {
-                    second = first;
-                    first = v;
-                } else if (v > second) {
-                    second = v;
-                }
-            }
-            open = first != -kInf;
-            score = second != -kInf ? first + second : first;
+// The same by a list: some lane for each of the K experts has its slot in *place and its key in *mine (the others'
+// places are K or more).  Returns the expert; with `ranked`, list->ranked has the first K + 1 in order, -1 after the last.
+template <int kPer>
+__device__ __forceinline__ int choose(uint32_t (&key)[kPer], int K, bool ranked, Lists* list, int lane, int* place,
+                                      uint32_t* mine) {
+    const int wanted = K + (ranked ? 1 : 0);
+    uint32_t best = key[0];
+#pragma unroll
+    for (int j = 1; j < kPer; ++j) best = max(best, key[j]);
+    uint32_t least = kClosed + 1;
+    for (int k = 0; k < wanted; ++k) {
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        if (top <= kClosed) {
+            least = kClosed + 1;
+            break;
         }
-        // rank among the groups, equal ones by the lower index; closed groups come last
+        least = top;
+        if (best == top) best = 0;
+    }
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const unsigned there = __ballot_sync(0xffffffffu, key[j] >= least);
+        const int at = n + __popc(there & ((1u << lane) - 1));
+        if (key[j] >= least && at < 32) list->found[at] = static_cast<uint64_t>(key[j]) << 32 | (0xffffffffu - (j * 32 + lane));
+        n += __popc(there);
+    }
+    __syncwarp();
+    int e = -1;
+    if (n <= 32) {
+        const uint64_t own = lane < n ? list->found[lane] : 0;
         int rank = 0;
-        V below = -kInf;
-        for (int g = 0; g < G; ++g) {
-            const V other = __shfl_sync(0xffffffffu, score, g);
-            const bool other_open = __shfl_sync(0xffffffffu, open ? 1 : 0, g) != 0;
-            if (!other_open || g == lane) continue;
-            const bool higher = key_of(other) > key_of(score) || (key_of(other) == key_of(score) && g < lane);
-            if (!open || higher) ++rank;
-            else if (other > below) below = other;
+        for (int i = 0; i < n; ++i) rank += list->found[i] > own;
+        *place = lane < n ? rank : wanted;
+        *mine = static_cast<uint32_t>(own >> 32);
+        e = lane < n ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(own)) : -1;
+    } else {
+        // many equal values, or few lanes with open ones
+        uint32_t left[kPer];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) left[j] = key[j];
+        e = choose_in_rounds(left, min(wanted, 32), kClosed, lane);
+        *place = e >= 0 ? lane : wanted;
+        uint32_t found = 0;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const uint32_t other = __shfl_sync(0xffffffffu, key[j], e & 31);
+            if (e >= 0 && e / 32 == j) found = other;
         }
-        const bool kept = lane < G && open && rank < p.topk_groups;
-        if (close && sizeof(V) == 4) {
-            // the last one kept against the first one dropped
-            const bool last = kept && rank == p.topk_groups - 1 && below != static_cast<V>(-kInf);
-            const float a = static_cast<float>(score), b = static_cast<float>(below);
-            if (__any_sync(0xffffffffu, last && !(a - b > 2.0f * (reach(a) + reach(b))))) *close = true;
+        *mine = found;
+    }
+    if (ranked) {
+        if (lane <= K) list->ranked[lane] = -1;
+        if (lane == 0) list->ranked[32] = -1;
+        __syncwarp();
+        if (e >= 0 && *place <= K) list->ranked[*place] = static_cast<int16_t>(e);
+    }
+    __syncwarp();
+    return e;
+}
+
+// Closes the experts of all but the topk_groups best groups.  c is in shared memory by expert.
+template <typename V>
+__device__ __forceinline__ void keep_groups(const RouteParams& p, V* c, int lane, bool* close) {
+    const int G = p.num_groups, size = p.E / G;
+    // lanes of a group: a power of two
+    int share = 1;
+    while (share * 2 * G <= 32) share *= 2;
+    const int g = lane / share, sub = lane & (share - 1), turns = (size + share - 1) / share;
+    V first = -kInf, second = -kInf;
+    if (g < G)
+        for (int i = 0, at = g % turns; i < turns; ++i, at = at + 1 == turns ? 0 : at + 1) {     // (each group in another bank)
+            const int e = at * share + sub;
+            const V v = e < size ? c[g * size + e] : static_cast<V>(-kInf);
+            if (v != v || v > first) {
+                second = first;
+                first = v;
+            } else if (v > second) {
+                second = v;
+            }
         }
-        if (lane < G && !kept)
-            for (int i = 0; i < size; ++i) c[lane * size + i] = -kInf;
+    for (int o = 1; o < share; o *= 2) {
+        const V other = __shfl_xor_sync(0xffffffffu, first, o), next = __shfl_xor_sync(0xffffffffu, second, o);
+        const bool higher = key_of(other) > key_of(first);
+        const V rest = higher ? first : other, own = higher ? next : second;
+        first = higher ? other : first;
+        second = key_of(rest) > key_of(own) ? rest : own;
+    }
+    const bool open = g < G && first != static_cast<V>(-kInf);
+    const V score = second != static_cast<V>(-kInf) ? first + second : first;
+    // rank among the groups, equal ones by the lower index; closed groups come last
+    int rank = 0;
+    V below = -kInf;
+    for (int o = 0; o < G; ++o) {
+        const V other = __shfl_sync(0xffffffffu, score, o * share);
+        const bool other_open = __shfl_sync(0xffffffffu, open ? 1 : 0, o * share) != 0;
+        if (!other_open || o == g) continue;
+        const bool higher = key_of(other) > key_of(score) || (key_of(other) == key_of(score) && o < g);
+        if (!open || higher)
+            ++rank;
+        else if (other > below)
+            below = other;
+    }
+    const bool kept = open && rank < p.topk_groups;
+    if (close && sizeof(V) == 4) {
+        // the last one kept against the first one dropped
+        const bool last = kept && rank == p.topk_groups - 1 && below != static_cast<V>(-kInf);
+        const float a = static_cast<float>(score), b = static_cast<float>(below);
+        if (__any_sync(0xffffffffu, last && !(a - b > 2.0f * (reach(a) + reach(b))))) *close = true;
+    }
+    if (g < G && !kept)
+        for (int i = sub; i < size; i += share) c[g * size + i] = -kInf;
+    __syncwarp();
+}
+
+// The choice by c in 64 bits: lane k gets the k-th expert, or -1.
+template <int kPer>
+__device__ __noinline__ int choose_by_doubles(const RouteParams& p, const float (&l)[kPer], const float (&c)[kPer],
+                                              bool all, float largest, double* mem, int lane) {
+    const bool softmax = p.score == EP_SCORE_SOFTMAX;
+    double total = 0.0;
+    if (softmax) {
+#pragma unroll 1
+        for (int j = 0; j < kPer; ++j)
+            if (l[j] != -kInf) total += exp(static_cast<double>(l[j]) - largest);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
+    double c64[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int e = j * 32 + lane;
+        const double d = l[j];
+        c64[j] = -kInf;
+        if (e < p.E && l[j] != -kInf && (all || c[j] != -kInf)) {
+            const double s = softmax ? exp(d - largest) / total : 1.0 / (1.0 + exp(-d));
+            c64[j] = s + (p.bias ? static_cast<double>(p.bias[e]) : 0.0);
+        }
+    }
+    if (all) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            if (j * 32 + lane < p.E) mem[j * 32 + lane] = c64[j];
+        __syncwarp();
+        keep_groups(p, mem, lane, static_cast<bool*>(nullptr));
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            if (j * 32 + lane < p.E) c64[j] = mem[j * 32 + lane];
         __syncwarp();
     }
-};
+    uint64_t key[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) key[j] = c64[j] == -kInf ? 0ull : key_of(p.bias ? c64[j] : static_cast<double>(l[j]));
+    return choose_in_rounds(key, p.K, uint64_t{0}, lane);
+}
 
 template <typename L, int kPer, bool kByScore>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p) {
     extern __shared__ double smem[];     // [kWarps][E] where groups are kept
+    __shared__ Lists lists[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    Lists* const list = &lists[warp];
+    const bool softmax = p.score == EP_SCORE_SOFTMAX;
     pdl_wait();
     pdl_launch_dependents();
-    for (int t = blockIdx.x * kWarps + warp; t < p.T; t += gridDim.x * kWarps) {
+    constexpr bool kAhead = kPer <= 16;      // the next row is asked for before this one's work
+    const int step = gridDim.x * kWarps, first = blockIdx.x * kWarps + warp;
+    const L* const logits = static_cast<const L*>(p.logits);
+    float ahead[kPer];
+    if (kAhead && first < p.T) load_row(logits + first * p.row_stride, p.E, lane, ahead);
+    for (int t = first; t < p.T; t += step) {
         const int64_t out = static_cast<int64_t>(t) * p.K;
+        const L* const row = logits + t * p.row_stride;
+        float l[kPer];
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) l[j] = ahead[j];
+            if (t < p.T - step) load_row(row + step * p.row_stride, p.E, lane, ahead);
+        } else {
+            load_row(row, p.E, lane, l);
+        }
         if (p.token_mask && p.token_mask[t] == 0) {
             if (lane < p.K) {
                 p.topk_idx[out + lane] = -1;
@@ -144,109 +264,86 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
             }
             continue;
         }
-        const L* row = static_cast<const L*>(p.logits) + t * p.row_stride;
-        Chooser<L, kPer, kByScore> ch{p, row, lane};
-        load_row(row, p.E, lane, ch.l);
-        float largest = -kInf;
+        float largest = 0.0f, total = 0.0f;
+        if (softmax && (kByScore || !p.normalize)) {
+            largest = l[0];
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) largest = fmaxf(largest, ch.l[j]);
-        const bool softmax = p.score == EP_SCORE_SOFTMAX;
-        float total = 0.0f;
-        if (softmax) {
+            for (int j = 1; j < kPer; ++j) largest = fmaxf(largest, l[j]);
             largest = warp_max(largest);
-            if (kByScore || !p.normalize) {
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) total += expf(ch.l[j] - largest);
-                total = warp_sum(total);
-            }
+            for (int j = 0; j < kPer; ++j) total += expf(l[j] - largest);
+            total = warp_sum(total);
         }
-        uint32_t key[kPer];
-        int mine;
+        uint32_t key[kPer], mine;
+        int e, place;
         if constexpr (!kByScore) {
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) key[j] = ch.l[j] == -kInf ? 0u : key_of(ch.l[j]);
-            mine = ch.choose(key, nullptr);
+            for (int j = 0; j < kPer; ++j) key[j] = key_of(l[j]);
+            e = choose(key, p.K, false, list, lane, &place, &mine);
         } else {
             bool close = false;
             float c[kPer];
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
-                const int e = j * 32 + lane;
-                const float s = softmax ? expf(ch.l[j] - largest) / total : sigmoid_shifted(ch.l[j], 0.0f);
-                c[j] = ch.l[j] == -kInf ? -kInf : s + (p.bias && e < p.E ? p.bias[e] : 0.0f);
+                const int expert = j * 32 + lane;
+                const float s = softmax ? expf(l[j] - largest) / total : sigmoid_shifted(l[j], 0.0f);
+                c[j] = l[j] == -kInf ? -kInf : s + (p.bias && expert < p.E ? p.bias[expert] : 0.0f);
             }
             const bool grouped = p.topk_groups < p.num_groups;
+            double* const mem = smem + static_cast<size_t>(warp) * p.E;
             if (grouped) {
-                float* const mem = reinterpret_cast<float*>(smem + static_cast<size_t>(warp) * p.E);
+                float* const m = reinterpret_cast<float*>(mem);
 #pragma unroll
                 for (int j = 0; j < kPer; ++j)
-                    if (j * 32 + lane < p.E) mem[j * 32 + lane] = c[j];
+                    if (j * 32 + lane < p.E) m[j * 32 + lane] = c[j];
                 __syncwarp();
-                ch.keep_groups(mem, &close);
+                keep_groups(p, m, lane, &close);
 #pragma unroll
                 for (int j = 0; j < kPer; ++j)
-                    if (j * 32 + lane < p.E) c[j] = mem[j * 32 + lane];
+                    if (j * 32 + lane < p.E) c[j] = m[j * 32 + lane];
                 __syncwarp();
             }
             // without a bias the choice among the kept ones goes by the logits
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) key[j] = c[j] == -kInf ? 0u : key_of(p.bias ? c[j] : ch.l[j]);
-            bool near = false;
-            mine = ch.choose(key, &near);
-            if (close || (p.bias && near)) {
-                double total64 = 0.0;
-                if (softmax) {
-#pragma unroll 1
-                    for (int j = 0; j < kPer; ++j)
-                        if (ch.l[j] != -kInf) total64 += exp(static_cast<double>(ch.l[j]) - largest);
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) total64 += __shfl_xor_sync(0xffffffffu, total64, o);
+            for (int j = 0; j < kPer; ++j) key[j] = c[j] == -kInf ? 0u : key_of(p.bias ? c[j] : l[j]);
+            e = choose(key, p.K, true, list, lane, &place, &mine);
+            if (p.bias) {
+                // neighbours of the first K + 1 that fp32 may have turned round: lane k the k-th and the next
+                bool near = false;
+                const int a = lane < p.K ? list->ranked[lane] : -1, b = lane < p.K ? list->ranked[lane + 1] : -1;
+                if (a >= 0 && b >= 0) {
+                    const float la = to_float(row[a]), lb = to_float(row[b]), ba = p.bias[a], bb = p.bias[b];
+                    const float ca = (softmax ? expf(la - largest) / total : sigmoid_shifted(la, 0.0f)) + ba;
+                    const float cb = (softmax ? expf(lb - largest) / total : sigmoid_shifted(lb, 0.0f)) + bb;
+                    near = ca - cb <= reach(ca) + reach(cb) && !(la == lb && ba == bb);
                 }
-                uint64_t key64[kPer];
-                double c64[kPer];
-#pragma unroll
-                for (int j = 0; j < kPer; ++j) {
-                    const int e = j * 32 + lane;
-                    const double d = ch.l[j];
-                    c64[j] = -kInf;
-                    if (c[j] != -kInf || (grouped && ch.l[j] != -kInf)) {
-                        const double s = softmax ? exp(d - largest) / total64 : 1.0 / (1.0 + exp(-d));
-                        c64[j] = s + (p.bias && e < p.E ? static_cast<double>(p.bias[e]) : 0.0);
-                    }
-                }
-                if (grouped) {
-                    double* const mem = smem + static_cast<size_t>(warp) * p.E;
-#pragma unroll
-                    for (int j = 0; j < kPer; ++j)
-                        if (j * 32 + lane < p.E) mem[j * 32 + lane] = c64[j];
-                    __syncwarp();
-                    ch.keep_groups(mem, nullptr);
-#pragma unroll
-                    for (int j = 0; j < kPer; ++j)
-                        if (j * 32 + lane < p.E) c64[j] = mem[j * 32 + lane];
-                    __syncwarp();
-                }
-#pragma unroll
-                for (int j = 0; j < kPer; ++j)
-                    key64[j] = c64[j] == -kInf ? 0ull : key_of(p.bias ? c64[j] : static_cast<double>(ch.l[j]));
-                mine = ch.choose(key64, nullptr);
+                close |= __any_sync(0xffffffffu, near) || p.K == 32;     // (the 33rd has no lane)
+            }
+            if (close) {
+                e = choose_by_doubles(p, l, c, grouped, largest, mem, lane);
+                place = e >= 0 ? lane : p.K;
             }
         }
-        // weights, by the lane of each slot
-        const bool there = lane < p.K && mine >= 0;
-        const float l = there ? to_float(row[mine]) : -kInf;
+        // weights, by the lane that has a slot
+        const bool there = e >= 0 && place < p.K;
+        const float v = !there ? -kInf : kByScore ? to_float(row[e]) : value_of(mine);
         float w;
         if (p.normalize) {
-            const float top = warp_max(l);
-            const float s = softmax ? (there ? expf(l - top) : 0.0f) : (there ? sigmoid_shifted(l, shift_of(top)) : 0.0f);
+            const float top = warp_max(v);
+            const float s = !there ? 0.0f : softmax ? expf(v - top) : sigmoid_shifted(v, shift_of(top));
             const float sum = warp_sum(s);
-            w = there ? s / sum * p.scale : 0.0f;
+            w = s / sum * p.scale;
         } else {
-            w = there ? (softmax ? expf(l - largest) / total : sigmoid_shifted(l, 0.0f)) * p.scale : 0.0f;
+            w = (softmax ? expf(v - largest) / total : sigmoid_shifted(v, 0.0f)) * p.scale;
         }
-        if (lane < p.K) {
-            p.topk_idx[out + lane] = mine;
-            p.topk_weights[out + lane] = w;
+        const int filled = __popc(__ballot_sync(0xffffffffu, there));
+        if (there) {
+            p.topk_idx[out + place] = e;
+            p.topk_weights[out + place] = w;
+        }
+        if (lane >= filled && lane < p.K) {
+            p.topk_idx[out + lane] = -1;
+            p.topk_weights[out + lane] = 0.0f;
         }
     }
 }
@@ -263,7 +360,8 @@ cudaError_t launch_route(const RouteParams& p, cudaStream_t stream) {
             const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
             if (e != cudaSuccess) return e;
         }
-        const int blocks = (p.T + kWarps - 1) / kWarps;
+        // (many tokens: warps that go on to another token have asked for its row)
+        const int blocks = std::min((p.T + kWarps - 1) / kWarps, device_info().num_sms * 16);
         return launch_pdl(kernel, dim3(blocks), dim3(kWarps * 32), smem, stream, p);
     });
 }

@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "experts.cuh"   // exp2_approx, reciprocal_approx
 #include "route.cuh"
 
 namespace epg {
@@ -28,10 +29,11 @@ __device__ __forceinline__ void load_row(const L* row, int E, int lane, float (&
     }
 }
 
+// The largest value of a warp, NaN aside.
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -49,6 +51,14 @@ __device__ __forceinline__ float sigmoid_shifted(float l, float shift) {
 }
 __device__ __forceinline__ float shift_of(float largest) { return largest < -16.0f ? largest : 0.0f; }
 
+// The same as the hardware's 2^x and 1/x give it, without a shift: (sigmoid(l), 1 - sigmoid(l)), each good to 4e-7 of
+// itself and 2^-24 |l|, what l's own last place moves it by.
+__device__ __forceinline__ float sigmoid_fast(float l, float* rest) {
+    const float e = exp2_approx(-kLog2E * fabsf(l)), r = reciprocal_approx(1.0f + e), small = e * r;
+    *rest = l < 0.0f ? r : small;
+    return l < 0.0f ? small : r;
+}
+
 // Sequence of token t: the last q with offset[q] <= t, -1 or S for tokens
 // before the first or behind the last one.
 __device__ __forceinline__ int sequence_of(const int32_t* offset, int S, int t) {
@@ -62,6 +72,13 @@ __device__ __forceinline__ int sequence_of(const int32_t* offset, int S, int t) 
             hi = mid - 1;
     }
     return lo;
+}
+
+// The same by a warp, all lanes alike.
+__device__ __forceinline__ int warp_sequence_of(const int32_t* offset, int S, int t, int lane) {
+    if (!offset) return 0;
+    if (S >= 32) return sequence_of(offset, S, t);
+    return __popc(__ballot_sync(0xffffffffu, lane <= S && offset[lane <= S ? lane : S] <= t)) - 1;
 }
 
 // Calls f with the type of the logits and the elements of a row in a lane.

@@ -530,7 +530,8 @@ ep_status_t ep_moe_few_tokens(const void* x, const int64_t* topk_idx, const floa
  * num_groups    1, or a divisor of E up to EP_MAX_GROUPS; 1 <= topk_groups <= num_groups, with
  *               topk_groups * E / num_groups >= K.
  * topk_idx      int64 [T, K]; topk_weights fp32 [T, K].
- * Limits: E <= EP_MAX_EXPERTS, K <= min(E, EP_MAX_TOPK), T * E and T * K below 2^31 (beyond: EP_ERR_UNSUPPORTED).
+ * Limits: E <= EP_MAX_EXPERTS, K <= min(E, EP_MAX_TOPK), T <= 2^30, T * E and
+ * T * K below 2^31 (beyond: EP_ERR_UNSUPPORTED).
  */
 ep_status_t ep_route(const void* logits, int logits_dtype, int64_t row_stride, const float* bias,
                      const uint8_t* token_mask, int num_tokens, int num_experts, int num_topk, int score,
