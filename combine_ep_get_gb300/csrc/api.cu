@@ -1011,8 +1011,7 @@ ep_status_t ep_balance_loss(const void* logits, int logits_dtype, int64_t row_st
     p.load = load;
     p.counts = num_tokens_per_expert;
     char* ws = static_cast<char*>(workspace);
-    p.part_sum = reinterpret_cast<float*>(ws + b.off_sum);
-    p.part_count = reinterpret_cast<int32_t*>(ws + b.off_count);
+    p.part = reinterpret_cast<int2*>(ws + b.off_part);
     p.part_tokens = reinterpret_cast<int32_t*>(ws + b.off_tokens);
     p.part_loss = reinterpret_cast<float*>(ws + b.off_loss);
     p.arrived = reinterpret_cast<uint32_t*>(ws + b.off_arrived);

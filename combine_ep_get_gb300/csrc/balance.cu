@@ -22,44 +22,59 @@ constexpr int kThreads = kBalanceWarps * 32;
 
 __device__ __forceinline__ int clamped(int v, int n) { return v < 0 ? 0 : v > n ? n : v; }
 
-// Scores of a row as parts of their sum, for a sigmoid 1 - score too; false for a row whose logits are all -inf.
-// *base and *inverse: a softmax's q is 2^(log2(e) l - base) * inverse; a sigmoid's base is its shift.  Exponentials and reciprocals are the hardware's
-// (sigmoid_fast): exact ones took half of the kernels' instructions.
-template <int kPer>
-__device__ __forceinline__ bool normalised_scores(const float (&l)[kPer], int score, float (&q)[kPer], float (&rest)[kPer],
-                                                  float* base, float* inverse) {
-    float largest = l[0];
-    bool nan = l[0] != l[0];
+// Scores of a row before they are divided by their sum, for a sigmoid 1 - score too; false for a row whose logits are
+// all -inf.  *base: a softmax's q is 2^(log2(e) l - base), a sigmoid's is shifted by it.  Exponentials and reciprocals
+// are the hardware's (sigmoid_fast): exact ones took half of the kernels' instructions.
+template <bool kSoftmax, int kPer>
+__device__ __forceinline__ bool scores_of(const float (&l)[kPer], float (&q)[kPer], float (&rest)[kPer], float* base) {
+    float largest = l[0], any = 0.0f;      // any: NaN if one is
 #pragma unroll
-    for (int j = 1; j < kPer; ++j) {
-        largest = fmaxf(largest, l[j]);
-        nan |= l[j] != l[j];
-    }
+    for (int j = 0; j < kPer; ++j) largest = fmaxf(largest, l[j]);
     largest = warp_max(largest);
-    // (a NaN is something, and stays one)
-    if (largest == -kInf && !__any_sync(0xffffffffu, nan)) return false;
-    float sum = 0.0f;
-    *base = score == EP_SCORE_SOFTMAX ? largest * kLog2E : shift_of(largest);
-    if (score == EP_SCORE_SOFTMAX) {
+    if (largest == -kInf) {      // (a NaN is something, and stays one)
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) sum += q[j] = exp2_approx(fmaf(l[j], kLog2E, -*base));
+        for (int j = 0; j < kPer; ++j) any += l[j];
+        if (!__any_sync(0xffffffffu, any != any)) return false;
+    }
+    *base = kSoftmax ? largest * kLog2E : shift_of(largest);
+    if (kSoftmax) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) q[j] = exp2_approx(fmaf(l[j], kLog2E, -*base));
     } else if (*base == 0.0f) {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) sum += q[j] = sigmoid_fast(l[j], &rest[j]);
+        for (int j = 0; j < kPer; ++j) q[j] = sigmoid_fast(l[j], &rest[j]);
     } else {
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            sum += q[j] = sigmoid_shifted(l[j], *base);
+            q[j] = sigmoid_shifted(l[j], *base);
             rest[j] = sigmoid_shifted(-l[j], 0.0f);
         }
     }
-    *inverse = 1.0f / warp_sum(sum);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) q[j] *= *inverse;
     return true;
 }
 
-template <typename L, int kPer>
+// What a token's work needs from memory, asked for while the token before is worked on.
+template <typename L, int kPer, bool kFull>
+struct Ahead {
+    float l[kPer];
+    int64_t named;      // the lane's slot
+    float g;            // its derivative (the gradient)
+    bool there;
+    template <class P>
+    __device__ __forceinline__ void ask(const P& p, int t, int lane, const int64_t* idx, const float* d_weights) {
+        load_row<kPer, kFull>(static_cast<const L*>(p.logits) + t * p.row_stride, p.E, lane, l);
+        there = !p.token_mask || p.token_mask[t] != 0;
+        named = -1;
+        g = 0.0f;
+        if (lane < p.K) {
+            const int64_t at = static_cast<int64_t>(t) * p.K + lane;
+            if (idx) named = idx[at];
+            if (d_weights) g = d_weights[at];
+        }
+    }
+};
+
+template <typename L, int kPer, bool kFull, bool kSoftmax>
 __global__ void __launch_bounds__(kThreads) balance_sums_kernel(const BalanceParams p) {
     extern __shared__ float smem[];      // [kBalanceWarps][E] sums, [E] counts, tokens
     int* const count = reinterpret_cast<int*>(smem + kBalanceWarps * p.E);
@@ -81,6 +96,8 @@ __global__ void __launch_bounds__(kThreads) balance_sums_kernel(const BalancePar
                 continue;
             }
         }
+        Ahead<L, kPer, kFull> ahead;
+        if (at + warp < stop) ahead.ask(p, at + warp, lane, p.topk_idx, nullptr);
         for (int e = threadIdx.x; e < p.E; e += kThreads) count[e] = 0;
         if (threadIdx.x == 0) *tokens = 0;
         __syncthreads();
@@ -88,35 +105,26 @@ __global__ void __launch_bounds__(kThreads) balance_sums_kernel(const BalancePar
         int live = 0;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) sum[j] = 0.0f;
-        constexpr bool kAhead = kPer <= 16;      // the next row is asked for before this one's work
-        const L* const logits = static_cast<const L*>(p.logits);
-        float ahead[kPer];
-        if (kAhead && at + warp < stop) load_row(logits + (at + warp) * p.row_stride, p.E, lane, ahead);
         for (int t = at + warp; t < stop; t += kBalanceWarps) {
-            float l[kPer], s[kPer], rest[kPer], base, inverse;
-            if constexpr (kAhead) {
+            const Ahead<L, kPer, kFull> now = ahead;
+            if (t + kBalanceWarps < stop) ahead.ask(p, t + kBalanceWarps, lane, p.topk_idx, nullptr);
+            float s[kPer], rest[kPer], base;
+            if (!now.there || !scores_of<kSoftmax>(now.l, s, rest, &base)) continue;
+            float all = 0.0f;
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) l[j] = ahead[j];
-                if (t + kBalanceWarps < stop) load_row(logits + (t + kBalanceWarps) * p.row_stride, p.E, lane, ahead);
-            } else {
-                load_row(logits + t * p.row_stride, p.E, lane, l);
-            }
-            if (p.token_mask && p.token_mask[t] == 0) continue;
-            if (!normalised_scores(l, p.score, s, rest, &base, &inverse)) continue;
+            for (int j = 0; j < kPer; ++j) all += s[j];
+            all = 1.0f / warp_sum(all);
             ++live;
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) sum[j] += s[j];
-            if (lane < p.K) {
-                const int64_t e = p.topk_idx[static_cast<int64_t>(t) * p.K + lane];
-                if (e >= 0 && e < p.E)
-                    atomicAdd(&count[e], 1);
-                else if (e != -1)
-                    atomicOr(p.status, EP_ERR_INVALID_INDEX);
-            }
+            for (int j = 0; j < kPer; ++j) sum[j] = fmaf(s[j], all, sum[j]);
+            if (now.named >= 0 && now.named < p.E)
+                atomicAdd(&count[now.named], 1);
+            else if (now.named != -1)
+                atomicOr(p.status, EP_ERR_INVALID_INDEX);
         }
 #pragma unroll
         for (int j = 0; j < kPer; ++j)
-            if (j * 32 + lane < p.E) smem[warp * p.E + j * 32 + lane] = sum[j];
+            if (kFull || j * 32 + lane < p.E) smem[warp * p.E + j * 32 + lane] = sum[j];
         if (lane == 0) atomicAdd(tokens, live);
         __syncthreads();
         const int64_t piece = blockIdx.x + q;
@@ -125,8 +133,7 @@ __global__ void __launch_bounds__(kThreads) balance_sums_kernel(const BalancePar
                 float all = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kBalanceWarps; ++w) all += smem[w * p.E + e];
-                p.part_sum[piece * p.E + e] = all;
-                p.part_count[piece * p.E + e] = count[e];
+                p.part[piece * p.E + e] = make_int2(__float_as_int(all), count[e]);
             }
             if (threadIdx.x == 0) p.part_tokens[piece] = *tokens;
         }
@@ -135,15 +142,17 @@ __global__ void __launch_bounds__(kThreads) balance_sums_kernel(const BalancePar
     }
 }
 
-constexpr int kParts = 32;       // shares of a sequence's pieces, one warp each
+// A CTA adds a sequence's pieces for eight experts: 32 bytes of scores' sums and as many of counts a piece, 128
+// pieces at a time (32 experts a CTA, 32 pieces at a time, left it waiting for ten pieces one after another).
+constexpr int kLossThreads = 1024, kLossWarps = kLossThreads / 32;
 
-__global__ void __launch_bounds__(kParts * 32) balance_loss_kernel(const BalanceParams p) {
-    __shared__ float sums[kParts][33];
-    __shared__ int counts[kParts][33], live[kParts];
+__global__ void __launch_bounds__(kLossThreads) balance_loss_kernel(const BalanceParams p) {
+    __shared__ float sums[kLossWarps][kBalanceChunk];
+    __shared__ int counts[kLossWarps][kBalanceChunk], live[kLossWarps];
     __shared__ bool last;
-    const int lane = threadIdx.x & 31, part = threadIdx.x / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, in_chunk = lane % kBalanceChunk;
     const int chunks = (p.E + kBalanceChunk - 1) / kBalanceChunk;
-    const int q = blockIdx.x / chunks, e = blockIdx.x % chunks * kBalanceChunk + lane;
+    const int q = blockIdx.x / chunks, e = blockIdx.x % chunks * kBalanceChunk + in_chunk;
     pdl_wait();
     pdl_launch_dependents();
     int first = 0, end = p.T;
@@ -156,34 +165,51 @@ __global__ void __launch_bounds__(kParts * 32) balance_loss_kernel(const Balance
     const int tile0 = first / p.tile_tokens, tile1 = end > first ? (end - 1) / p.tile_tokens + 1 : tile0;
     float sum = 0.0f;
     int count = 0, n = 0;
-    for (int tile = tile0 + part; tile < tile1; tile += kParts) {
+#pragma unroll 4
+    for (int tile = tile0 + threadIdx.x / kBalanceChunk; tile < tile1; tile += kLossThreads / kBalanceChunk) {
         const int64_t piece = tile + q;
         if (!EP_IN(piece, p.tiles + p.S)) continue;
         if (e < p.E) {
-            sum += p.part_sum[piece * p.E + e];
-            count += p.part_count[piece * p.E + e];
+            const int2 part = p.part[piece * p.E + e];
+            sum += __int_as_float(part.x);
+            count += part.y;
         }
-        n += p.part_tokens[piece];
+        if (in_chunk == 0) n += p.part_tokens[piece];
     }
-    sums[part][lane] = sum;
-    counts[part][lane] = count;
-    if (lane == 0) live[part] = n;
+    n = __reduce_add_sync(0xffffffffu, n);
+#pragma unroll
+    for (int o = kBalanceChunk; o < 32; o *= 2) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        count += __shfl_xor_sync(0xffffffffu, count, o);
+    }
+    if (lane < kBalanceChunk) {
+        sums[warp][lane] = sum;
+        counts[warp][lane] = count;
+    }
+    if (lane == 0) live[warp] = n;
     __syncthreads();
-    if (part == 0) {
+    if (warp == 0) {
         sum = 0.0f;
-        count = n = 0;
-        for (int i = 0; i < kParts; ++i) {
-            sum += sums[i][lane];
-            count += counts[i][lane];
-            n += live[i];
+        count = 0;
+#pragma unroll
+        for (int i = 0; i < kLossWarps; i += 32 / kBalanceChunk) {
+            sum += sums[i + lane / kBalanceChunk][in_chunk];
+            count += counts[i + lane / kBalanceChunk][in_chunk];
         }
+#pragma unroll
+        for (int o = kBalanceChunk; o < 32; o *= 2) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            count += __shfl_xor_sync(0xffffffffu, count, o);
+        }
+        n = __reduce_add_sync(0xffffffffu, live[lane]);
         const float tokens = static_cast<float>(n);
         const float load = n > 0 ? p.coeff * p.E / (static_cast<float>(p.S) * p.K) * (count / tokens) / tokens : 0.0f;
-        if (e < p.E) {
+        const bool mine = lane < kBalanceChunk && e < p.E;
+        if (mine) {
             p.load[static_cast<int64_t>(q) * p.E + e] = load;
             if (p.counts) p.counts[static_cast<int64_t>(q) * p.E + e] = count;
         }
-        const float loss = warp_sum(e < p.E && n > 0 ? load * sum : 0.0f);
+        const float loss = warp_sum(mine && n > 0 ? load * sum : 0.0f);
         if (lane == 0) {
             p.part_loss[blockIdx.x] = loss;
             __threadfence();
@@ -195,107 +221,91 @@ __global__ void __launch_bounds__(kParts * 32) balance_loss_kernel(const Balance
     // shares of the parts by thread, then by warp
     __threadfence();
     float all = 0.0f;
-    for (unsigned i = threadIdx.x; i < gridDim.x; i += kParts * 32) all += __ldcg(p.part_loss + i);
+    for (unsigned i = threadIdx.x; i < gridDim.x; i += kLossThreads) all += __ldcg(p.part_loss + i);
     all = warp_sum(all);
-    if (lane == 0) sums[part][0] = all;
+    if (lane == 0) sums[warp][0] = all;
     __syncthreads();
-    if (part == 0) {
+    if (warp == 0) {
         all = warp_sum(sums[lane][0]);
         if (lane == 0) *p.loss = all;
     }
 }
 
-template <typename L, int kPer>
+template <typename L, int kPer, bool kFull, bool kSoftmax>
 __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteBackwardParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     pdl_wait();
     pdl_launch_dependents();
-    const bool softmax = p.score == EP_SCORE_SOFTMAX;
     const float d_loss = p.load ? *p.d_loss : 0.0f;
-    constexpr bool kAhead = kPer <= 16;      // the next row is asked for before this one's work
     const int step = gridDim.x * kBalanceWarps, first = blockIdx.x * kBalanceWarps + warp;
-    const L* const logits = static_cast<const L*>(p.logits);
-    float ahead[kPer], load[kPer];
+    const int64_t* const idx = p.d_topk_weights ? p.topk_idx : nullptr;
+    Ahead<L, kPer, kFull> ahead;
+    float load[kPer];
     int load_of = -1;        // the sequence whose derivatives `load` holds
 #pragma unroll
     for (int j = 0; j < kPer; ++j) load[j] = 0.0f;
-    if (kAhead && first < p.T) load_row(logits + first * p.row_stride, p.E, lane, ahead);
+    if (first < p.T) ahead.ask(p, first, lane, idx, p.d_topk_weights);
     for (int t = first; t < p.T; t += step) {
-        const L* const row = logits + t * p.row_stride;
+        const L* const row = static_cast<const L*>(p.logits) + t * p.row_stride;
         L* const out = static_cast<L*>(p.d_logits) + t * p.d_row_stride;
-        float l[kPer], s[kPer], rest[kPer], d[kPer], base, inverse;
-        if constexpr (kAhead) {
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) l[j] = ahead[j];
-            if (t < p.T - step) load_row(row + step * p.row_stride, p.E, lane, ahead);
-        } else {
-            load_row(row, p.E, lane, l);
-        }
+        const Ahead<L, kPer, kFull> now = ahead;
+        if (t < p.T - step) ahead.ask(p, t + step, lane, idx, p.d_topk_weights);
         // the token's slots, a lane each, with their experts' logits
         int e = -1;
-        float g = 0.0f, v = -kInf;
-        if (p.d_topk_weights && lane < p.K) {
-            const int64_t at = static_cast<int64_t>(t) * p.K + lane, named = p.topk_idx[at];
-            if (named >= 0 && named < p.E) {
-                e = static_cast<int>(named);
-                g = p.d_topk_weights[at] * p.scale;
-                v = to_float(row[e]);
-            } else if (named != -1) {
-                atomicOr(p.status, EP_ERR_INVALID_INDEX);
-            }
+        float v = -kInf;
+        const float g = now.g * p.scale;
+        if (now.named >= 0 && now.named < p.E) {
+            e = static_cast<int>(now.named);
+            v = to_float(row[e]);
+        } else if (now.named != -1) {
+            atomicOr(p.status, EP_ERR_INVALID_INDEX);
         }
-        if ((p.token_mask && p.token_mask[t] == 0) || !normalised_scores(l, p.score, s, rest, &base, &inverse)) {
+        float s[kPer], rest[kPer], base;
+        if (!now.there || !scores_of<kSoftmax>(now.l, s, rest, &base)) {
 #pragma unroll
             for (int j = 0; j < kPer; ++j)
-                if (j * 32 + lane < p.E) from_float(out + j * 32 + lane, 0.0f);
+                if (kFull || j * 32 + lane < p.E) from_float(out + j * 32 + lane, 0.0f);
             continue;
         }
-        // through the loss
-        float mean = 0.0f;
+        // The loss's mean derivative, over the scores' sum.
         const int q = p.load ? warp_sequence_of(p.seq_offset, p.S, t, lane) : -1;
         const bool in_loss = q >= 0 && q < p.S;
-        if (in_loss) {
-            if (q != load_of) {
-                load_of = q;
+        if (q != load_of) {
+            load_of = q;
 #pragma unroll
-                for (int j = 0; j < kPer; ++j)
-                    load[j] = j * 32 + lane < p.E ? p.load[static_cast<int64_t>(q) * p.E + j * 32 + lane] * d_loss : 0.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) mean += load[j] * s[j];
-            mean = warp_sum(mean);
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                d[j] = s[j] * (load[j] - mean);
-                if (!softmax) d[j] *= rest[j];
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) d[j] = 0.0f;
+            for (int j = 0; j < kPer; ++j)
+                load[j] = in_loss && (kFull || j * 32 + lane < p.E)
+                              ? p.load[static_cast<int64_t>(q) * p.E + j * 32 + lane] * d_loss : 0.0f;
         }
+        float inverse = 0.0f, mean = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            inverse += s[j];
+            mean = fmaf(load[j], s[j], mean);
+        }
+        warp_sums(inverse, mean);
+        inverse = 1.0f / inverse;
+        mean *= inverse;
         // Through the weights: the slots' lanes know their experts' whole derivative, and store it after the row's.
         float r = 0.0f;
         if (p.d_topk_weights) {
-            const float top = warp_max(v);
             if (p.normalize) {
-                const float u = v == -kInf ? 0.0f : softmax ? exp2_approx((v - top) * kLog2E) : sigmoid_shifted(v, shift_of(top));
-                const float sum = warp_sum(u), part = u == 0.0f ? 0.0f : u / sum;
-                r = part * (g - warp_sum(part * g));
+                const float top = warp_max(v);
+                const float u = v == -kInf ? 0.0f : kSoftmax ? exp2_approx((v - top) * kLog2E) : sigmoid_shifted(v, shift_of(top));
+                float sum = u, weighted = u * g;
+                warp_sums(sum, weighted);
+                r = u == 0.0f ? 0.0f : u / sum * (g - weighted / sum);
             } else if (v != -kInf) {
-                r = (softmax ? exp2_approx(fmaf(v, kLog2E, -base)) * inverse : sigmoid_shifted(v, 0.0f)) * g;
+                r = (kSoftmax ? exp2_approx(fmaf(v, kLog2E, -base)) * inverse : sigmoid_shifted(v, 0.0f)) * g;
             }
-            if (softmax && !p.normalize) {
-                // every expert loses its share of the chosen ones' sum
-                const float spread = warp_sum(r);
-                mean += spread;
-#pragma unroll
-                for (int j = 0; j < kPer; ++j) d[j] -= s[j] * spread;
-            }
-            if (!softmax && e >= 0) r *= sigmoid_shifted(-v, 0.0f);
+            if (kSoftmax && !p.normalize) mean += warp_sum(r);      // every expert loses its share of the chosen ones' sum
+            if (!kSoftmax && e >= 0) r *= sigmoid_shifted(-v, 0.0f);
         }
 #pragma unroll
-        for (int j = 0; j < kPer; ++j)
-            if (j * 32 + lane < p.E) from_float(out + j * 32 + lane, d[j]);
+        for (int j = 0; j < kPer; ++j) {
+            const float d = s[j] * inverse * (load[j] - mean);
+            if (kFull || j * 32 + lane < p.E) from_float(out + j * 32 + lane, kSoftmax || !in_loss ? d : d * rest[j]);
+        }
         if (p.d_topk_weights) {
             // an expert that is named twice gets both parts, in the order of the slots, from the first one's lane
             const unsigned same = __match_any_sync(0xffffffffu, e >= 0 ? e : -1 - lane);
@@ -309,17 +319,17 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteBac
             }
             __syncwarp();     // after the row's stores
             if (e >= 0 && (same & ((1u << lane) - 1)) == 0) {
+                const float a = in_loss ? p.load[static_cast<int64_t>(q) * p.E + e] * d_loss : 0.0f;
                 float own = 0.0f;
                 if (v == -kInf) {
                     own = 0.0f;
-                } else if (softmax) {
-                    const float s_e = exp2_approx(fmaf(v, kLog2E, -base)) * inverse;
-                    own = s_e * ((in_loss ? p.load[static_cast<int64_t>(q) * p.E + e] * d_loss : 0.0f) - mean);
+                } else if (kSoftmax) {
+                    own = exp2_approx(fmaf(v, kLog2E, -base)) * inverse * (a - mean);
                 } else if (in_loss) {
                     float rest_e;
-                    const float s_e = (base == 0.0f ? sigmoid_fast(v, &rest_e) : sigmoid_shifted(v, base)) * inverse;
+                    const float s_e = base == 0.0f ? sigmoid_fast(v, &rest_e) : sigmoid_shifted(v, base);
                     if (base != 0.0f) rest_e = sigmoid_shifted(-v, 0.0f);
-                    own = s_e * (p.load[static_cast<int64_t>(q) * p.E + e] * d_loss - mean) * rest_e;
+                    own = s_e * inverse * (a - mean) * rest_e;
                 }
                 from_float(out + e, own + r);
             }
@@ -330,9 +340,12 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteBac
 }  // namespace
 
 cudaError_t launch_balance_loss(const BalanceParams& p, cudaStream_t stream) {
-    const cudaError_t e = with_row_type(p.dtype, p.E, [&](auto* type, auto per) {
+    const cudaError_t e = with_row_type(p.dtype, p.E, [&](auto* type, auto per, auto full) {
         using L = std::remove_const_t<std::remove_pointer_t<decltype(type)>>;
-        const auto kernel = balance_sums_kernel<L, decltype(per)::value>;
+        constexpr int kPer = decltype(per)::value;
+        constexpr bool kFull = decltype(full)::value;
+        const auto kernel = p.score == EP_SCORE_SOFTMAX ? balance_sums_kernel<L, kPer, kFull, true>
+                                                        : balance_sums_kernel<L, kPer, kFull, false>;
         const size_t smem = static_cast<size_t>(kBalanceWarps + 1) * p.E * 4 + 16;
         if (smem > 48 * 1024) {
             const cudaError_t err =
@@ -343,13 +356,16 @@ cudaError_t launch_balance_loss(const BalanceParams& p, cudaStream_t stream) {
     });
     if (e != cudaSuccess) return e;
     const int chunks = (p.E + kBalanceChunk - 1) / kBalanceChunk;
-    return launch_pdl(balance_loss_kernel, dim3(static_cast<unsigned>(p.S) * chunks), dim3(kParts * 32), 0, stream, p);
+    return launch_pdl(balance_loss_kernel, dim3(static_cast<unsigned>(p.S) * chunks), dim3(kLossThreads), 0, stream, p);
 }
 
 cudaError_t launch_route_backward(const RouteBackwardParams& p, cudaStream_t stream) {
-    return with_row_type(p.dtype, p.E, [&](auto* type, auto per) {
+    return with_row_type(p.dtype, p.E, [&](auto* type, auto per, auto full) {
         using L = std::remove_const_t<std::remove_pointer_t<decltype(type)>>;
-        const auto kernel = route_backward_kernel<L, decltype(per)::value>;
+        constexpr int kPer = decltype(per)::value;
+        constexpr bool kFull = decltype(full)::value;
+        const auto kernel = p.score == EP_SCORE_SOFTMAX ? route_backward_kernel<L, kPer, kFull, true>
+                                                        : route_backward_kernel<L, kPer, kFull, false>;
         // (many tokens: warps that go on to another token have asked for its row)
         const int blocks = std::min((p.T + kBalanceWarps - 1) / kBalanceWarps, device_info().num_sms * 8);
         return launch_pdl(kernel, dim3(blocks), dim3(kThreads), 0, stream, p);

@@ -46,9 +46,10 @@ __device__ __forceinline__ float value_of(uint32_t k) {
 // How far c in fp32 may lie from c: the score is good to a few units of the last place, the sum to half a one.
 __device__ __forceinline__ float reach(float c) { return 5e-7f * fmaxf(1.0f, fabsf(c)); }
 
-// What a warp's choice needs in shared memory.
-struct Lists {
-    uint64_t found[32];
+// What a warp's choice needs in shared memory: the candidates in the order of their indices, and the chosen ones' places.
+struct alignas(16) Lists {
+    uint32_t key[32];
+    int16_t expert[32];
     int16_t ranked[33];
 };
 
@@ -85,33 +86,40 @@ __device__ __forceinline__ int choose(uint32_t (&key)[kPer], int K, bool ranked,
     uint32_t best = key[0];
 #pragma unroll
     for (int j = 1; j < kPer; ++j) best = max(best, key[j]);
-    uint32_t least = kClosed + 1;
+    uint32_t least = 0;
+#pragma unroll 2
     for (int k = 0; k < wanted; ++k) {
-        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-        if (top <= kClosed) {
-            least = kClosed + 1;
-            break;
-        }
-        least = top;
-        if (best == top) best = 0;
+        least = __reduce_max_sync(0xffffffffu, best);
+        if (best == least) best = 0;
     }
+    least = max(least, kClosed + 1);      // (fewer lanes with open ones than wanted: all that are open)
     int n = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         const unsigned there = __ballot_sync(0xffffffffu, key[j] >= least);
         const int at = n + __popc(there & ((1u << lane) - 1));
-        if (key[j] >= least && at < 32) list->found[at] = static_cast<uint64_t>(key[j]) << 32 | (0xffffffffu - (j * 32 + lane));
+        if (key[j] >= least && at < 32) {
+            list->key[at] = key[j];
+            list->expert[at] = static_cast<int16_t>(j * 32 + lane);
+        }
         n += __popc(there);
     }
     __syncwarp();
     int e = -1;
     if (n <= 32) {
-        const uint64_t own = lane < n ? list->found[lane] : 0;
+        // larger ones and equal ones before come first
+        const uint32_t own = lane < n ? list->key[lane] : 0;
         int rank = 0;
-        for (int i = 0; i < n; ++i) rank += list->found[i] > own;
+        for (int i = 0; i < n; i += 4) {
+            const uint4 k = *reinterpret_cast<const uint4*>(list->key + i);
+            rank += k.x > own - (i < lane);
+            rank += i + 1 < n && k.y > own - (i + 1 < lane);
+            rank += i + 2 < n && k.z > own - (i + 2 < lane);
+            rank += i + 3 < n && k.w > own - (i + 3 < lane);
+        }
         *place = lane < n ? rank : wanted;
-        *mine = static_cast<uint32_t>(own >> 32);
-        e = lane < n ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(own)) : -1;
+        *mine = own;
+        e = lane < n ? list->expert[lane] : -1;
     } else {
         // many equal values, or few lanes with open ones
         uint32_t left[kPer];
@@ -166,25 +174,25 @@ __device__ __forceinline__ void keep_groups(const RouteParams& p, V* c, int lane
     }
     const bool open = g < G && first != static_cast<V>(-kInf);
     const V score = second != static_cast<V>(-kInf) ? first + second : first;
-    // rank among the groups, equal ones by the lower index; closed groups come last
-    int rank = 0;
-    V below = -kInf;
-    for (int o = 0; o < G; ++o) {
-        const V other = __shfl_sync(0xffffffffu, score, o * share);
-        const bool other_open = __shfl_sync(0xffffffffu, open ? 1 : 0, o * share) != 0;
-        if (!other_open || o == g) continue;
-        const bool higher = key_of(other) > key_of(score) || (key_of(other) == key_of(score) && o < g);
-        if (!open || higher)
-            ++rank;
-        else if (other > below)
-            below = other;
+    // the best groups, one round each, equal ones by the lower index
+    auto key = open && sub == 0 ? key_of(score) : decltype(key_of(score))(0);
+    unsigned keep = 0;
+    V worst = 0;
+    for (int k = 0; k < p.topk_groups; ++k) {
+        const auto top = key_max(key);
+        if (top == 0) break;
+        const int winner = __ffs(__ballot_sync(0xffffffffu, key == top)) - 1;
+        if (lane == winner) key = 0;
+        keep |= 1u << (winner / share);
+        worst = __shfl_sync(0xffffffffu, score, winner);
     }
-    const bool kept = open && rank < p.topk_groups;
+    const bool kept = g < G && (keep >> g & 1);
     if (close && sizeof(V) == 4) {
-        // the last one kept against the first one dropped
-        const bool last = kept && rank == p.topk_groups - 1 && below != static_cast<V>(-kInf);
-        const float a = static_cast<float>(score), b = static_cast<float>(below);
-        if (__any_sync(0xffffffffu, last && !(a - b > 2.0f * (reach(a) + reach(b))))) *close = true;
+        // the last one kept against the best one dropped
+        const auto next = key_max(key);
+        const int other = next == 0 ? -1 : __ffs(__ballot_sync(0xffffffffu, key == next)) - 1;
+        const float b = __shfl_sync(0xffffffffu, static_cast<float>(score), other & 31), a = static_cast<float>(worst);
+        if (other >= 0 && !(a - b > 2.0f * (reach(a) + reach(b)))) *close = true;
     }
     if (g < G && !kept)
         for (int i = sub; i < size; i += share) c[g * size + i] = -kInf;
@@ -232,7 +240,7 @@ __device__ __noinline__ int choose_by_doubles(const RouteParams& p, const float 
     return choose_in_rounds(key, p.K, uint64_t{0}, lane);
 }
 
-template <typename L, int kPer, bool kByScore>
+template <typename L, int kPer, bool kFull, bool kByScore>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p) {
     extern __shared__ double smem[];     // [kWarps][E] where groups are kept
     __shared__ Lists lists[kWarps];
@@ -245,7 +253,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
     const int step = gridDim.x * kWarps, first = blockIdx.x * kWarps + warp;
     const L* const logits = static_cast<const L*>(p.logits);
     float ahead[kPer];
-    if (kAhead && first < p.T) load_row(logits + first * p.row_stride, p.E, lane, ahead);
+    if (kAhead && first < p.T) load_row<kPer, kFull>(logits + first * p.row_stride, p.E, lane, ahead);
     for (int t = first; t < p.T; t += step) {
         const int64_t out = static_cast<int64_t>(t) * p.K;
         const L* const row = logits + t * p.row_stride;
@@ -253,9 +261,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
         if constexpr (kAhead) {
 #pragma unroll
             for (int j = 0; j < kPer; ++j) l[j] = ahead[j];
-            if (t < p.T - step) load_row(row + step * p.row_stride, p.E, lane, ahead);
+            if (t < p.T - step) load_row<kPer, kFull>(row + step * p.row_stride, p.E, lane, ahead);
         } else {
-            load_row(row, p.E, lane, l);
+            load_row<kPer, kFull>(row, p.E, lane, l);
         }
         if (p.token_mask && p.token_mask[t] == 0) {
             if (lane < p.K) {
@@ -330,9 +338,11 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
         float w;
         if (p.normalize) {
             const float top = warp_max(v);
-            const float s = !there ? 0.0f : softmax ? expf(v - top) : sigmoid_shifted(v, shift_of(top));
-            const float sum = warp_sum(s);
-            w = s / sum * p.scale;
+            float s = 0.0f, rest;
+            if (there)
+                s = softmax ? exp2_approx((v - top) * kLog2E)
+                            : shift_of(top) == 0.0f ? sigmoid_fast(v, &rest) : sigmoid_shifted(v, shift_of(top));
+            w = s * (p.scale / warp_sum(s));
         } else {
             w = (softmax ? expf(v - largest) / total : sigmoid_shifted(v, 0.0f)) * p.scale;
         }
@@ -351,11 +361,13 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
 }  // namespace
 
 cudaError_t launch_route(const RouteParams& p, cudaStream_t stream) {
-    return with_row_type(p.dtype, p.E, [&](auto* type, auto per) {
+    return with_row_type(p.dtype, p.E, [&](auto* type, auto per, auto full) {
         using L = std::remove_const_t<std::remove_pointer_t<decltype(type)>>;
         const bool grouped = p.topk_groups < p.num_groups;
         const size_t smem = grouped ? static_cast<size_t>(kWarps) * p.E * 8 : 0;
-        const auto kernel = p.bias || grouped ? route_kernel<L, decltype(per)::value, true> : route_kernel<L, decltype(per)::value, false>;
+        constexpr int kPer = decltype(per)::value;
+        constexpr bool kFull = decltype(full)::value;
+        const auto kernel = p.bias || grouped ? route_kernel<L, kPer, kFull, true> : route_kernel<L, kPer, kFull, false>;
         if (smem > 48 * 1024) {
             const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
             if (e != cudaSuccess) return e;

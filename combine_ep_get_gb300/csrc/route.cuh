@@ -32,8 +32,7 @@ struct BalanceParams {
     float* load;                 // [S][E]
     int32_t* counts;             // [S][E] or null
     // workspace: one piece is one tile's tokens of one sequence, numbered tile + sequence
-    float* part_sum;             // [tiles + S][E] sums of scores
-    int32_t* part_count;         // [tiles + S][E] entries naming each expert
+    int2* part;                  // [tiles + S][E] sums of scores (their bits), entries naming each expert
     int32_t* part_tokens;        // [tiles + S] tokens that count
     float* part_loss;            // [S][chunks of experts]
     uint32_t* arrived;           // [1]
@@ -64,11 +63,11 @@ cudaError_t launch_route_backward(const RouteBackwardParams& p, cudaStream_t str
 
 // Workspace carve-up shared by the size query and the call.
 constexpr int kBalanceWarps = 8;
-constexpr int kBalanceChunk = 32;       // experts of one CTA of the second kernel
-constexpr int kBalanceTiles = 304;      // at most: two CTAs for each of 152 SMs
+constexpr int kBalanceChunk = 8;        // experts of one CTA of the second kernel
+constexpr int kBalanceTiles = 608;      // at most: four CTAs for each of 152 SMs
 struct BalanceWorkspace {
     int tile_tokens, tiles;
-    size_t off_sum, off_count, off_tokens, off_loss, off_arrived, total;
+    size_t off_part, off_tokens, off_loss, off_arrived, total;
 };
 inline BalanceWorkspace balance_workspace(int T, int E, int S) {
     const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
@@ -77,9 +76,8 @@ inline BalanceWorkspace balance_workspace(int T, int E, int S) {
     b.tile_tokens = each < kBalanceWarps ? kBalanceWarps : (each + kBalanceWarps - 1) / kBalanceWarps * kBalanceWarps;
     b.tiles = T > 0 ? (T + b.tile_tokens - 1) / b.tile_tokens : 0;
     const size_t pieces = static_cast<size_t>(b.tiles) + S, chunks = (static_cast<size_t>(E) + kBalanceChunk - 1) / kBalanceChunk;
-    b.off_sum = 0;
-    b.off_count = up(pieces * E * 4);
-    b.off_tokens = b.off_count + up(pieces * E * 4);
+    b.off_part = 0;
+    b.off_tokens = up(pieces * E * 8);
     b.off_loss = b.off_tokens + up(pieces * 4);
     b.off_arrived = b.off_loss + up(static_cast<size_t>(S) * chunks * 4);
     b.total = b.off_arrived + 256;

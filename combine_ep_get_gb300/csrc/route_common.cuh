@@ -19,13 +19,13 @@ __device__ __forceinline__ void from_float(__half* p, float v) { *p = __float2ha
 
 constexpr float kInf = __builtin_huge_valf();
 
-// A row's logits; -inf behind the last expert.
-template <int kPer, typename L>
+// A row's logits; -inf behind the last expert.  kFull: there are 32 kPer experts.
+template <int kPer, bool kFull = false, typename L>
 __device__ __forceinline__ void load_row(const L* row, int E, int lane, float (&v)[kPer]) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         const int e = j * 32 + lane;
-        v[j] = e < E ? to_float(row[e]) : -kInf;
+        v[j] = kFull || e < E ? to_float(row[e]) : -kInf;
     }
 }
 
@@ -39,6 +39,16 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+
+// Two sums at once: a sum's five exchanges wait for one another.
+__device__ __forceinline__ void warp_sums(float& a, float& b) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float x = __shfl_xor_sync(0xffffffffu, a, o), y = __shfl_xor_sync(0xffffffffu, b, o);
+        a += x;
+        b += y;
+    }
 }
 
 // sigmoid(l) exp(-shift), shift <= 0: with the largest logit of a sum as shift
@@ -81,17 +91,20 @@ __device__ __forceinline__ int warp_sequence_of(const int32_t* offset, int S, in
     return __popc(__ballot_sync(0xffffffffu, lane <= S && offset[lane <= S ? lane : S] <= t)) - 1;
 }
 
-// Calls f with the type of the logits and the elements of a row in a lane.
+// Calls f with the type of the logits, the elements of a row in a lane, and whether a row fills them.
 template <typename F>
 cudaError_t with_row_type(int dtype, int E, F f) {
     const auto sized = [&](auto* type) {
-        if (E <= 32) return f(type, std::integral_constant<int, 1>());
-        if (E <= 64) return f(type, std::integral_constant<int, 2>());
-        if (E <= 128) return f(type, std::integral_constant<int, 4>());
-        if (E <= 256) return f(type, std::integral_constant<int, 8>());
-        if (E <= 512) return f(type, std::integral_constant<int, 16>());
-        if (E <= 1024) return f(type, std::integral_constant<int, 32>());
-        return f(type, std::integral_constant<int, 64>());
+        const auto full = [&](auto per) {
+            return E == 32 * decltype(per)::value ? f(type, per, std::true_type()) : f(type, per, std::false_type());
+        };
+        if (E <= 32) return full(std::integral_constant<int, 1>());
+        if (E <= 64) return full(std::integral_constant<int, 2>());
+        if (E <= 128) return full(std::integral_constant<int, 4>());
+        if (E <= 256) return full(std::integral_constant<int, 8>());
+        if (E <= 512) return f(type, std::integral_constant<int, 16>(), std::false_type());
+        if (E <= 1024) return f(type, std::integral_constant<int, 32>(), std::false_type());
+        return f(type, std::integral_constant<int, 64>(), std::false_type());
     };
     if (dtype == EP_FP32) return sized(static_cast<const float*>(nullptr));
     if (dtype == EP_FP16) return sized(static_cast<const __half*>(nullptr));
