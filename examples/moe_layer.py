@@ -1,6 +1,7 @@
-"""A mixture-of-experts layer on the library: one call for a few tokens, the
-rows path (layout, expanded dispatch, two experts' products, expanded combine)
-for many, and the rows path's backward pass.
+"""A mixture-of-experts layer on the library: the router with its balance loss,
+one call for a few tokens, the rows path (layout, expanded dispatch, two
+experts' products, expanded combine) for many, and the backward pass of
+router and rows path.
 
     python examples/moe_layer.py [--tokens 4096] [--hidden 2048] [--inner 1024] [--experts 32] [--topk 4]
 
@@ -34,6 +35,29 @@ class MoeLayer:
         if ws is None or ws.numel() < nbytes:
             ws = self._workspace[what] = torch.empty(nbytes, dtype=torch.uint8, device=self.w_up.device)
         return ws
+
+    def route(self, logits, topk, score=ep.EP_SCORE_SOFTMAX, bias=None, token_mask=None, coeff=None, **how):
+        """topk_idx and topk_weights from the router's logits [T, E]; with coeff also the balance loss over all tokens
+        and what route_backward() needs."""
+        T, E = logits.shape
+        idx = torch.empty((T, topk), dtype=torch.int64, device=logits.device)
+        weights = torch.empty((T, topk), device=logits.device)
+        ep.ep_route(logits, idx, weights, self.status, score=score, bias=bias, token_mask=token_mask, **how)
+        if coeff is None:
+            return idx, weights
+        loss, load = torch.empty(1, device=logits.device), torch.empty((1, E), device=logits.device)
+        ws = self._scratch("balance", ep.ep_balance_loss_workspace_bytes(T, E))
+        ep.ep_balance_loss(logits, idx, ws, loss, load, self.status, score=score, token_mask=token_mask, coeff=coeff)
+        kept = {k: v for k, v in how.items() if k in ("normalize", "scale")}
+        return idx, weights, loss, (logits, idx, load, dict(score=score, token_mask=token_mask, **kept))
+
+    def route_backward(self, d_topk_weights, d_loss, saved):
+        """Gradient of the router's logits."""
+        logits, idx, load, how = saved
+        d_logits = torch.empty_like(logits, memory_format=torch.contiguous_format)
+        ep.ep_route_backward(logits, idx, d_logits, self.status, d_topk_weights=d_topk_weights, load=load, d_loss=d_loss,
+                             **how)
+        return d_logits
 
     def few_tokens(self, x, topk_idx, topk_weights, residual=None):
         """The whole layer in one call, at most EP_FEW_MAX_TOKENS tokens."""
@@ -141,6 +165,11 @@ def main():
     d_out = torch.randn(x.shape, device="cuda").to(torch.bfloat16)
     _, saved = layer.rows(x, idx, weights, train=True)
     timed("rows path, backward", lambda: layer.backward(d_out, saved))
+    logits = torch.randn((a.tokens, a.experts), device="cuda")
+    timed("router", lambda: layer.route(logits, a.topk))
+    timed("router and balance loss", lambda: layer.route(logits, a.topk, coeff=0.01))
+    _, _, _, kept = layer.route(logits, a.topk, coeff=0.01)
+    timed("router, backward", lambda: layer.route_backward(weights, torch.ones(1, device="cuda"), kept))
     status = int(layer.status.item())
     print("status:", ep.ep_status_string(status))
     return status
