@@ -508,6 +508,12 @@ def ep_moe_few_tokens(x, topk_idx, topk_weights, w_up, w_down, workspace, out, d
     return _check(code, "ep_moe_few_tokens")
 
 
+def _here(t, name):
+    """A call's kernels run on the current device: its tensors have to be there (pinned ones are -1)."""
+    at = t.get_device()
+    assert at < 0 or _current_device is None or at == _current_device(), "%s: on another than the current device" % name
+
+
 _ROW_TYPES = {torch.bfloat16: EP_BF16, torch.float16: EP_FP16, torch.float32: EP_FP32}
 
 
@@ -515,6 +521,7 @@ def _rows_of(t, shape, name):
     """Address, type and row stride of a matrix whose rows are contiguous (columns of a wider one will do)."""
     assert t.dtype in _ROW_TYPES and t.shape == shape and (t.is_cuda or t.is_pinned()), \
         "%s: a %s tensor of bf16, fp16 or fp32 on the GPU is wanted" % (name, tuple(shape))
+    _here(t, name)
     rows, cols = shape
     assert cols <= 1 or rows == 0 or t.stride(1) == 1, "%s: rows must be contiguous" % name
     stride = t.stride(0) if rows > 1 else cols
@@ -600,6 +607,7 @@ def ep_route_backward(logits, topk_idx, d_logits, d_status, d_topk_weights=None,
 def _weights4(w, sf, zero, depth, name):
     """Addresses of 4-bit weights, their scales and zero points, the scales' type and the group."""
     E, n_w, half = w.shape
+    _here(w, name)
     assert half * 2 == depth and sf.dtype in (torch.bfloat16, torch.float32), "%s: codes [E, n_w, k / 2] are wanted" % name
     groups = sf.shape[1]
     assert groups > 0 and depth % groups == 0, "%s: scales [E, k / group, n_w] are wanted" % name

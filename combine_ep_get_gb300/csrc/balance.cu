@@ -88,7 +88,8 @@ __global__ void __launch_bounds__(kThreads) balance_sums_kernel(const BalancePar
     for (int at = begin; at < end;) {
         int stop = end;
         if (p.seq_offset) {
-            while (q < p.S && p.seq_offset[q + 1] <= at) ++q;
+            if (q < p.S && p.seq_offset[q + 1] <= at) q = warp_sequence_of(p.seq_offset, p.S, at, lane);
+            while (q < p.S && p.seq_offset[q + 1] <= at) ++q;      // (offsets that do not ascend: go on all the same)
             if (q >= p.S) break;
             stop = min(end, p.seq_offset[q + 1]);
             if (q < 0) {        // before the first sequence
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) balance_sums_kernel(const BalancePar
             float all = 0.0f;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) all += s[j];
-            all = 1.0f / warp_sum(all);
+            all = reciprocal_approx(warp_sum(all));
             ++live;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) sum[j] = fmaf(s[j], all, sum[j]);
@@ -253,13 +254,13 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteBac
         // the token's slots, a lane each, with their experts' logits
         int e = -1;
         float v = -kInf;
-        const float g = now.g * p.scale;
-        if (now.named >= 0 && now.named < p.E) {
+        if (now.there && now.named >= 0 && now.named < p.E) {
             e = static_cast<int>(now.named);
             v = to_float(row[e]);
-        } else if (now.named != -1) {
+        } else if (now.there && now.named != -1) {
             atomicOr(p.status, EP_ERR_INVALID_INDEX);
         }
+        const float g = v == -kInf ? 0.0f : now.g * p.scale;      // (whatever stands in a slot of no expert)
         float s[kPer], rest[kPer], base;
         if (!now.there || !scores_of<kSoftmax>(now.l, s, rest, &base)) {
 #pragma unroll
@@ -284,7 +285,7 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteBac
             mean = fmaf(load[j], s[j], mean);
         }
         warp_sums(inverse, mean);
-        inverse = 1.0f / inverse;
+        inverse = reciprocal_approx(inverse);
         mean *= inverse;
         // Through the weights: the slots' lanes know their experts' whole derivative, and store it after the row's.
         float r = 0.0f;
@@ -294,7 +295,8 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteBac
                 const float u = v == -kInf ? 0.0f : kSoftmax ? exp2_approx((v - top) * kLog2E) : sigmoid_shifted(v, shift_of(top));
                 float sum = u, weighted = u * g;
                 warp_sums(sum, weighted);
-                r = u == 0.0f ? 0.0f : u / sum * (g - weighted / sum);
+                const float over = reciprocal_approx(sum);
+                r = u == 0.0f ? 0.0f : u * over * (g - weighted * over);
             } else if (v != -kInf) {
                 r = (kSoftmax ? exp2_approx(fmaf(v, kLog2E, -base)) * inverse : sigmoid_shifted(v, 0.0f)) * g;
             }

@@ -160,7 +160,8 @@ cudaError_t launch_expert_gemm_w4(const ExpertGemmW4Params& p, cudaStream_t stre
     a.status = p.status;
     // popular experts have a few times the mean
     const int64_t likely = p.E == 1 ? p.rows : std::min(p.rows, 2 * ((p.rows + p.E - 1) / p.E));
-    return launch(a, p.w, p.rows, likely, [&](int rows) { return p.rows / rows + p.E; }, stream);
+    const int64_t active = std::min<int64_t>(p.E, p.rows);
+    return launch(a, p.w, p.rows, likely, [&](int rows) { return active + (p.rows - active) / rows; }, stream);
 }
 
 cudaError_t launch_few_tokens_w4(const FewTokensW4Params& p, cudaStream_t stream) {
@@ -179,7 +180,7 @@ cudaError_t launch_few_tokens_w4(const FewTokensW4Params& p, cudaStream_t stream
     a.y = p.h;
     a.status = p.status;
     const int entries = p.T * p.K, active = std::min(p.E, entries);
-    const auto tiles = [&](int rows) { return static_cast<int64_t>(entries) / rows + active; };
+    const auto tiles = [&](int rows) { return static_cast<int64_t>(active) + (entries - active) / rows; };
     const int likely = std::min(p.T, 2 * ((entries + p.E - 1) / p.E));
     cudaError_t e = launch(a, p.up, entries, likely, tiles, stream);
     if (e != cudaSuccess) return e;

@@ -48,8 +48,8 @@ __device__ __forceinline__ float reach(float c) { return 5e-7f * fmaxf(1.0f, fab
 
 // What a warp's choice needs in shared memory: the candidates in the order of their indices, and the chosen ones' places.
 struct alignas(16) Lists {
-    uint32_t key[32];
-    int16_t expert[32];
+    uint32_t key[36];        // (the last four: zeros behind 32, and where what is no candidate goes)
+    int16_t expert[36];
     int16_t ranked[33];
 };
 
@@ -87,35 +87,32 @@ __device__ __forceinline__ int choose(uint32_t (&key)[kPer], int K, bool ranked,
 #pragma unroll
     for (int j = 1; j < kPer; ++j) best = max(best, key[j]);
     uint32_t least = 0;
-#pragma unroll 2
+#pragma unroll 4
     for (int k = 0; k < wanted; ++k) {
         least = __reduce_max_sync(0xffffffffu, best);
-        if (best == least) best = 0;
+        best = best == least ? 0 : best;
     }
     least = max(least, kClosed + 1);      // (fewer lanes with open ones than wanted: all that are open)
     int n = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         const unsigned there = __ballot_sync(0xffffffffu, key[j] >= least);
-        const int at = n + __popc(there & ((1u << lane) - 1));
-        if (key[j] >= least && at < 32) {
-            list->key[at] = key[j];
-            list->expert[at] = static_cast<int16_t>(j * 32 + lane);
-        }
+        const int at = key[j] >= least ? min(n + __popc(there & ((1u << lane) - 1)), 32) : 32;
+        list->key[at] = key[j];
+        list->expert[at] = static_cast<int16_t>(j * 32 + lane);
         n += __popc(there);
     }
     __syncwarp();
     int e = -1;
     if (n <= 32) {
-        // larger ones and equal ones before come first
+        // larger ones come first, and equal ones before
+        if (lane < 4) list->key[n + lane] = 0;
+        __syncwarp();
         const uint32_t own = lane < n ? list->key[lane] : 0;
-        int rank = 0;
+        int rank = __popc(__match_any_sync(0xffffffffu, own) & ((1u << lane) - 1));
         for (int i = 0; i < n; i += 4) {
             const uint4 k = *reinterpret_cast<const uint4*>(list->key + i);
-            rank += k.x > own - (i < lane);
-            rank += i + 1 < n && k.y > own - (i + 1 < lane);
-            rank += i + 2 < n && k.z > own - (i + 2 < lane);
-            rank += i + 3 < n && k.w > own - (i + 3 < lane);
+            rank += (k.x > own) + (k.y > own) + (k.z > own) + (k.w > own);
         }
         *place = lane < n ? rank : wanted;
         *mine = own;
@@ -342,7 +339,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
             if (there)
                 s = softmax ? exp2_approx((v - top) * kLog2E)
                             : shift_of(top) == 0.0f ? sigmoid_fast(v, &rest) : sigmoid_shifted(v, shift_of(top));
-            w = s * (p.scale / warp_sum(s));
+            w = s * (p.scale * reciprocal_approx(warp_sum(s)));
         } else {
             w = (softmax ? expf(v - largest) / total : sigmoid_shifted(v, 0.0f)) * p.scale;
         }

@@ -577,7 +577,8 @@ ep_status_t ep_balance_loss(const void* logits, int logits_dtype, int64_t row_st
  *               + *d_loss * sum over i of load[q,i] * d p_i / d l,  q = t's sequence.
  * Every row is written: zero for masked tokens and those with only logits of -inf;
  * tokens in no sequence have the first part alone.  An expert that two slots of a
- * token name gets both slots' parts.
+ * token name gets both slots' parts.  What stands in d_topk_weights where a slot
+ * names no expert, and in a masked token's row and slots, reaches nothing.
  *
  * logits .. scale  as in the forward calls; topk_idx as ep_route left it
  *                  (entries outside [-1, E) set EP_ERR_INVALID_INDEX and are skipped).
@@ -606,9 +607,12 @@ ep_status_t ep_route_backward(const void* logits, int logits_dtype, int64_t row_
 
 /*
  * Experts' matrix product with 4-bit weights, for the rows of a decode step
- * (few for each expert); one expert of one row is a matrix-vector product.
- * Every argument but the weights as ep_expert_gemm, bf16 rows, accumulated in
- * fp32; the weights' products are exact, scales are applied in fp32.
+ * (few for each expert: beyond 32 the weights are read again for every 32);
+ * one expert of one row is a matrix-vector product.  Every argument but the
+ * weights as ep_expert_gemm, bf16 rows, accumulated in fp32: products of codes
+ * and rows are exact, scales are applied in fp32 to each group's sum.  With
+ * zero points a row that is not finite may give NaN where the formula has an
+ * infinity.
  *
  * w             uint8 [E, n_w, k_dim / 2].
  * w_sf          scales [E, k_dim / group, n_w] of sf_dtype EP_BF16 or EP_FP32.

@@ -276,6 +276,42 @@ def test_backward_of_closed_repeated_and_bad_entries(score, normalize):
     check_backward(l, idx, score, d_weights=dw, normalize=normalize, want_status=B.EP_ERR_INVALID_INDEX)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_what_stands_in_masked_places_reaches_nothing(score, normalize):
+    """Garbage in masked tokens' rows and slots, and NaN where a slot names no expert."""
+    from gpu_path import B
+    T, E, K = 80, 40, 4
+    clean = make_logits(gen(4), T, E, "fp32").contiguous()
+    mask = torch.rand(T, generator=gen(3), device="cuda") > 0.3
+    l = clean.clone()
+    l[~mask] = float("nan")
+    idx, w = run_route(l, K, score, mask=mask, normalize=normalize)
+    assert torch.equal(idx, ref.route(clean, K, score, mask=mask)[0]) and bool((w[~mask] == 0).all())
+    idx[::3, 2] = -1
+    loss, load, counts = run_balance(l, idx, score, mask=mask)
+    want, want_load, want_counts = ref.balance(clean, idx, score, mask=mask)
+    assert torch.equal(counts.long(), want_counts) and abs(float(loss) - float(want)) < 1e-5 * float(want)
+    dw = torch.randn((T, K), generator=gen(5), device="cuda")
+    dw[idx < 0] = float("nan")
+    idx[~mask] = 99999
+    out = torch.empty_like(l)
+    st, d_loss = status(), torch.ones(1, device="cuda")
+    B.ep_route_backward(l, idx, out, st, d_topk_weights=dw, load=load, d_loss=d_loss, token_mask=mask, normalize=normalize,
+                        score=B.EP_SCORE_SOFTMAX if score == "softmax" else B.EP_SCORE_SIGMOID)
+    assert int(st.item()) == 0
+    want, bound = ref.backward(clean, torch.where(idx < E, idx, -1), score, torch.nan_to_num(dw), load, d_loss, None, mask,
+                               normalize)
+    assert bool(((out.double() - want).abs() <= ref.rounded(want, bound, out.dtype)).all())
+
+
+def test_offsets_with_many_empty_sequences():
+    l = make_logits(gen(6), 500, 32, "bf16")
+    idx = ref.route(l, 2, "softmax")[0].contiguous()
+    cuts = torch.cat([torch.zeros(3000), torch.full((3000,), 117.0), torch.full((2000,), 499.0), torch.full((1000,), 500.0)])
+    check_balance(l, idx, "softmax", offset=cuts.to(torch.int32).cuda())
+
+
 def test_backward_in_place():
     l = make_logits(gen(4), 100, 64, "bf16").contiguous()
     idx = ref.route(l, 5, "softmax")[0].contiguous()
