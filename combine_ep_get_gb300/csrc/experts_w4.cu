@@ -87,7 +87,9 @@ cudaError_t launch_variant(Which which, Args a, const Weights4& w, Tiles row_til
     if (!weight_maps(&a, w, half)) return cudaErrorInvalidValue;
     const int sf_bytes = 2 * (kSlotK / w.group * a.slots) * half * item;
     a.x_offset = V::kCodeBytes;
-    a.sf_offset = up(a.x_offset + a.slots * a.tile_rows * kRowPitch, 128);
+    // (FP4: behind the rows their units, and room for those of rows that a warp reads in vain)
+    const int units = w.format == EP_W4_FP ? (a.slots * a.tile_rows + 32) * 4 : 0;
+    a.sf_offset = up(a.x_offset + a.slots * a.tile_rows * kRowPitch + units, 128);
     a.zero_offset = a.sf_offset + sf_bytes;
     a.stage_bytes = up(a.zero_offset + (w.zero ? sf_bytes : 0), 512);
     const int fixed = 512 + kTeam * V::kTeams * V::kSums * 128 + static_cast<int>(sizeof(Shared)) +
@@ -132,8 +134,8 @@ cudaError_t launch(Args a, const Weights4& w, int64_t rows, int64_t likely, Tile
     a.whole = a.K % kSlotK == 0;
     // two shares at least: one share's 512 features would be more than a box may have
     const bool few = likely <= 8 && a.whole && a.K >= 2 * kSlotK;
-    a.tile_rows = rows < 8 ? static_cast<int>(rows) : likely <= 8 ? 8 : likely <= 16 ? 16 : 32;
-    const bool mid = !few && likely <= 16 && a.whole && a.K >= 2 * kSlotK;
+    a.tile_rows = rows < 8 ? static_cast<int>(rows) : likely <= 8 ? 8 : likely <= 32 ? 16 : 32;
+    const bool mid = !few && likely <= 32 && a.whole && a.K >= 2 * kSlotK;
     a.slots = few ? best_slots(a, row_tiles(a.tile_rows), likely) : mid ? 2 : 1;
     if (few) return launch_variant<Few>(kFew, a, w, row_tiles, stream);
     return mid ? launch_variant<Mid>(kMid, a, w, row_tiles, stream) : launch_variant<Wide>(kWide, a, w, row_tiles, stream);

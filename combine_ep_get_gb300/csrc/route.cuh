@@ -64,7 +64,7 @@ cudaError_t launch_route_backward(const RouteBackwardParams& p, cudaStream_t str
 // Workspace carve-up shared by the size query and the call.
 constexpr int kBalanceWarps = 8;
 constexpr int kBalanceChunk = 8;        // experts of one CTA of the second kernel
-constexpr int kBalanceTiles = 608;      // at most: four CTAs for each of 152 SMs
+constexpr int kBalanceTiles = 512;      // at most (304: 15.1 us for 32768 tokens, 608: 13.7, 512: 12.8)
 struct BalanceWorkspace {
     int tile_tokens, tiles;
     size_t off_part, off_tokens, off_loss, off_arrived, total;
@@ -73,7 +73,7 @@ inline BalanceWorkspace balance_workspace(int T, int E, int S) {
     const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     BalanceWorkspace b;
     const int each = (T + kBalanceTiles - 1) / kBalanceTiles;
-    b.tile_tokens = each < kBalanceWarps ? kBalanceWarps : (each + kBalanceWarps - 1) / kBalanceWarps * kBalanceWarps;
+    b.tile_tokens = each < 2 * kBalanceWarps ? 2 * kBalanceWarps : (each + kBalanceWarps - 1) / kBalanceWarps * kBalanceWarps;
     b.tiles = T > 0 ? (T + b.tile_tokens - 1) / b.tile_tokens : 0;
     const size_t pieces = static_cast<size_t>(b.tiles) + S, chunks = (static_cast<size_t>(E) + kBalanceChunk - 1) / kBalanceChunk;
     b.off_part = 0;
