@@ -106,8 +106,8 @@ cudaError_t launch_variant(Which which, Args a, const Weights4& w, Tiles row_til
 }
 
 // Shares for up to 8 rows of an expert: the least time of the CTAs' turns, a turn's tiles at what the memory gives
-// the SMs at work (an SM's warps take no more than 47 bytes a ns), 0.8 us a tile, and the tile's rows at 60.  One row, [7168, 7168]
-// by 2, 4, 8 shares: 31, 21, 17 us a call on its own; 8 experts of one row, 7168 -> 2 x 2048, SWIGLU, 37.5, 39.6, 43.6,
+// the SMs at work (an SM's warps take no more than 47 bytes a ns), 0.8 us a tile, and the tile's rows at 60 bytes a ns.
+// One row, [7168, 7168] by 2, 4, 8 shares: 31, 21, 17 us a call on its own; 8 experts of one row, 7168 -> 2 x 2048, SWIGLU, 37.5, 39.6, 43.6,
 // and 2048 -> 7168 27.3, 23.2, 31; 64 experts of four rows 175, 193, 240 and 115, 124, 160.
 int best_slots(const Args& a, int64_t row_tiles, int64_t likely) {
     const double sms = device_info().num_sms;
@@ -132,7 +132,9 @@ int best_slots(const Args& a, int64_t row_tiles, int64_t likely) {
 template <typename Tiles>
 cudaError_t launch(Args a, const Weights4& w, int64_t rows, int64_t likely, Tiles row_tiles, cudaStream_t stream) {
     a.whole = a.K % kSlotK == 0;
-    // two shares at least: one share's 512 features would be more than a box may have
+    // Two shares at least: one share's 512 features would be more than a box may have.  Up to 32 likely rows by tiles
+    // of 16: 64 experts of 12 and 16 rows, 7168 -> 2 x 2048, 242 us, by tiles of 32 289 and 293, of 8 318 and 324 (of 8
+    // rows 197, by tiles of 8 185, but 2048 -> 7168 152 and 156).
     const bool few = likely <= 8 && a.whole && a.K >= 2 * kSlotK;
     a.tile_rows = rows < 8 ? static_cast<int>(rows) : likely <= 8 ? 8 : likely <= 32 ? 16 : 32;
     const bool mid = !few && likely <= 32 && a.whole && a.K >= 2 * kSlotK;

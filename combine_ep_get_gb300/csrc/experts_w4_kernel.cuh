@@ -4,7 +4,11 @@
 //
 // A call reads half a byte a weight and has few rows to multiply it by, so the
 // weights' bytes bound it if what is done to each weight is little: about 11
-// of them a cycle go through each quarter of an SM at the memory's rate.
+// of them a cycle go through each quarter of an SM at the memory's rate.  256
+// experts of 4 rows, 7168 -> 2 x 2048, int with groups of 128: 600 us for 3.83
+// GB, 6.4 TB/s.  Groups of 32 have four times the scales to apply to the sums,
+// and FP4 rows to convert as well: 2048 -> 7168, 565 us for 2.1 GB, bound by
+// the instructions' issue.
 // Codes become bf16 values in registers, exactly, and meet the rows in the
 // warp's own MMA (m16n8k16), whose operands are registers: tcgen05 would want
 // the values written to shared or tensor memory first, twice the bytes that
@@ -21,13 +25,13 @@
 // A word of eight int codes of one feature gives the pairs (k, k + 4), k = 0 .. 3:
 // the operand's order of k is any that both sides share, so x is paired that
 // way too (four byte permutations a 16-byte read).  32 k's are 16 bytes of a
-// feature, a word for each of four lanes; the 128-byte swizzle lets 8
+// feature, a word for each of four lanes; the 64-byte swizzle lets 8
 // features' reads meet all banks.
 //
 // A CTA walks tiles (expert, rows, features).  Warp 0 asks for codes, scales and
-// zero points by tensor maps, warps 0 and 1 copy the rows, 16 bytes a lane
-// (bulk copies of a row's 256 bytes: 64 experts of 8 rows 271 -> 480 us),
-// into a ring of stages.  Teams of eight warps multiply, a stage a team in
+// zero points by tensor maps, warps 0 and 1 copy the rows, 16 bytes a lane (bulk
+// copies of a row's 256 bytes: 64 experts of 8 rows 271 -> 480 us), for FP4
+// through registers, where they become fp16, into a ring of stages.  Teams of eight warps multiply, a stage a team in
 // turn: a stage is `slots` shares of 128 k's, a share 8 / slots pieces of
 // features (two halves: gate and up for SWIGLU).  Many shares: tiles of few
 // features, which fill the SMs evenly, but rows are read for each tile
@@ -570,9 +574,9 @@ __global__ void __launch_bounds__(V::kThreads, 1) experts_w4_kernel(const __grid
                     if (EP_IN(source, p.mode == kFewUp ? p.T : few ? p.T * p.topk : p.rows)) from[i] = p.x + source * p.K;
                 }
             }
-            // FP4: rows come through registers, those of the next stage asked for as the last leave them (64
-            // experts of 8 rows, 7168 -> 2 x 2048: 293 us; asked for before the stage's wait 298, turned where asynchronous
-            // copies had left them 312).
+            // FP4: rows come through registers, those of the next stage asked for as the last leave them (64 experts of 8
+            // rows, 7168 -> 2 x 2048: 288 us, two stages ahead 289; asked for just before the stage's wait 298, turned
+            // where asynchronous copies had left them 312).
             uint4 asked[kForm == EP_W4_FP ? kMost : 1];
             const auto ask = [&](int i, int step, int pass) {
                 const int k = step * kSlotK * p.slots + (chunk0 + pass * (kCopyWarps * 32)) * 8;

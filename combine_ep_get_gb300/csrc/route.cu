@@ -8,9 +8,10 @@
 //
 // The choice.  The K-th largest of the lanes' largest values bounds the K-th
 // largest value from below, and few values reach it: they go to a list, whose
-// members find their places by comparing themselves with one another.  About
-// 200 instructions a token of 256 experts bound the kernel for many tokens; K
-// rounds of a warp's maximum over what is left took 400.
+// members find their places by comparing themselves with one another.  The
+// instructions bound the kernel for many tokens, about 400 for one of 256
+// experts, 8 chosen (32768 bf16 tokens 14.9 us, 2.5 TB/s); K rounds of a warp's
+// maximum over what is left took 29.6 us.
 #include <algorithm>
 #include <type_traits>
 

@@ -607,12 +607,14 @@ ep_status_t ep_route_backward(const void* logits, int logits_dtype, int64_t row_
 
 /*
  * Experts' matrix product with 4-bit weights, for the rows of a decode step
- * (few for each expert: beyond 32 the weights are read again for every 32);
- * one expert of one row is a matrix-vector product.  Every argument but the
- * weights as ep_expert_gemm, bf16 rows, accumulated in fp32: products of codes
- * and rows are exact, scales are applied in fp32 to each group's sum.  With
- * zero points a row that is not finite may give NaN where the formula has an
- * infinity.
+ * (few for each expert: the weights are read again for every 8, 16 or 32 of
+ * them, as num_rows / E has it); one expert of one row is a matrix-vector
+ * product.  Every argument but the weights as ep_expert_gemm, bf16 rows,
+ * accumulated in fp32: products of codes and rows are exact, scales are applied
+ * in fp32 to each group's sum.  EP_W4_FP: a row's value that is less than 2^-31
+ * of the largest of its 128 k's (k / 128 alike) is rounded, by 2^-39 of that one
+ * at most.  With zero points a row that is not finite may give NaN where the
+ * formula has an infinity.
  *
  * w             uint8 [E, n_w, k_dim / 2].
  * w_sf          scales [E, k_dim / group, n_w] of sf_dtype EP_BF16 or EP_FP32.

@@ -140,6 +140,53 @@ def test_product_extremes():
         assert bool((y[:4, 1] == 0).all()) and bool((y[1] == 0).all())
 
 
+@pytest.mark.parametrize("rows", [1, 7, 16, 70])
+@pytest.mark.parametrize("K,group", [(512, 32), (1024, 128), (416, 32)])
+def test_fp4_rows_of_every_size(rows, K, group):
+    """Rows whose 128 k's lie many powers of two apart, and apart from one another; subnormal ones, infinities, NaN.
+
+    A row's values may be rounded to 2^-39 of the largest of their 128 k's (fp16 holds bf16's values to 2^-31 of it,
+    and has a step of 2^-38 of it below), which counts where the largest meets a weight of zero."""
+    from gpu_path import B
+    g = gen(rows + K)
+    N = 72
+    x = normal(g, rows, K).float()
+    blocks_ = -(-K // 128)
+    far = torch.randint(-55, 56, (rows, blocks_), generator=g, device="cuda").repeat_interleave(128, 1)[:, :K]
+    near = -torch.randint(0, 45, (rows, K), generator=g, device="cuda")
+    near[rows // 2] = 0
+    x = torch.ldexp(x, far + near)
+    if rows > 3:
+        x[0] = 0.0
+        x[1] = torch.ldexp(normal(g, K).float(), torch.tensor(-132, device="cuda"))
+    x = x.to(BF)
+    w, sf, _ = ref.make(g, 1, N, K, group, "fp4")
+    off, cnt, _ = blocks([rows])
+
+    def call():
+        y = torch.empty((rows, N), dtype=BF, device="cuda")
+        B.ep_expert_gemm_w4(x, w, sf, off, cnt, y, status(), w_format=B.EP_W4_FP)
+        return y
+
+    y = call()
+    v, big = ref.values(w[0], sf[0], None, "fp4")
+    xd = x.double()
+    largest = torch.stack([b.abs().amax(1) for b in xd.split(128, 1)], 1).repeat_interleave(128, 1)[:, :K]
+    want, bound = ref.product_rows(xd, v, big, None, "none", None, None)
+    check(y, want, bound + 2.0 ** -39 * (largest @ v.abs().T) + 2.0 ** -133)
+    if rows > 3:
+        x[2, 5], x[2, K - 1], x[3, 130] = float("inf"), 3e38, float("nan")
+        # (a group's sum is fp32 before its scale: 3e38 times a code of 1.5 or more is beyond fp32's 3.4e38, and an
+        # infinity there, which against the other one gives NaN)
+        codes = ref.values(w[0], torch.ones_like(sf[0]), None, "fp4")[0].unflatten(1, (-1, group))
+        sums = torch.einsum("rgk,fgk->rfg", x.double().unflatten(1, (-1, group)), codes).float().double()
+        got, want = call(), (sums * sf[0].double().T).sum(-1)
+        keep = [r for r in range(rows) if r not in (2, 3)]
+        assert torch.equal(got[keep], y[keep]) and bool(got[3].isnan().all())
+        assert torch.equal(got[2].isnan(), want[2].isnan())
+        assert torch.equal(got[2].nan_to_num(0.0, 1.0, -1.0), want[2].nan_to_num(0.0, 1.0, -1.0).to(BF))
+
+
 def test_product_skips_rows_beyond_and_overlapping_blocks():
     from gpu_path import B
     g = gen(3)
