@@ -326,6 +326,17 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
                 close |= __any_sync(0xffffffffu, near) || p.K == 32;     // (the 33rd has no lane)
             }
             if (close) {
+                // one logit and one bias everywhere (a router before its first step) is a tie in any number of bits
+                const float first_l = __shfl_sync(0xffffffffu, l[0], 0), first_b = p.bias ? p.bias[0] : 0.0f;
+                bool differs = false;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    const int expert = j * 32 + lane;
+                    if (expert < p.E) differs |= l[j] != first_l || (p.bias && p.bias[expert] != first_b);
+                }
+                close = __any_sync(0xffffffffu, differs);
+            }
+            if (close) {
                 e = choose_by_doubles(p, l, c, grouped, largest, mem, lane);
                 place = e >= 0 ? lane : p.K;
             }
