@@ -44,8 +44,23 @@ __device__ __forceinline__ float value_of(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-// How far c in fp32 may lie from c: the score is good to a few units of the last place, the sum to half a one.
-__device__ __forceinline__ float reach(float c) { return 5e-7f * fmaxf(1.0f, fabsf(c)); }
+// How far a score s in fp32 may lie from the formula's, x its logit less the row's largest.  With u = 2^-24, in s: softmax
+// |x| u by x's rounding and 4 u by expf's (2 units of the last place), for s itself and for the total, where the mean of |x|
+// by the scores is at most ln E < 8; the total's additions, at most kPer - 1 in a lane and 5 between lanes; the division's u.
+// Sigmoid, e = expf(-|l|): (4 (1 - s) + 2) u where s >= 1/2, (4 + 4 s + 2) u below: at most 8 s u, and at most 4 u.  (Down
+// at the subnormal numbers a few of their steps; beyond |x| = 128 a score is 0.)
+constexpr float kHalfStep = 5.9604645e-8f;     // u
+template <int kPer>
+__device__ __forceinline__ float score_reach(bool softmax, float s, float x) {
+    return kHalfStep * (softmax ? s * (kPer + 24.0f + fminf(-x, 128.0f)) : fminf(9.0f * s, 4.5f)) + 1.2e-38f;
+}
+// The most of any score of a row: s (a - x) falls with -x, from the largest score on, 1 over the total.
+template <int kPer>
+__device__ __forceinline__ float row_reach(bool softmax, float total) {
+    return score_reach<kPer>(softmax, softmax ? 1.0f / total : 1.0f, 0.0f);
+}
+// How far c = s + bias may: its own rounding besides.
+__device__ __forceinline__ float sum_reach(float of_score, float c) { return of_score + kHalfStep * fabsf(c); }
 
 // What a warp's choice needs in shared memory: the candidates in the order of their indices, and the chosen ones' places.
 struct alignas(16) Lists {
@@ -144,8 +159,9 @@ __device__ __forceinline__ int choose(uint32_t (&key)[kPer], int K, bool ranked,
 }
 
 // Closes the experts of all but the topk_groups best groups.  c is in shared memory by expert.
+// With `close`, which says whether c's rounding may have made another choice: of_score, how far a score may be off.
 template <typename V>
-__device__ __forceinline__ void keep_groups(const RouteParams& p, V* c, int lane, bool* close) {
+__device__ __forceinline__ void keep_groups(const RouteParams& p, V* c, int lane, float of_score, bool* close) {
     const int G = p.num_groups, size = p.E / G;
     // lanes of a group: a power of two
     int share = 1;
@@ -190,7 +206,8 @@ __device__ __forceinline__ void keep_groups(const RouteParams& p, V* c, int lane
         const auto next = key_max(key);
         const int other = next == 0 ? -1 : __ffs(__ballot_sync(0xffffffffu, key == next)) - 1;
         const float b = __shfl_sync(0xffffffffu, static_cast<float>(score), other & 31), a = static_cast<float>(worst);
-        if (other >= 0 && !(a - b > 2.0f * (reach(a) + reach(b)))) *close = true;
+        const float reach = 4.0f * of_score + 2.0f * kHalfStep * (fabsf(a) + fabsf(b));
+        if (other >= 0 && !(a - b > reach)) *close = true;
     }
     if (g < G && !kept)
         for (int i = sub; i < size; i += share) c[g * size + i] = -kInf;
@@ -226,7 +243,7 @@ __device__ __noinline__ int choose_by_doubles(const RouteParams& p, const float 
         for (int j = 0; j < kPer; ++j)
             if (j * 32 + lane < p.E) mem[j * 32 + lane] = c64[j];
         __syncwarp();
-        keep_groups(p, mem, lane, static_cast<bool*>(nullptr));
+        keep_groups(p, mem, lane, 0.0f, static_cast<bool*>(nullptr));
 #pragma unroll
         for (int j = 0; j < kPer; ++j)
             if (j * 32 + lane < p.E) c64[j] = mem[j * 32 + lane];
@@ -303,7 +320,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
                 for (int j = 0; j < kPer; ++j)
                     if (j * 32 + lane < p.E) m[j * 32 + lane] = c[j];
                 __syncwarp();
-                keep_groups(p, m, lane, &close);
+                keep_groups(p, m, lane, row_reach<kPer>(softmax, total), &close);
 #pragma unroll
                 for (int j = 0; j < kPer; ++j)
                     if (j * 32 + lane < p.E) c[j] = m[j * 32 + lane];
@@ -319,9 +336,11 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
                 const int a = lane < p.K ? list->ranked[lane] : -1, b = lane < p.K ? list->ranked[lane + 1] : -1;
                 if (a >= 0 && b >= 0) {
                     const float la = to_float(row[a]), lb = to_float(row[b]), ba = p.bias[a], bb = p.bias[b];
-                    const float ca = (softmax ? expf(la - largest) / total : sigmoid_shifted(la, 0.0f)) + ba;
-                    const float cb = (softmax ? expf(lb - largest) / total : sigmoid_shifted(lb, 0.0f)) + bb;
-                    near = ca - cb <= reach(ca) + reach(cb) && !(la == lb && ba == bb);
+                    const float sa = softmax ? expf(la - largest) / total : sigmoid_shifted(la, 0.0f), ca = sa + ba;
+                    const float sb = softmax ? expf(lb - largest) / total : sigmoid_shifted(lb, 0.0f), cb = sb + bb;
+                    const float ra = sum_reach(score_reach<kPer>(softmax, sa, la - largest), ca);
+                    const float rb = sum_reach(score_reach<kPer>(softmax, sb, lb - largest), cb);
+                    near = ca - cb <= ra + rb && !(la == lb && ba == bb);
                 }
                 close |= __any_sync(0xffffffffu, near) || p.K == 32;     // (the 33rd has no lane)
             }
