@@ -202,12 +202,16 @@ __device__ __forceinline__ void keep_groups(const RouteParams& p, V* c, int lane
     }
     const bool kept = g < G && (keep >> g & 1);
     if (close && sizeof(V) == 4) {
-        // the last one kept against the best one dropped
+        // The last one kept against the best one dropped, by the most that any group's sum may be off: its two members'
+        // scores, their c's and its own rounding.  (The members may be far larger than their sum, and another kept group's
+        // sum, larger than the last one's, may be off by more.)
+        const float one = static_cast<float>(first), two = second != static_cast<V>(-kInf) ? static_cast<float>(second) : 0.0f;
+        const float off = 2.0f * of_score + kHalfStep * (fabsf(one) + fabsf(two) + fabsf(static_cast<float>(score)));
+        const float reach = open && one != kInf ? off : 0.0f;      // (+inf is itself in any number of bits)
         const auto next = key_max(key);
         const int other = next == 0 ? -1 : __ffs(__ballot_sync(0xffffffffu, key == next)) - 1;
         const float b = __shfl_sync(0xffffffffu, static_cast<float>(score), other & 31), a = static_cast<float>(worst);
-        const float reach = 4.0f * of_score + 2.0f * kHalfStep * (fabsf(a) + fabsf(b));
-        if (other >= 0 && !(a - b > reach)) *close = true;
+        if (!(a - b > 2.0f * warp_max(reach)) && other >= 0) *close = true;
     }
     if (g < G && !kept)
         for (int i = sub; i < size; i += share) c[g * size + i] = -kInf;

@@ -25,3 +25,22 @@ def test_one_expert_far_above_many(E, groups):
         bias = torch.zeros(E, device="cuda")
         bias[other] = float(s[0] - s[other]) + step * 7e-8
         check_route(l, 2, "softmax", bias=bias, groups=groups, topk_groups=1)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("topk_groups", [1, 2, 3])
+def test_groups_whose_large_biases_cancel(score, topk_groups):
+    """Two experts of a group have biases of 1000 and -1000: c rounds by 3e-5, the group's sum is about the others'.  Their
+    sums lie within 5e-5 of one another."""
+    T, E, G = 600, 12, 4
+    g = gen(topk_groups)
+    l = torch.randn((T, E), generator=g, device="cuda") * 0.01
+    l[:, 2::3] -= 6.0                                  # (the third of a group is far below)
+    l[:, ::3] += (torch.rand((T, G), generator=g, device="cuda") - 0.5) * (2e-4 if score == "sigmoid" else 6e-4)
+    # one value for both of a group's two best: their sum is what moves
+    l[:, 1::3] = l[:, ::3].mean(1, keepdim=True)
+    l[:, ::3] = l[:, 1::3] + (l[:, ::3] - l[:, 1::3]) * 0.01
+    bias = torch.zeros(E, device="cuda")
+    bias[3], bias[4], bias[5] = 1000.0, -1000.0, -2000.0
+    check_route(l, 2, score, bias=bias, groups=G, topk_groups=topk_groups)
+    check_route(l, 2, score, bias=bias + 0.125, groups=G, topk_groups=topk_groups)
