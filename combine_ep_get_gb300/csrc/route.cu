@@ -336,15 +336,38 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
             e = choose(key, p.K, true, list, lane, &place, &mine);
             if (p.bias) {
                 // neighbours of the first K + 1 that fp32 may have turned round: lane k the k-th and the next
-                bool near = false;
+                bool near = false, tie = false;
+                float la = 0.0f, ba = 0.0f, ca = 0.0f, ra = 0.0f;
+                const auto sum = [&](float logit, float b, float* reach) {
+                    const float s = softmax ? expf(logit - largest) / total : sigmoid_shifted(logit, 0.0f);
+                    *reach = sum_reach(score_reach<kPer>(softmax, s, logit - largest), s + b);
+                    return s + b;
+                };
                 const int a = lane < p.K ? list->ranked[lane] : -1, b = lane < p.K ? list->ranked[lane + 1] : -1;
                 if (a >= 0 && b >= 0) {
-                    const float la = to_float(row[a]), lb = to_float(row[b]), ba = p.bias[a], bb = p.bias[b];
-                    const float sa = softmax ? expf(la - largest) / total : sigmoid_shifted(la, 0.0f), ca = sa + ba;
-                    const float sb = softmax ? expf(lb - largest) / total : sigmoid_shifted(lb, 0.0f), cb = sb + bb;
-                    const float ra = sum_reach(score_reach<kPer>(softmax, sa, la - largest), ca);
-                    const float rb = sum_reach(score_reach<kPer>(softmax, sb, lb - largest), cb);
-                    near = ca - cb <= ra + rb && !(la == lb && ba == bb);
+                    const float lb = to_float(row[b]), bb = p.bias[b];
+                    la = to_float(row[a]);
+                    ba = p.bias[a];
+                    float rb;
+                    ca = sum(la, ba, &ra);
+                    const float cb = sum(lb, bb, &rb);
+                    const bool same = la == lb && ba == bb;
+                    near = ca - cb <= ra + rb && !same;
+                    tie = same && lane == p.K - 1;
+                }
+                if (__any_sync(0xffffffffu, tie)) {
+                    // The last one chosen and the next are alike, whatever the number of bits; one behind them may come before both.
+                    la = __shfl_sync(0xffffffffu, la, p.K - 1);
+                    ba = __shfl_sync(0xffffffffu, ba, p.K - 1);
+                    ca = __shfl_sync(0xffffffffu, ca, p.K - 1);
+                    ra = __shfl_sync(0xffffffffu, ra, p.K - 1);
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) {
+                        if (c[j] == -kInf || c[j] > ca || (l[j] == la && p.bias[j * 32 + lane] == ba)) continue;
+                        float r;
+                        const float other = sum(l[j], p.bias[j * 32 + lane], &r);
+                        near |= ca - other <= ra + r;
+                    }
                 }
                 close |= __any_sync(0xffffffffu, near) || p.K == 32;     // (the 33rd has no lane)
             }

@@ -44,3 +44,33 @@ def test_groups_whose_large_biases_cancel(score, topk_groups):
     bias[3], bias[4], bias[5] = 1000.0, -1000.0, -2000.0
     check_route(l, 2, score, bias=bias, groups=G, topk_groups=topk_groups)
     check_route(l, 2, score, bias=bias + 0.125, groups=G, topk_groups=topk_groups)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_a_tie_at_the_last_slot_and_a_third_value_next_to_it(score, groups):
+    """The last slot's expert and the next are of one logit and one bias; a third one's c, of another logit and bias, lies
+    within fp32's last places of theirs."""
+    T, E, K = 4000, 40, 2
+    g = gen(groups)
+    l = torch.full((T, E), -9.0, device="cuda")
+    l[:, 7] = 3.0
+    tied = torch.rand(T, generator=g, device="cuda") * 0.5 + 1.0
+    l[:, 11] = l[:, 12] = tied
+    bias = torch.zeros(E, device="cuda")
+    bias[33] = 0.0625
+    # the third one's logit: c = that of the tied ones, within a few last places
+    off = (torch.rand(T, generator=g, device="cuda", dtype=torch.float64) - 0.5) * 3e-7
+    if score == "sigmoid":
+        want = torch.sigmoid(tied.double()) - 0.0625 + off
+        l[:, 33] = torch.logit(want).float()
+    else:
+        # e^x / (rest + e^x) = s of the tied ones - bias, which x changes too: to its fixed point
+        rest = torch.exp(l.double()).sum(1) - torch.exp(l[:, 33].double())
+        x = torch.exp(tied.double()) * 0.5
+        for _ in range(200):
+            x = (torch.exp(tied.double()) / (rest + x) - 0.0625 + off) * (rest + x)
+        l[:, 33] = torch.log(x).float()
+    check_route(l, K, score, bias=bias, groups=groups, topk_groups=groups)
+    if groups > 1:
+        check_route(l, K, score, bias=bias, groups=groups, topk_groups=groups - 1)
