@@ -20,11 +20,15 @@ namespace {
 
 constexpr int kThreads = kBalanceWarps * 32;
 
+// exp(l - base) by the hardware's 2^x.
+__device__ __forceinline__ float exp_below(float l, float base) { return exp2_approx((l - base) * kLog2E); }
+
 __device__ __forceinline__ int clamped(int v, int n) { return v < 0 ? 0 : v > n ? n : v; }
 
 // Scores of a row before they are divided by their sum, for a sigmoid 1 - score too; false for a row whose logits are
-// all -inf.  *base: a softmax's q is 2^(log2(e) l - base), a sigmoid's is shifted by it.  Exponentials and reciprocals
-// are the hardware's (sigmoid_fast): exact ones took half of the kernels' instructions.
+// all -inf.  *base: a softmax's q is exp(l - base) (the difference first: a product of either, rounded, is off by more
+// than the exponent's range where logits are large), a sigmoid's is shifted by it.  Exponentials and reciprocals are
+// the hardware's (sigmoid_fast): exact ones took half of the kernels' instructions.
 template <bool kSoftmax, int kPer>
 __device__ __forceinline__ bool scores_of(const float (&l)[kPer], float (&q)[kPer], float (&rest)[kPer], float* base) {
     float largest = l[0], any = 0.0f;      // any: NaN if one is
@@ -36,10 +40,10 @@ __device__ __forceinline__ bool scores_of(const float (&l)[kPer], float (&q)[kPe
         for (int j = 0; j < kPer; ++j) any += l[j];
         if (!__any_sync(0xffffffffu, any != any)) return false;
     }
-    *base = kSoftmax ? largest * kLog2E : shift_of(largest);
+    *base = kSoftmax ? largest : shift_of(largest);
     if (kSoftmax) {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) q[j] = exp2_approx(fmaf(l[j], kLog2E, -*base));
+        for (int j = 0; j < kPer; ++j) q[j] = exp_below(l[j], *base);
     } else if (*base == 0.0f) {
 #pragma unroll
         for (int j = 0; j < kPer; ++j) q[j] = sigmoid_fast(l[j], &rest[j]);
@@ -292,13 +296,13 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteBac
         if (p.d_topk_weights) {
             if (p.normalize) {
                 const float top = warp_max(v);
-                const float u = v == -kInf ? 0.0f : kSoftmax ? exp2_approx((v - top) * kLog2E) : sigmoid_shifted(v, shift_of(top));
+                const float u = v == -kInf ? 0.0f : kSoftmax ? exp_below(v, top) : sigmoid_shifted(v, shift_of(top));
                 float sum = u, weighted = u * g;
                 warp_sums(sum, weighted);
                 const float over = reciprocal_approx(sum);
                 r = u == 0.0f ? 0.0f : u * over * (g - weighted * over);
             } else if (v != -kInf) {
-                r = (kSoftmax ? exp2_approx(fmaf(v, kLog2E, -base)) * inverse : sigmoid_shifted(v, 0.0f)) * g;
+                r = (kSoftmax ? exp_below(v, base) * inverse : sigmoid_shifted(v, 0.0f)) * g;
             }
             if (kSoftmax && !p.normalize) mean += warp_sum(r);      // every expert loses its share of the chosen ones' sum
             if (!kSoftmax && e >= 0) r *= sigmoid_shifted(-v, 0.0f);
@@ -326,7 +330,7 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteBac
                 if (v == -kInf) {
                     own = 0.0f;
                 } else if (kSoftmax) {
-                    own = exp2_approx(fmaf(v, kLog2E, -base)) * inverse * (a - mean);
+                    own = exp_below(v, base) * inverse * (a - mean);
                 } else if (in_loss) {
                     float rest_e;
                     const float s_e = base == 0.0f ? sigmoid_fast(v, &rest_e) : sigmoid_shifted(v, base);
