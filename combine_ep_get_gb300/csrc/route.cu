@@ -423,7 +423,7 @@ cudaError_t launch_route(const RouteParams& p, cudaStream_t stream) {
         constexpr int kPer = decltype(per)::value;
         constexpr bool kFull = decltype(full)::value;
         const auto kernel = p.bias || grouped ? route_kernel<L, kPer, kFull, true> : route_kernel<L, kPer, kFull, false>;
-        if (smem > 48 * 1024) {
+        if (smem + kWarps * sizeof(Lists) > 48 * 1024) {     // what a kernel may have unasked, its own arrays among it
             const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
             if (e != cudaSuccess) return e;
         }
