@@ -387,36 +387,62 @@ def ep_combine_hierarchical(y, topk_idx, topk_weights, num_experts, num_ranks, r
     return _check(code, "ep_combine_hierarchical")
 
 
-def _take(t, dtype, shape, name):
+def _here(t, name):
+    """Device of a call's first tensor, for the others' checks: a call's kernels run on the current device, and its
+    tensors have to be there (pinned ones are on none, -1)."""
+    at = t.get_device()
+    assert at < 0 or at == _now(), "%s: on another than the current device" % name
+    return at
+
+
+def _now():
+    return _current_device() if _current_device is not None else torch.cuda.current_device()
+
+
+def _reached(t, here):
+    """Whether kernels reach a tensor: on the GPU or pinned; with `here`, from _here, on that GPU (the current one where
+    the first tensor is pinned)."""
+    if here is None:
+        return t.is_cuda or t.is_pinned()
+    at = t.get_device()
+    return at == (here if here >= 0 else _now()) if at >= 0 else t.is_cuda or t.is_pinned()
+
+
+def _take(t, dtype, shape, name, here=None):
     """Address of a contiguous tensor of this type and shape (the library
     takes no strides) on the GPU (or pinned, which kernels reach too); None
     stays None."""
     if t is None:
         return None
-    assert t.dtype is dtype and t.shape == shape and t.is_contiguous() and (t.is_cuda or t.is_pinned()), \
-        "%s: a contiguous %s tensor of shape %s on the GPU is wanted" % (name, dtype, tuple(shape))
+    assert t.dtype is dtype and t.shape == shape and t.is_contiguous() and (
+        (t.is_cuda if here is None else t.get_device() == here >= 0) or _reached(t, here)), \
+        "%s: a contiguous %s tensor of shape %s on the current GPU is wanted" % (name, dtype, tuple(shape))
     return t.data_ptr()
 
 
-def _take_any(t, name):
+def _take_any(t, name, here=None):
     """Address of a contiguous tensor of any shape on the GPU."""
-    assert t.is_contiguous() and (t.is_cuda or t.is_pinned()), "%s: a contiguous tensor on the GPU is wanted" % name
+    assert t.is_contiguous() and (
+        (t.is_cuda if here is None else t.get_device() == here >= 0) or _reached(t, here)), \
+        "%s: a contiguous tensor on the current GPU is wanted" % name
     return t.data_ptr()
 
 
-def _word(d_status):
+def _word(d_status, here=None):
     """Address of the status word; None stays None (the library answers invalid_arg)."""
     if d_status is None:
         return None
-    assert d_status.dtype is torch.int32 and (d_status.is_cuda or d_status.is_pinned()), \
-        "d_status: an int32 word on the GPU is wanted"
+    assert d_status.dtype is torch.int32 and (
+        (d_status.is_cuda if here is None else d_status.get_device() == here >= 0) or _reached(d_status, here)), \
+        "d_status: an int32 word on the current GPU is wanted"
     return d_status.data_ptr()
 
 
-def _blocks(expert_offset, num_tokens_per_expert, E):
+def _blocks(expert_offset, num_tokens_per_expert, E, here=None):
     """Addresses of the experts' blocks (offsets may go on past the last expert's)."""
     assert expert_offset.dtype is torch.int32 and expert_offset.numel() >= E
-    return _take_any(expert_offset, "expert_offset"), _take(num_tokens_per_expert, torch.int32, (E,), "num_tokens_per_expert")
+    return (_take_any(expert_offset, "expert_offset", here),
+            _take(num_tokens_per_expert, torch.int32, (E,), "num_tokens_per_expert", here))
 
 
 def ep_expert_gemm(x, w, expert_offset, num_tokens_per_expert, y, d_status, bias=None, activation=EP_ACT_NONE,
@@ -508,40 +534,34 @@ def ep_moe_few_tokens(x, topk_idx, topk_weights, w_up, w_down, workspace, out, d
     return _check(code, "ep_moe_few_tokens")
 
 
-def _here(t, name):
-    """A call's kernels run on the current device: its tensors have to be there (pinned ones are -1)."""
-    at = t.get_device()
-    assert at < 0 or _current_device is None or at == _current_device(), "%s: on another than the current device" % name
-
-
 _ROW_TYPES = {torch.bfloat16: EP_BF16, torch.float16: EP_FP16, torch.float32: EP_FP32}
 
 
 def _rows_of(t, shape, name):
-    """Address, type and row stride of a matrix whose rows are contiguous (columns of a wider one will do)."""
+    """Address, type, row stride and device of a matrix whose rows are contiguous (columns of a wider one will do)."""
     assert t.dtype in _ROW_TYPES and t.shape == shape and (t.is_cuda or t.is_pinned()), \
         "%s: a %s tensor of bf16, fp16 or fp32 on the GPU is wanted" % (name, tuple(shape))
-    _here(t, name)
+    here = _here(t, name)
     rows, cols = shape
     assert cols <= 1 or rows == 0 or t.stride(1) == 1, "%s: rows must be contiguous" % name
     stride = t.stride(0) if rows > 1 else cols
     assert stride >= cols, "%s: rows must not overlap" % name
-    return t.data_ptr(), _ROW_TYPES[t.dtype], stride
+    return t.data_ptr(), _ROW_TYPES[t.dtype], stride, here
 
 
-def _mask(token_mask, T):
+def _mask(token_mask, T, here):
     """Address of a token mask: bool or uint8, one byte a token."""
     if token_mask is None:
         return None
     assert token_mask.dtype in (torch.bool, torch.uint8), "token_mask: bool or uint8 is wanted"
-    return _take(token_mask, token_mask.dtype, (T,), "token_mask")
+    return _take(token_mask, token_mask.dtype, (T,), "token_mask", here)
 
 
-def _sequences(seq_offset):
+def _sequences(seq_offset, here):
     """Address of sequences' offsets and how many sequences there are; None: one of all tokens."""
     if seq_offset is None:
         return None, 1
-    return _take(seq_offset, torch.int32, (seq_offset.numel(),), "seq_offset"), seq_offset.numel() - 1
+    return _take(seq_offset, torch.int32, (seq_offset.numel(),), "seq_offset", here), seq_offset.numel() - 1
 
 
 def ep_route(logits, topk_idx, topk_weights, d_status, score=EP_SCORE_SOFTMAX, bias=None, token_mask=None, num_groups=1,
@@ -552,11 +572,13 @@ def ep_route(logits, topk_idx, topk_weights, d_status, score=EP_SCORE_SOFTMAX, b
     ep_get_layout, the dispatch and the few-token layers take."""
     T, E = logits.shape
     K = topk_idx.shape[1]
-    address, kind, stride = _rows_of(logits, (T, E), "logits")
-    code = _lib.ep_route(address, kind, stride, _take(bias, torch.float32, (E,), "bias"), _mask(token_mask, T), T, E, K,
-                         score, num_groups, num_groups if topk_groups is None else topk_groups, 1 if normalize else 0,
-                         scale, _take(topk_idx, torch.int64, (T, K), "topk_idx"),
-                         _take(topk_weights, torch.float32, (T, K), "topk_weights"), _word(d_status), _stream(stream))
+    address, kind, stride, here = _rows_of(logits, (T, E), "logits")
+    code = _lib.ep_route(address, kind, stride, _take(bias, torch.float32, (E,), "bias", here),
+                         _mask(token_mask, T, here), T, E, K, score, num_groups,
+                         num_groups if topk_groups is None else topk_groups, 1 if normalize else 0, scale,
+                         _take(topk_idx, torch.int64, (T, K), "topk_idx", here),
+                         _take(topk_weights, torch.float32, (T, K), "topk_weights", here), _word(d_status, here),
+                         _stream(stream))
     return _check(code, "ep_route")
 
 
@@ -573,13 +595,14 @@ def ep_balance_loss(logits, topk_idx, workspace, loss, load, d_status, score=EP_
     f32 = torch.float32
     T, E = logits.shape
     K = topk_idx.shape[1]
-    address, kind, stride = _rows_of(logits, (T, E), "logits")
-    offsets, S = _sequences(seq_offset)
-    code = _lib.ep_balance_loss(address, kind, stride, _take(topk_idx, torch.int64, (T, K), "topk_idx"),
-                                _mask(token_mask, T), offsets, T, E, K, S, score, coeff, _take(loss, f32, (1,), "loss"),
-                                _take(load, f32, (S, E), "load"),
-                                _take(num_tokens_per_expert, torch.int32, (S, E), "num_tokens_per_expert"),
-                                _take_any(workspace, "workspace"), workspace.nbytes, _word(d_status), _stream(stream))
+    address, kind, stride, here = _rows_of(logits, (T, E), "logits")
+    offsets, S = _sequences(seq_offset, here)
+    code = _lib.ep_balance_loss(address, kind, stride, _take(topk_idx, torch.int64, (T, K), "topk_idx", here),
+                                _mask(token_mask, T, here), offsets, T, E, K, S, score, coeff,
+                                _take(loss, f32, (1,), "loss", here), _take(load, f32, (S, E), "load", here),
+                                _take(num_tokens_per_expert, torch.int32, (S, E), "num_tokens_per_expert", here),
+                                _take_any(workspace, "workspace", here), workspace.nbytes,
+                                _word(d_status, here), _stream(stream))
     return _check(code, "ep_balance_loss")
 
 
@@ -592,28 +615,27 @@ def ep_route_backward(logits, topk_idx, d_logits, d_status, d_topk_weights=None,
     f32 = torch.float32
     T, E = logits.shape
     K = topk_idx.shape[1]
-    address, kind, stride = _rows_of(logits, (T, E), "logits")
-    out, out_kind, out_stride = _rows_of(d_logits, (T, E), "d_logits")
+    address, kind, stride, here = _rows_of(logits, (T, E), "logits")
+    out, out_kind, out_stride, _ = _rows_of(d_logits, (T, E), "d_logits")
     assert out_kind == kind, "d_logits: the logits' type is wanted"
-    offsets, S = _sequences(seq_offset)
-    code = _lib.ep_route_backward(address, kind, stride, _take(topk_idx, torch.int64, (T, K), "topk_idx"),
-                                  _mask(token_mask, T), _take(d_topk_weights, f32, (T, K), "d_topk_weights"),
-                                  _take(load, f32, (S, E), "load"), _take(d_loss, f32, (1,), "d_loss"), offsets, T, E, K,
-                                  S, score, 1 if normalize else 0, scale, out, out_stride, _word(d_status),
-                                  _stream(stream))
+    offsets, S = _sequences(seq_offset, here)
+    code = _lib.ep_route_backward(address, kind, stride, _take(topk_idx, torch.int64, (T, K), "topk_idx", here),
+                                  _mask(token_mask, T, here), _take(d_topk_weights, f32, (T, K), "d_topk_weights", here),
+                                  _take(load, f32, (S, E), "load", here), _take(d_loss, f32, (1,), "d_loss", here), offsets,
+                                  T, E, K, S, score, 1 if normalize else 0, scale, out, out_stride,
+                                  _word(d_status, here), _stream(stream))
     return _check(code, "ep_route_backward")
 
 
-def _weights4(w, sf, zero, depth, name):
+def _weights4(w, sf, zero, depth, name, here):
     """Addresses of 4-bit weights, their scales and zero points, the scales' type and the group."""
     E, n_w, half = w.shape
-    _here(w, name)
     assert half * 2 == depth and sf.dtype in (torch.bfloat16, torch.float32), "%s: codes [E, n_w, k / 2] are wanted" % name
     groups = sf.shape[1]
     assert groups > 0 and depth % groups == 0, "%s: scales [E, k / group, n_w] are wanted" % name
     shape = (E, groups, n_w)
-    return (_take(w, torch.uint8, (E, n_w, half), name), _take(sf, sf.dtype, shape, name + "'s scales"),
-            _take(zero, sf.dtype, shape, name + "'s zero points"), EP_FP32 if sf.dtype is torch.float32 else EP_BF16,
+    return (_take(w, torch.uint8, (E, n_w, half), name, here), _take(sf, sf.dtype, shape, name + "'s scales", here),
+            _take(zero, sf.dtype, shape, name + "'s zero points", here), EP_FP32 if sf.dtype is torch.float32 else EP_BF16,
             depth // groups)
 
 
@@ -629,13 +651,15 @@ def ep_expert_gemm_w4(x, w, w_sf, expert_offset, num_tokens_per_expert, y, d_sta
     gated = activation == EP_ACT_SWIGLU
     assert not gated or n_w % 2 == 0
     n_dim = n_w // 2 if gated else n_w
-    codes, sf, zero, sf_kind, group = _weights4(w, w_sf, w_zero, k_dim, "w")
-    first, count = _blocks(expert_offset, num_tokens_per_expert, E)
-    code = _lib.ep_expert_gemm_w4(_take(x, bf16, (rows, k_dim), "x"), codes, sf, zero, sf_kind, w_format, group,
-                                  _take(bias, f32, (E, n_w), "bias"), activation,
-                                  _take(row_weight, f32, (rows,), "row_weight"),
-                                  _take(residual, bf16, (rows, n_dim), "residual"), rows, k_dim, n_dim, E, first, count,
-                                  _take(y, bf16, (rows, n_dim), "y"), _word(d_status), _stream(stream))
+    here = _here(x, "x")
+    codes, sf, zero, sf_kind, group = _weights4(w, w_sf, w_zero, k_dim, "w", here)
+    first, count = _blocks(expert_offset, num_tokens_per_expert, E, here)
+    code = _lib.ep_expert_gemm_w4(_take(x, bf16, (rows, k_dim), "x", here), codes, sf, zero, sf_kind, w_format, group,
+                                  _take(bias, f32, (E, n_w), "bias", here), activation,
+                                  _take(row_weight, f32, (rows,), "row_weight", here),
+                                  _take(residual, bf16, (rows, n_dim), "residual", here), rows, k_dim, n_dim, E, first,
+                                  count, _take(y, bf16, (rows, n_dim), "y", here), _word(d_status, here),
+                                  _stream(stream))
     return _check(code, "ep_expert_gemm_w4")
 
 
@@ -656,13 +680,14 @@ def ep_moe_few_tokens_w4(x, topk_idx, topk_weights, w_up, up_sf, w_down, down_sf
     inner = w_down.shape[2] * 2
     assert n_w == (2 * inner if activation == EP_ACT_SWIGLU else inner) and w_down.shape[:2] == (E, H)
     assert up_sf.dtype is down_sf.dtype, "both scales are of one type"
-    up, sf_up, zero_up, sf_kind, up_group = _weights4(w_up, up_sf, up_zero, H, "w_up")
-    down, sf_down, zero_down, _, down_group = _weights4(w_down, down_sf, down_zero, inner, "w_down")
+    here = _here(x, "x")
+    up, sf_up, zero_up, sf_kind, up_group = _weights4(w_up, up_sf, up_zero, H, "w_up", here)
+    down, sf_down, zero_down, _, down_group = _weights4(w_down, down_sf, down_zero, inner, "w_down", here)
     code = _lib.ep_moe_few_tokens_w4(
-        _take(x, bf16, (T, H), "x"), _take(topk_idx, torch.int64, (T, K), "topk_idx"),
-        _take(topk_weights, f32, (T, K), "topk_weights"), up, sf_up, zero_up, up_group,
-        _take(bias_up, f32, (E, n_w), "bias_up"), activation, down, sf_down, zero_down, down_group,
-        _take(bias_down, f32, (E, H), "bias_down"), sf_kind, w_format, _take(residual, bf16, (T, H), "residual"), T, H,
-        inner, K, E, _take_any(workspace, "workspace"), workspace.nbytes, _take(out, bf16, (T, H), "out"),
-        _word(d_status), _stream(stream))
+        _take(x, bf16, (T, H), "x", here), _take(topk_idx, torch.int64, (T, K), "topk_idx", here),
+        _take(topk_weights, f32, (T, K), "topk_weights", here), up, sf_up, zero_up, up_group,
+        _take(bias_up, f32, (E, n_w), "bias_up", here), activation, down, sf_down, zero_down, down_group,
+        _take(bias_down, f32, (E, H), "bias_down", here), sf_kind, w_format,
+        _take(residual, bf16, (T, H), "residual", here), T, H, inner, K, E, _take_any(workspace, "workspace", here),
+        workspace.nbytes, _take(out, bf16, (T, H), "out", here), _word(d_status, here), _stream(stream))
     return _check(code, "ep_moe_few_tokens_w4")
