@@ -556,7 +556,8 @@ __global__ void __launch_bounds__(V::kThreads, 1) experts_w4_kernel(const __grid
             if (warp == 0 && blockIdx.x < tiles) {
                 const Tile r = tile_at(p, t, blockIdx.x, feature_tiles, tile_features, lane);
                 early = min(p.stages, steps);
-                for (int i = 0; i < early; ++i) load_weights(r, i, 0, i);
+                for (int i = 0; i < early; ++i)
+                    if (!drop || i > 0) load_weights(r, i, 0, i);
             }
             pdl_wait();
         }
@@ -612,7 +613,7 @@ __global__ void __launch_bounds__(V::kThreads, 1) experts_w4_kernel(const __grid
                 if (issued >= early) {
                     ok = wait_quietly(&s->empty[stage], (use & 1) ^ 1);
                     if (!ok) break;
-                    if (warp == 0) load_weights(r, stage, use, step);
+                    if (warp == 0 && !drop) load_weights(r, stage, use, step);
                 }
                 if (kForm == EP_W4_FP) {
                     if (!drop) to_stage(step, stage, use);
@@ -639,13 +640,13 @@ __global__ void __launch_bounds__(V::kThreads, 1) experts_w4_kernel(const __grid
             }
         }
         if (!ok) atomicOr(p.status, EP_ERR_TIMEOUT);
-        // no copy may still be in flight when the CTA ends
+        // no copy may still be in flight when the CTA ends (after a wait that ran out, each stage's all the same)
         copies_commit();
         copies_wait<0>();
         if (warp == 0) {
             issued = max(issued, early);
             for (int i = max(0, issued - p.stages); i < issued; ++i)
-                if (!wait_quietly(&s->full[i % p.stages][i / p.stages & 1], (i / p.stages >> 1) & 1)) break;
+                wait_quietly(&s->full[i % p.stages][i / p.stages & 1], (i / p.stages >> 1) & 1);
         }
     } else if (warp >= kFirstTeamWarp) {
         const int w = (warp - kFirstTeamWarp) % kTeam, team = (warp - kFirstTeamWarp) / kTeam;
