@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1) experts_fp8_kernel(const __gri
         if (!ok) atomicOr(p.status, EP_ERR_TIMEOUT);
         // no copy may still be in flight when the CTA ends
         for (int i = max(0, issued - kFp8Stages); i < issued; ++i)
-            if (!warp_wait(&s->full[i % kFp8Stages], (i / kFp8Stages) & 1)) break;
+            warp_wait(&s->full[i % kFp8Stages], (i / kFp8Stages) & 1);
     } else if (warp == 1) {
         Ring<kFp8Stages> ring;
         Ring<kAccs> accs;

@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_mma_kernel(const __grid_c
         // no copy may still be in flight when the CTA ends (a pair's end: rank 0 sees both CTAs')
         if (rank == 0)
             for (int i = max(0, issued - S::kStages); i < issued; ++i)
-                if (!warp_wait(&s->full[i % S::kStages], (i / S::kStages) & 1)) break;
+                warp_wait(&s->full[i % S::kStages], (i / S::kStages) & 1);
     } else if (warp == 1 && rank == 0) {
         Ring<S::kStages> ring;
         Ring<2> accs;
@@ -750,8 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1) weight_grad_kernel(const __grid_c
         for (int st = 0; st < S::kStages && st < issued; ++st) {
             const bool tail = (last_tail >> st) & 1;
             if (!tail && rank != 0) continue;
-            if (!warp_wait(tail ? &s->tail_full[st] : &s->full[st], (((tail ? tail_bits : full_bits) >> st) & 1) ^ 1))
-                break;
+            warp_wait(tail ? &s->tail_full[st] : &s->full[st], (((tail ? tail_bits : full_bits) >> st) & 1) ^ 1);
         }
     } else if (warp == 1 && rank == 0) {
         const uint32_t idesc = instr_desc(false, true, true, kM * kCtas, kGradK);
