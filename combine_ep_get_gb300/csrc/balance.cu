@@ -210,13 +210,13 @@ __global__ void __launch_bounds__(kLossThreads) balance_loss_kernel(const Balanc
         const float tokens = static_cast<float>(n);
         const float load = n > 0 ? p.coeff * p.E / (static_cast<float>(p.S) * p.K) * (count / tokens) / tokens : 0.0f;
         const bool mine = lane < kBalanceChunk && e < p.E;
-        if (mine) {
+        if (mine && EP_IN(q, p.S)) {
             p.load[static_cast<int64_t>(q) * p.E + e] = load;
             if (p.counts) p.counts[static_cast<int64_t>(q) * p.E + e] = count;
         }
         const float loss = warp_sum(mine && n > 0 ? load * sum : 0.0f);
         if (lane == 0) {
-            p.part_loss[blockIdx.x] = loss;
+            if (EP_IN(blockIdx.x, static_cast<int64_t>(p.S) * chunks)) p.part_loss[blockIdx.x] = loss;
             __threadfence();
             last = atomicAdd(p.arrived, 1u) == gridDim.x - 1;
         }
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteBac
         float v = -kInf;
         if (now.there && now.named >= 0 && now.named < p.E) {
             e = static_cast<int>(now.named);
-            v = to_float(row[e]);
+            if (EP_IN(t, p.T)) v = to_float(row[e]);
         } else if (now.there && now.named != -1) {
             atomicOr(p.status, EP_ERR_INVALID_INDEX);
         }
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteBac
         }
         // The loss's mean derivative, over the scores' sum.
         const int q = p.load ? warp_sequence_of(p.seq_offset, p.S, t, lane) : -1;
-        const bool in_loss = q >= 0 && q < p.S;
+        const bool in_loss = q >= 0 && q < p.S && EP_IN(q, p.S);
         if (q != load_of) {
             load_of = q;
 #pragma unroll
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteBac
                 r = sum;
             }
             __syncwarp();     // after the row's stores
-            if (e >= 0 && (same & ((1u << lane) - 1)) == 0) {
+            if (e >= 0 && (same & ((1u << lane) - 1)) == 0 && EP_IN(t, p.T) && EP_IN(e, p.E)) {
                 const float a = in_loss ? p.load[static_cast<int64_t>(q) * p.E + e] * d_loss : 0.0f;
                 float own = 0.0f;
                 if (v == -kInf) {

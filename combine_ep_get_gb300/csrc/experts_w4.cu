@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(128) few_sum_kernel(const FewTokensW4Params p)
     for (int k = 0; k < EP_FEW_MAX_TOPK; ++k) {
         const int entry = t * p.K + k;
         const int64_t e = k < p.K ? p.topk_idx[entry] : -1;
-        const bool there = e >= 0 && e < p.E;
+        const bool there = e >= 0 && e < p.E && EP_IN(entry, static_cast<int64_t>(p.T) * p.K);
         weight[k] = there ? p.topk_weights[entry] : 0.0f;
         part[k] = there ? *reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(entry) * p.H + f)
                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);

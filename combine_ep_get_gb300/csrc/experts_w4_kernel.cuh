@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(V::kThreads, 1) experts_w4_kernel(const __grid
             for (int chunk = warp - kFirstFinishWarp; chunk < chunks; chunk += kFinishWarps) {
                 const int h = chunk & 1, f = (chunk >> 1) * 32 + lane, feature = r.f0 + h * half + f;
                 const bool inside = feature < p.N;
-                const float bias = p.bias && inside ? p.bias[static_cast<int64_t>(r.e) * p.Nw + feature] : 0.0f;
+                const float bias = p.bias && inside && EP_IN(r.e, p.E) ? p.bias[static_cast<int64_t>(r.e) * p.Nw + feature] : 0.0f;
                 const float* const base = sums + (f / (16 * kM) * V::kSums + (h * kM + f / 16 % kM) * 4 + (f >> 3 & 1) * 2) * 32 +
                                           (f & 7) * 4;
                 const int turn = f >> 3 & 3;
@@ -774,7 +774,7 @@ __global__ void __launch_bounds__(V::kThreads, 1) experts_w4_kernel(const __grid
                 const int h = kGate ? 0 : chunk & 1, f = (kGate ? chunk : chunk >> 1) * 32 + lane;     // in the half
                 const int feature = r.f0 + h * half + f;
                 if (feature >= p.N) continue;
-                const float* const bias = p.bias ? p.bias + static_cast<int64_t>(r.e) * p.Nw + feature : nullptr;
+                const float* const bias = p.bias && EP_IN(r.e, p.E) ? p.bias + static_cast<int64_t>(r.e) * p.Nw + feature : nullptr;
                 const float b0 = bias ? bias[0] : 0.0f, b1 = kGate && bias ? bias[p.N] : 0.0f;
                 const float* const base = sums + (f / (16 * kM) * V::kSums + (h * kM + f / 16 % kM) * 4 + (f >> 3 & 1) * 2) * 32 +
                                           (f & 7) * 4;

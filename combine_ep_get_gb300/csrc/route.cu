@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
                     return s + b;
                 };
                 const int a = lane < p.K ? list->ranked[lane] : -1, b = lane < p.K ? list->ranked[lane + 1] : -1;
-                if (a >= 0 && b >= 0) {
+                if (a >= 0 && b >= 0 && EP_IN(a, p.E) && EP_IN(b, p.E)) {
                     const float lb = to_float(row[b]), bb = p.bias[b];
                     la = to_float(row[a]);
                     ba = p.bias[a];
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
             }
         }
         // weights, by the lane that has a slot
-        const bool there = e >= 0 && place < p.K;
+        const bool there = e >= 0 && place < p.K && EP_IN(e, p.E) && EP_IN(place, p.K);
         const float v = !there ? -kInf : kByScore ? to_float(row[e]) : value_of(mine);
         float w;
         if (p.normalize) {
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
             p.topk_idx[out + place] = e;
             p.topk_weights[out + place] = w;
         }
-        if (lane >= filled && lane < p.K) {
+        if (lane >= filled && lane < p.K && EP_IN(out + lane, static_cast<int64_t>(p.T) * p.K)) {
             p.topk_idx[out + lane] = -1;
             p.topk_weights[out + lane] = 0.0f;
         }

@@ -758,9 +758,10 @@ const char* ep_status_string(int32_t status);
 int ep_abi_version(void);
 
 /* 1 when this copy of the library is the bounds-checked build (every kernel
- * compiled with EP_GET_CHECKED=1: each global load and store is checked
- * against the extent its arguments declare, a failing access is skipped and
- * sets EP_ERR_OUT_OF_BOUNDS in *d_status), 0 for the product build.  The
+ * compiled with EP_GET_CHECKED=1: global loads and stores are checked against
+ * the extent their arguments declare, but for those whose index is a loop's own
+ * counter over just that extent; a failing access is skipped and sets
+ * EP_ERR_OUT_OF_BOUNDS in *d_status), 0 for the product build.  The
  * checked build computes the same results on valid input, more slowly. */
 int ep_bounds_checked(void);
 
