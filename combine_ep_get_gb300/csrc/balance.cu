@@ -352,10 +352,11 @@ cudaError_t launch_balance_loss(const BalanceParams& p, cudaStream_t stream) {
         constexpr bool kFull = decltype(full)::value;
         const auto kernel = p.score == EP_SCORE_SOFTMAX ? balance_sums_kernel<L, kPer, kFull, true>
                                                         : balance_sums_kernel<L, kPer, kFull, false>;
-        const size_t smem = static_cast<size_t>(kBalanceWarps + 1) * p.E * 4 + 16;
-        if (smem > 48 * 1024) {
+        const auto smem_of = [](int experts) { return (kBalanceWarps + 1) * experts * 4 + 16; };
+        const size_t smem = smem_of(p.E);
+        if (smem > 48 * 1024) {      // (the most that any call asks for: another thread's does not take it back)
             const cudaError_t err =
-                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(EP_MAX_EXPERTS));
             if (err != cudaSuccess) return err;
         }
         return launch_pdl(kernel, dim3(p.tiles > 0 ? p.tiles : 1), dim3(kThreads), smem, stream, p);

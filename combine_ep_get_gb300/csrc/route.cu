@@ -423,8 +423,11 @@ cudaError_t launch_route(const RouteParams& p, cudaStream_t stream) {
         constexpr int kPer = decltype(per)::value;
         constexpr bool kFull = decltype(full)::value;
         const auto kernel = p.bias || grouped ? route_kernel<L, kPer, kFull, true> : route_kernel<L, kPer, kFull, false>;
-        if (smem + kWarps * sizeof(Lists) > 48 * 1024) {     // what a kernel may have unasked, its own arrays among it
-            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        // Beyond what a kernel may have unasked, its own arrays among it: the most that any call asks for, so that a call
+        // of another thread does not take it back before the launch.
+        if (smem + kWarps * sizeof(Lists) > 48 * 1024) {
+            const cudaError_t e =
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarps * EP_MAX_EXPERTS * 8);
             if (e != cudaSuccess) return e;
         }
         // (many tokens: warps that go on to another token have asked for its row)
