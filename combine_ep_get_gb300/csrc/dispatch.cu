@@ -1253,9 +1253,11 @@ cudaError_t launch_dispatch_bulk_t(DispatchParams p, int max_ctas, cudaStream_t 
     static thread_local int blocks_per_sm = 1;
     static thread_local size_t configured_smem = 0;
     if (configured_device != di.device || configured_smem != smem) {
+        // the most that any call asks for: one limit for all threads, which another's shorter rows do not lower
+        static_assert(EP_DISPATCH_PIECE_MAX % 16 == 0, "a piece's slot is no longer than the longest piece");
         cudaError_t e = cudaFuncSetAttribute(dispatch_bf16_kernel<kStages, kStoreDepth>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
+                                             128 + kStages * EP_DISPATCH_PIECE_MAX);
         if (e != cudaSuccess) return e;
         int nb = 0;
         e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, dispatch_bf16_kernel<kStages, kStoreDepth>,
