@@ -265,6 +265,7 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const RouteBac
             atomicOr(p.status, EP_ERR_INVALID_INDEX);
         }
         const float g = v == -kInf ? 0.0f : now.g * p.scale;      // (whatever stands in a slot of no expert)
+        __syncwarp();      // d_logits may be the logits: the slots' are read before another lane writes the row
         float s[kPer], rest[kPer], base;
         if (!now.there || !scores_of<kSoftmax>(now.l, s, rest, &base)) {
 #pragma unroll
