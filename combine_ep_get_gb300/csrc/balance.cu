@@ -6,9 +6,14 @@
 // its part of the loss is sum_i load_i P_i, load_i = coeff E c_i / (S K n^2), which
 // is also the loss's derivative by each of its tokens' p_i.  Two kernels: the
 // first adds scores and counts over tiles of tokens, cut where a sequence
-// ends; the second adds the pieces of each sequence in their order, 32 experts
-// a CTA, and its last CTA the sequences' parts.  Every sum runs in an order
-// that only the sizes decide.
+// ends; the second adds the pieces of each sequence, eight experts a CTA and a
+// fixed share of the pieces a thread, and its last CTA the sequences' parts.
+// Every sum runs in an order that only the sizes decide.
+//
+// 32768 tokens of 256 experts, 8 chosen, inputs from memory: the loss 13.4 us for bf16 logits (1.5
+// TB/s), the gradient through both 20 us for fp32 ones (3.5 TB/s): instructions
+// of exponentials and sums bound both, and the loads and stores of 2 or 4
+// bytes a lane.
 #include <algorithm>
 #include <type_traits>
 

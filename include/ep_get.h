@@ -516,7 +516,8 @@ ep_status_t ep_moe_few_tokens(const void* x, const int64_t* topk_idx, const floa
  *             with `normalize`, times `scale`.
  * Equal values go to the lower index.  The choice is that of c in 64 bits: where
  * fp32 cannot tell neighbours apart, the token is chosen again in 64 (without a
- * bias the choice goes by the logits, which order as the scores do).  An
+ * bias the choice goes by the logits, which order as the scores do; with one and
+ * K = EP_MAX_TOPK every token is chosen in 64 bits, which takes ten times as long).  An
  * expert whose logit or c is -inf is closed: never chosen, and where too few
  * are open the last slots hold -1 with weight 0.  NaN counts as the largest
  * value, and shows in the weights.
