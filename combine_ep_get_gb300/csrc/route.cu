@@ -7,7 +7,7 @@
 // below it) and do not come from the same logit and bias, the token is chosen
 // once more by c in 64 bits (14 us; one of some 1900 tokens of 256 experts, sigmoid,
 // bias in steps of 0.001, 4 of 8 groups; with a bias and 32 slots, whose 33rd candidate has
-// no lane, every token).  32768 of those tokens: 77.7 us.
+// no lane, every token).  32768 of those tokens: 79.9 us.
 //
 // The choice.  The K-th largest of the lanes' largest values bounds the K-th
 // largest value from below, and few values reach it: they go to a list, whose
@@ -338,8 +338,10 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
             for (int j = 0; j < kPer; ++j) key[j] = c[j] == -kInf ? 0u : key_of(p.bias ? c[j] : l[j]);
             e = choose(key, p.K, true, list, lane, &place, &mine);
             if (p.bias) {
-                // neighbours of the first K + 1 that fp32 may have turned round: lane k the k-th and the next
-                bool near = false, tie = false;
+                // Neighbours of the first K + 1 that fp32 may have turned round: lane k the k-th and the next.  (Two values
+                // that it has turned round lie within both their reaches, so of the neighbours between them a pair does, or
+                // all are alike.)
+                bool near = false, beyond = false;
                 float la = 0.0f, ba = 0.0f, ca = 0.0f, ra = 0.0f;
                 const auto sum = [&](float logit, float b, float* reach) {
                     const float s = softmax ? expf(logit - largest) / total : sigmoid_shifted(logit, 0.0f);
@@ -356,10 +358,11 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
                     const float cb = sum(lb, bb, &rb);
                     const bool same = la == lb && ba == bb;
                     near = ca - cb <= ra + rb && !same;
-                    tie = same && lane == p.K - 1;
+                    // Behind the last slot's, one that is not listed may come before it: where the next one is of the same logit
+                    // and bias, or fp32 knows the other's score less well than the next one's.
+                    beyond = lane == p.K - 1 && (same || ca - cb <= ra + sum_reach(row_reach<kPer>(softmax, total), ca));
                 }
-                if (__any_sync(0xffffffffu, tie)) {
-                    // The last one chosen and the next are alike, whatever the number of bits; one behind them may come before both.
+                if (__any_sync(0xffffffffu, beyond && !near)) {
                     la = __shfl_sync(0xffffffffu, la, p.K - 1);
                     ba = __shfl_sync(0xffffffffu, ba, p.K - 1);
                     ca = __shfl_sync(0xffffffffu, ca, p.K - 1);

@@ -74,3 +74,21 @@ def test_a_tie_at_the_last_slot_and_a_third_value_next_to_it(score, groups):
     check_route(l, K, score, bias=bias, groups=groups, topk_groups=groups)
     if groups > 1:
         check_route(l, K, score, bias=bias, groups=groups, topk_groups=groups - 1)
+
+
+@pytest.mark.parametrize("E", [256, 512, 1024, 2048])
+def test_a_value_behind_the_next_one_that_fp32_knows_less_well(E):
+    """One logit of 0 among others near -16.6, each of which adds a whole last place to the largest one's exponential: its
+    score comes out too small.  Two experts of small scores, known far better, lie next to one another at the last slot;
+    the first one's c, by a bias, lies behind both in fp32 and sweeps through them in 64 bits."""
+    l = torch.full((2, E), -16.6, device="cuda")
+    l[:, 0] = 0.0
+    l[1, 1:] += (torch.rand(E - 1, generator=gen(E), device="cuda") - 0.5) * 0.05
+    s = torch.softmax(l[:1].double(), 1)[0]
+    for gap in (1.2e-7, 2.4e-7, 5e-7, 1e-6):
+        for step in range(-50, 51):
+            bias = torch.zeros(E, device="cuda")
+            bias[E // 3], bias[E // 2] = 0.5, 0.5 - gap
+            bias[0] = float(0.5 - s[0]) + step * 6e-8
+            for K in (1, 2):
+                check_route(l, K, "softmax", bias=bias)
